@@ -339,3 +339,10 @@ def gemm_mxfp6_nt(a, b, scale_a, scale_b, fmt="e2m3", out=None, stream=None):
     _call(lib().gemm_mxfp6_nt, dev, stream, FP6_FORMATS[fmt], M, N, K, a.data_ptr(), b.data_ptr(),
           scale_a.data_ptr(), scale_b.data_ptr(), c.data_ptr())
     return c
+
+
+# The feed-forward layers' operators (libtgemm_ffn.so; ffn.set_tile is their
+# tile override).
+from . import ffn  # noqa: E402
+from .ffn import (epilogue_backward, expert_combine, expert_combine_backward, expert_gather,  # noqa: E402,F401
+                  gemm_epilogue, gemm_grouped, gemm_grouped_tn, route_plan, route_topk, route_topk_backward)

@@ -1,4 +1,4 @@
-"""Build libtgemm.so in-tree with hipcc for gfx950.
+"""Build libtgemm.so and libtgemm_ffn.so in-tree with hipcc for gfx950.
 
     python -m dense_tiled_gemm_bf16_amd.build
 """
@@ -7,6 +7,8 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -15,10 +17,15 @@ LIB = os.path.join(PKG, "libtgemm.so")
 SOURCES = [os.path.join(CSRC, "tgemm_kernels.hip"), os.path.join(CSRC, "tgemm_quant.hip"),
            os.path.join(CSRC, "tgemm_clock.hip"), os.path.join(CSRC, "tgemm_scratch.hip"),
            os.path.join(CSRC, "tgemm_abi.cpp")]
+FFN_LIB = os.path.join(PKG, "libtgemm_ffn.so")
+FFN_SOURCES = [os.path.join(CSRC, "tgemm_ffn_gemm_bf16.hip"), os.path.join(CSRC, "tgemm_ffn_gemm_f16.hip"),
+               os.path.join(CSRC, "tgemm_ffn_gemm.hip"), os.path.join(CSRC, "tgemm_ffn_rows.hip"),
+               os.path.join(CSRC, "tgemm_ffn_rowops.hip"), os.path.join(CSRC, "tgemm_ffn_route.hip"),
+               os.path.join(CSRC, "tgemm_ffn_abi.cpp")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [
-    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
+    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
     "-Wall", "-Wno-unused-command-line-argument", "-fvisibility=hidden",
     # (Device helpers are unused in the host pass, which compiles no kernel bodies.)
     "-Wno-unneeded-internal-declaration",
@@ -28,8 +35,7 @@ FLAGS = [
 ]
 
 
-def build(verbose: bool = False) -> str:
-    cmd = [HIPCC, *FLAGS, "-o", LIB + ".tmp", *SOURCES]
+def _run(cmd, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -40,7 +46,20 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError(f"hipcc failed ({res.returncode}):\n{err}")
     if verbose and err.strip():
         print(err, file=sys.stderr)
-    os.replace(LIB + ".tmp", LIB)
+
+
+def build(verbose: bool = False) -> str:
+    """Compiles every source (several at a time) and links the two libraries."""
+    with tempfile.TemporaryDirectory(prefix="tgemm_build_") as tmp:
+        def obj(src):
+            return os.path.join(tmp, os.path.basename(src) + ".o")
+
+        with ThreadPoolExecutor(max_workers=4) as pool:
+            list(pool.map(lambda src: _run([HIPCC, *FLAGS, "-c", src, "-o", obj(src)], verbose),
+                          SOURCES[:1] + FFN_SOURCES + SOURCES[1:]))
+        for lib, sources in ((LIB, SOURCES), (FFN_LIB, FFN_SOURCES)):
+            _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", lib + ".tmp", *map(obj, sources)], verbose)
+            os.replace(lib + ".tmp", lib)
     return LIB
 
 

@@ -1,0 +1,80 @@
+// Which kernel a feed-forward product takes (host code).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "tgemm_ffn_internal.hpp"
+#include "tgemm_shapes.hpp"
+
+namespace tgemm {
+namespace ffn {
+
+bool tile_supported(const Gemm &g, int tm, int tn) {
+  if (tm == 16 && tn == 16) return !g.trans_a && g.trans_b;
+  if (tm == 256 && tn == 192) return g.trans_b && !is_gated(g.act) && g.groups == 0;
+  return (tm == 256 && tn == 256) || (tm == 128 && tn == 128) || (tm == 64 && tn == 64);
+}
+
+namespace {
+
+// Most rows of a weight that take the kernel for few rows.
+constexpr int64_t kFewRows = 64;
+
+// The shape with the least estimated time (as pick_shape), over groups of
+// about the same size, whose last row tile is half full on average.
+template <size_t NS>
+Shape pick_grouped(const Shape (&shapes)[NS], int64_t M, int64_t N, int64_t groups, int cus) {
+  Shape best{};
+  double best_t = 0;
+  const int64_t hit = std::min(groups, M);
+  for (const Shape &s : shapes) {
+    if (s.tn == 192) continue;
+    const double tiles = ((double)M / s.tm + 0.5 * (double)hit) * (double)((N + s.tn - 1) / s.tn);
+    const double waves = tiles / cus < 1.0 ? 1.0 : tiles / cus + 0.5;
+    const double t = waves * s.tm * s.tn / s.rel;
+    if (best.tm == 0 || t < best_t) {
+      best = s;
+      best_t = t;
+    }
+  }
+  return best;
+}
+
+}  // namespace
+
+hipError_t launch_gemm(const Gemm &g) {
+  int tm = g.tile_m, tn = g.tile_n;
+  if (tm == 0) {
+    const bool rows_ok = !g.trans_a && g.trans_b;
+    const int64_t rows = g.groups ? (g.M + g.groups - 1) / g.groups : g.M;
+    if (rows_ok && rows <= kFewRows) {
+      tm = tn = 16;
+    } else {
+      Shape s;
+      if (g.groups)
+        s = pick_grouped(kShapesBK, g.M, g.N, g.groups, g.cus);
+      else if (g.trans_b && !is_gated(g.act))
+        s = pick_shape(kShapesBK, g.M, g.N, g.cus);
+      else
+        s = pick_shape(kShapesBN, g.M, g.N, g.cus);
+      tm = s.tm;
+      tn = s.tn;
+    }
+  }
+  if (tm == 16) return launch_rows(g);
+  return g.dtype == 1 ? launch_gemm_f16(g, tm, tn) : launch_gemm_bf16(g, tm, tn);
+}
+
+hipError_t launch_grouped_tn(const GroupedTn &g) {
+  int tm = g.tile_m, tn = g.tile_n;
+  if (tm == 0) {
+    const Shape s = pick_shape(kShapesBN, g.P * g.groups, g.Q, g.cus);
+    tm = s.tm;
+    tn = s.tn;
+  }
+  return g.dtype == 1 ? launch_tn_f16(g, tm, tn) : launch_tn_bf16(g, tm, tn);
+}
+
+}  // namespace ffn
+}  // namespace tgemm

@@ -1,0 +1,282 @@
+// Products of few rows with an epilogue, dense or grouped, for gfx950: single
+// tokens and small batches against weights stored K-contiguous (N x K).
+//
+// What bounds such a product is reading the weight once.  A workgroup takes
+// 16 NB rows of the weight (columns of C) and up to 16 MB rows of A, and its
+// eight waves divide K: wave w takes units of 64 K elements (a 128-byte line
+// of each row) w, w + 8, ...  Weights and rows of A go from memory straight
+// into the registers of v_mfma_f32_16x16x32 (lane l holds row l % 16, eight
+// K elements from 8 (l / 16)), no LDS between: each weight byte is used by
+// one wave only.  Four units are loaded ahead of their products, so a wave
+// has 8 NB KiB of weights in flight.  The waves' sums meet in LDS, are added
+// in wave order (the result does not depend on timing) and pass through the
+// epilogue.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "tgemm_ffn_math.hpp"
+
+namespace tgemm {
+namespace ffn {
+namespace {
+
+typedef __attribute__((ext_vector_type(8))) __bf16 v8bf;
+typedef __attribute__((ext_vector_type(8))) _Float16 v8h;
+
+constexpr uint32_t kOOB = 0x80000000u;  // an offset past every resource
+
+struct RowsArgs {
+  const uint8_t *A, *B;
+  uint8_t *C;
+  const uint8_t *bias, *res;
+  uint8_t *pre;
+  int M, N, K;  // N: output columns
+  int lda, ldb, ldc, ldr, ldp;
+  int act, half;
+  int tiles_m, tiles_n;  // dense
+  // grouped
+  const int32_t *offsets, *rows;
+  int groups, src_rows;
+  int64_t stride_b, stride_bias;
+};
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void *p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, bytes, 0x00020000);
+}
+
+template <int DT>
+__device__ __forceinline__ v4f mfma(const v4u &x, const v4u &y, const v4f &c) {
+  if constexpr (DT == 1)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, x), __builtin_bit_cast(v8h, y), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, x), __builtin_bit_cast(v8bf, y), c, 0, 0, 0);
+}
+
+template <int DT>
+__device__ __forceinline__ void load4(const uint8_t *p, float (&v)[4]) {
+  const v2u w = *(const v2u *)p;
+  unpack2<DT>(w[0], v);
+  unpack2<DT>(w[1], v + 2);
+}
+template <int DT>
+__device__ __forceinline__ void store4(uint8_t *p, const float (&v)[4]) {
+  *(v2u *)p = v2u{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+}
+
+constexpr int kWaves = 8;
+constexpr int kThr = 64 * kWaves;
+
+template <int DT, int MB, int NB, bool GATED, bool GROUPED>
+__global__ __launch_bounds__(kThr) void rows_kernel(const RowsArgs a) {
+  constexpr int kTM = 16 * MB, kOutB = GATED ? NB / 2 : NB, kCols = 16 * kOutB;
+  constexpr int kU = MB * 2 + NB > 8 ? 2 : 4;  // units in flight a wave
+  __shared__ v4f part[kWaves][NB * MB][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+
+  // The tile: rows m0 .. of M (M counts from row `lo` on), columns n0 ...
+  const uint8_t *A = a.A, *B = a.B, *bias = a.bias;
+  int M = a.M, lo = 0, m0, n0;
+  if constexpr (GROUPED) {
+    const int total = total_units(a.offsets, a.groups, a.M, kTM, a.tiles_n, lane);
+    const int wg = (int)blockIdx.x;
+    if (wg >= total) return;
+    const int xcd = wg & 7, base = total >> 3, rem = total & 7;
+    const Found f = find_unit(a.offsets, a.groups, a.M, xcd * base + min(xcd, rem) + (wg >> 3), kTM, a.tiles_n, lane);
+    if (f.e < 0) return;
+    // Row tiles of one column block follow each other: they share its
+    // weights in the XCD's L2.
+    M = f.hi - f.lo;
+    lo = f.lo;
+    const int tiles_m = (M + kTM - 1) / kTM;
+    n0 = f.unit / tiles_m * kCols;
+    m0 = (f.unit % tiles_m) * kTM;
+    B += (size_t)f.e * (size_t)a.stride_b * 2;
+    if (bias) bias += (size_t)f.e * (size_t)a.stride_bias * 2;
+  } else {
+    m0 = (int)blockIdx.x % a.tiles_m * kTM;
+    n0 = (int)blockIdx.x / a.tiles_m * kCols;
+  }
+
+  // Lane l's row of every block and its 16-byte chunk of a unit's first half.
+  const int r = lane & 15, g = lane >> 4;
+  const int cols = min(a.N - n0, kCols);
+  const auto rb = rsrc_of(B + (size_t)n0 * a.ldb * 2,
+                          ((uint32_t)((GATED ? a.half : 0) + cols - 1) * (uint32_t)a.ldb + (uint32_t)a.K) * 2u);
+  uint32_t boff[NB], aoff[MB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    const int c = (GATED ? b >> 1 : b) * 16 + r;
+    const int row = c + (GATED && (b & 1) ? a.half : 0);
+    boff[b] = c < cols ? (uint32_t)row * (uint32_t)a.ldb * 2u + 16u * (uint32_t)g : kOOB;
+  }
+  __amdgpu_buffer_rsrc_t ra;
+  if (GROUPED && a.rows) {
+    ra = rsrc_of(A, a.src_rows > 0 ? ((uint32_t)(a.src_rows - 1) * (uint32_t)a.lda + (uint32_t)a.K) * 2u : 0u);
+#pragma unroll
+    for (int b = 0; b < MB; ++b) {
+      const int m = m0 + 16 * b + r;
+      const int src = m < M ? a.rows[lo + m] : -1;
+      aoff[b] = src >= 0 && src < a.src_rows ? (uint32_t)src * (uint32_t)a.lda * 2u + 16u * (uint32_t)g : kOOB;
+    }
+  } else {
+    ra = rsrc_of(A + (size_t)(lo + m0) * a.lda * 2,
+                 ((uint32_t)(min(M - m0, kTM) - 1) * (uint32_t)a.lda + (uint32_t)a.K) * 2u);
+#pragma unroll
+    for (int b = 0; b < MB; ++b)
+      aoff[b] = m0 + 16 * b + r < M ? (uint32_t)(16 * b + r) * (uint32_t)a.lda * 2u + 16u * (uint32_t)g : kOOB;
+  }
+
+  v4f acc[NB][MB];
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int j = 0; j < MB; ++j) acc[i][j] = v4f{};
+  const int units = (a.K + 63) >> 6;
+  for (int u0 = wave; u0 < units; u0 += kWaves * kU) {
+    v4u x[kU][2][NB], y[kU][2][MB];
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      const int u = u0 + kWaves * i;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        // (K % 8 == 0: a lane's chunk is all inside K or all outside, where
+        // both operands read zeros; a unit past the last is all outside.)
+        const bool in = 64 * u + 32 * s + 8 * g < a.K;
+        const uint32_t at = (uint32_t)u * 128u + 64u * (uint32_t)s;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+          x[i][s][b] = __builtin_amdgcn_raw_buffer_load_b128(rb, in ? boff[b] : kOOB, at, 0);
+#pragma unroll
+        for (int b = 0; b < MB; ++b)
+          y[i][s][b] = __builtin_amdgcn_raw_buffer_load_b128(ra, in ? aoff[b] : kOOB, at, 0);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kU; ++i)
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int m = 0; m < MB; ++m) acc[n][m] = mfma<DT>(x[i][s][n], y[i][s][m], acc[n][m]);
+  }
+#pragma unroll
+  for (int n = 0; n < NB; ++n)
+#pragma unroll
+    for (int m = 0; m < MB; ++m) part[wave][n * MB + m][lane] = acc[n][m];
+  __syncthreads();
+
+  // Lane l of block (n, m) holds row 16 m + l % 16, columns 4 (l / 16) .. + 3.
+  auto sum = [&](int blk, int l, float (&v)[4]) {
+    v4f s = part[0][blk][l];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) s += part[w][blk][l];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = s[q];
+  };
+  with_act<GATED>(a.act, [&](auto act_) {
+    constexpr int ACT = decltype(act_)::value;
+    for (int it = threadIdx.x; it < kOutB * MB * 64; it += kThr) {
+      const int l = it & 63, mb = (it >> 6) % MB, ob = (it >> 6) / MB;
+      const int m = m0 + 16 * mb + (l & 15), c = 16 * ob + 4 * (l >> 4);
+      if (m >= M || c >= cols) continue;
+      const int n = n0 + c;
+      const size_t row = (size_t)(lo + m);
+      float z[4], up[4], v[4];
+      sum((GATED ? 2 * ob : ob) * MB + mb, l, z);
+      if constexpr (GATED) sum((2 * ob + 1) * MB + mb, l, up);
+      if (bias) {
+        load4<DT>(bias + (size_t)n * 2, v);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) z[q] += v[q];
+        if constexpr (GATED) {
+          load4<DT>(bias + (size_t)(a.half + n) * 2, v);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) up[q] += v[q];
+        }
+      }
+      if (a.pre) {
+        uint8_t *p = a.pre + (row * a.ldp + n) * 2;
+        store4<DT>(p, z);
+        if constexpr (GATED) store4<DT>(p + (size_t)a.half * 2, up);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        z[q] = act_fwd<ACT>(z[q]);
+        if constexpr (GATED) z[q] *= up[q];
+      }
+      if (a.res) {
+        load4<DT>(a.res + (row * a.ldr + n) * 2, v);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) z[q] += v[q];
+      }
+      store4<DT>(a.C + (row * a.ldc + n) * 2, z);
+    }
+  });
+}
+
+template <int DT, int MB, int NB, bool GATED>
+hipError_t launch_one(const Gemm &g) {
+  RowsArgs a{};
+  a.A = static_cast<const uint8_t *>(g.A);
+  a.B = static_cast<const uint8_t *>(g.B);
+  a.C = static_cast<uint8_t *>(g.C);
+  a.bias = static_cast<const uint8_t *>(g.bias);
+  a.res = static_cast<const uint8_t *>(g.residual);
+  a.pre = static_cast<uint8_t *>(g.preact);
+  a.M = (int)g.M;
+  a.N = (int)(GATED ? g.N / 2 : g.N);
+  a.K = (int)g.K;
+  a.lda = (int)g.lda;
+  a.ldb = (int)g.ldb;
+  a.ldc = (int)g.ldc;
+  a.ldr = (int)g.ldr;
+  a.ldp = (int)g.ldp;
+  a.act = g.act;
+  a.half = GATED ? a.N : 0;
+  a.offsets = g.offsets;
+  a.rows = g.rows;
+  a.groups = (int)g.groups;
+  a.src_rows = (int)g.src_rows;
+  a.stride_b = g.stride_b;
+  a.stride_bias = g.stride_bias;
+  constexpr int kCols = 16 * (GATED ? NB / 2 : NB), kTM = 16 * MB;
+  a.tiles_n = (a.N + kCols - 1) / kCols;
+  a.tiles_m = (int)((g.M + kTM - 1) / kTM);
+  const int64_t tm = g.groups ? g.M / kTM + std::min(g.groups, g.M) : a.tiles_m;
+  const int64_t wgs = tm * a.tiles_n;
+  if (wgs > (int64_t)(UINT32_MAX / kThr)) return hipErrorInvalidConfiguration;
+  void *args[] = {&a};
+  const void *fn = g.groups ? reinterpret_cast<const void *>(&rows_kernel<DT, MB, NB, GATED, true>)
+                            : reinterpret_cast<const void *>(&rows_kernel<DT, MB, NB, GATED, false>);
+  return hipLaunchKernel(fn, dim3((unsigned)wgs), dim3(kThr), args, 0, g.stream);
+}
+
+template <int DT, int MB>
+hipError_t launch_mb(const Gemm &g) {
+  if (is_gated(g.act)) return launch_one<DT, MB, 2, true>(g);
+  // One block of 16 columns a workgroup while that leaves no more than two
+  // workgroups a CU.
+  return (g.N + 15) / 16 * std::max<int64_t>(g.groups, 1) <= 2 * g.cus ? launch_one<DT, MB, 1, false>(g)
+                                                                       : launch_one<DT, MB, 2, false>(g);
+}
+
+template <int DT>
+hipError_t launch_dt(const Gemm &g) {
+  // Rows of a weight: all of them, or the groups' average (a group with more
+  // takes several row tiles).
+  const int64_t rows = g.groups ? (g.M + g.groups - 1) / g.groups : g.M;
+  if (rows <= 16) return launch_mb<DT, 1>(g);
+  if (rows <= 32) return launch_mb<DT, 2>(g);
+  return launch_mb<DT, 4>(g);
+}
+
+}  // namespace
+
+hipError_t launch_rows(const Gemm &g) { return g.dtype == 1 ? launch_dt<1>(g) : launch_dt<0>(g); }
+
+}  // namespace ffn
+}  // namespace tgemm

@@ -1,0 +1,401 @@
+// The feed-forward products' tiled kernels for gfx950: the K loop of
+// tgemm_kernel.hpp under a fused epilogue (bias, activation, residual, the
+// values before the activation kept for a backward pass), for one weight
+// (dense) or one weight for each group of rows (grouped), and the grouped
+// product over rows that gives each group's weight gradient.
+//
+// What bounds them is the K loop: a 256 x 256 tile at K = 4096 is 64 slices
+// of about 2 us each, and the epilogue's traffic (residual, values before
+// the activation) streams at the end of each tile.
+//
+// The epilogue goes through LDS: the accumulators are indexed statically, so
+// work on them directly would be unrolled 512 times for every activation
+// (code of hundreds of KB a kernel), while a rolled loop over LDS rows keeps
+// one copy of each activation and gives every global access 256 contiguous
+// bytes of a row.  The round trip is about 4096 LDS clocks (2 us) a
+// 256 x 256 tile.
+#pragma once
+
+#include "tgemm_ffn_math.hpp"
+#include "tgemm_kernel.hpp"
+#include "tgemm_shapes.hpp"
+
+namespace tgemm {
+namespace ffn {
+namespace {
+
+// The epilogue's operands (device pointers of the element type; grouped:
+// already at the group's first row or its own entry).
+struct Tail {
+  const uint8_t *bias;  // or nullptr
+  const uint8_t *res;   // or nullptr
+  uint8_t *pre;         // or nullptr
+  int ldr, ldp;
+  int act;
+  int half;  // gated: columns of one half (the second half's offset); else 0
+};
+
+struct Groups {
+  const int32_t *offsets;
+  const int32_t *rows;  // or nullptr
+  int groups, R, src_rows;
+  int64_t stride_b, stride_bias;  // elements
+  int tiles_n;
+};
+
+template <int DT, bool GATED, bool GROUPED>
+struct FfnExt {
+  static constexpr bool kOn = true, kGated = GATED, kGather = GROUPED;
+  int m0, n0;
+  int half;
+  const int32_t *rows;
+  int src_rows;
+  Tail t;
+
+  // Rows [first, first + 64) of the wave tile (32 for 64 x 64 tiles) go
+  // through the wave's own LDS area as binary32, 16-byte chunk k of row r at
+  // place (k / 2 + k % 2 * half the chunks) ^ (r % 8): the writes (16 rows
+  // at one chunk) and the reads (a row's even chunks, then its odd ones)
+  // each spread over all banks.
+  template <class K>
+  __device__ __forceinline__ void store(K &k) const {
+    constexpr int kWM = K::kWM, kWN = K::kWN, kNBn = K::kNBn;
+    constexpr int kRows = kWM < 64 ? kWM : 64, kChunks = kWN / 4;
+    static_assert(K::kBlk == 16 && kChunks % 8 == 0 && kRows * kWN * 4 <= K::kSlotB && kRows * kWN * 4 <= K::kSlotA, "staging area");
+    const int lane = k.lane;
+    LDS_AS uint8_t *area = k.wave == 0   ? k.slots.a[0]
+                           : k.wave == 1 ? k.slots.a[1]
+                           : k.wave == 2 ? k.slots.b[0]
+                                         : k.slots.b[1];
+    // Every wave's reads of the slots and loads into them are done.
+    barrier();
+#pragma unroll
+    for (int ph = 0; ph < kWM / kRows; ++ph) {
+#pragma unroll
+      for (int j = 0; j < kRows / 16; ++j) {
+        const int r = 16 * j + (lane & 15);
+#pragma unroll
+        for (int i = 0; i < kNBn; ++i) {
+          const int c = 4 * i + (lane >> 4);
+          const int at = ((c >> 1) + (c & 1) * (kChunks / 2)) ^ (r & 7);
+          *(LDS_AS f32x4 *)(area + r * (kWN * 4) + at * 16) = k.acc[i][ph * (kRows / 16) + j];
+        }
+      }
+      asm volatile("" ::: "memory");
+      with_act<GATED>(t.act, [&](auto act) { rows_out<decltype(act)::value, kRows>(k, area, ph * kRows); });
+      asm volatile("" ::: "memory");
+    }
+  }
+
+  __device__ static __forceinline__ void read8(const LDS_AS uint8_t *row, int r7, int c, int odd, float (&v)[8]) {
+    const f32x4 lo = *(const LDS_AS f32x4 *)(row + ((c ^ r7) << 4));
+    const f32x4 hi = *(const LDS_AS f32x4 *)(row + (((c + odd) ^ r7) << 4));
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      v[q] = lo[q];
+      v[4 + q] = hi[q];
+    }
+  }
+
+  template <int ACT, int ROWS, class K>
+  __device__ __forceinline__ void rows_out(K &k, const LDS_AS uint8_t *area, int first) const {
+    constexpr int kWN = K::kWN, kOdd = kWN / 8;
+    constexpr int kOutN = GATED ? kWN / 2 : kWN;   // output columns of the wave tile
+    constexpr int kPer = kOutN / 8;                // 8-column pieces of a row
+    constexpr int kIter = ROWS * kPer / 64;
+    constexpr int kBatch = kIter % 4 == 0 ? 4 : kIter % 2 == 0 ? 2 : 1;
+    static_assert(ROWS * kPer % 64 == 0, "whole passes");
+    const int mb = m0 + k.wave_m * K::kWM + first, nb = n0 + k.wave_n * kOutN;
+    const int M = k.a.M, N = k.a.N;
+#pragma unroll 1
+    for (int it = 0; it < kIter; it += kBatch) {
+      v4u res[kBatch];
+      int row[kBatch], col[kBatch];
+      bool ok[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int idx = (it + b) * 64 + k.lane;
+        row[b] = idx / kPer;
+        col[b] = idx - row[b] * kPer;
+        ok[b] = mb + row[b] < M && nb + 8 * col[b] < N;
+        if (t.res && ok[b])
+          res[b] = *(const v4u *)(t.res + ((size_t)(mb + row[b]) * t.ldr + nb + 8 * col[b]) * 2);
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int m = mb + row[b], n = nb + 8 * col[b];
+        const LDS_AS uint8_t *lr = area + row[b] * (kWN * 4);
+        float z[8], u[8];
+        if constexpr (GATED) {
+          const int c = 4 * (col[b] >> 1) + (col[b] & 1);
+          read8(lr, row[b] & 7, c, kOdd, z);
+          read8(lr, row[b] & 7, c + 2, kOdd, u);
+        } else {
+          read8(lr, row[b] & 7, col[b], kOdd, z);
+        }
+        if (!ok[b]) continue;
+        if (t.bias) {
+          float bv[8];
+          unpack8<DT>(*(const v4u *)(t.bias + (size_t)n * 2), bv);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) z[q] += bv[q];
+          if constexpr (GATED) {
+            unpack8<DT>(*(const v4u *)(t.bias + (size_t)(t.half + n) * 2), bv);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) u[q] += bv[q];
+          }
+        }
+        if (t.pre) {
+          uint8_t *p = t.pre + ((size_t)m * t.ldp + n) * 2;
+          *(v4u *)p = pack8<DT>(z);
+          if constexpr (GATED) *(v4u *)(p + (size_t)t.half * 2) = pack8<DT>(u);
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          z[q] = act_fwd<ACT>(z[q]);
+          if constexpr (GATED) z[q] *= u[q];
+        }
+        if (t.res) {
+          float rv[8];
+          unpack8<DT>(res[b], rv);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) z[q] += rv[q];
+        }
+        *(v4u *)(k.a.C + ((size_t)m * k.a.ldc + n) * 2) = pack8<DT>(z);
+      }
+    }
+  }
+};
+
+// The grouped product over rows: the plain epilogue.
+struct TnExt {
+  static constexpr bool kOn = true, kGated = false, kGather = false;
+  int m0, n0;
+  template <class K>
+  __device__ __forceinline__ void store(K &k) const {
+    k.epilogue();
+  }
+};
+
+// Workgroups that share an XCD take consecutive tiles (as tile_of).
+__device__ __forceinline__ int xcd_order(int wg, int total) {
+  const int xcd = wg & 7, base = total >> 3, rem = total & 7;
+  return xcd * base + min(xcd, rem) + (wg >> 3);
+}
+
+// Tile v of a group's tiles_m x tiles_n: groups of kGroupM tile rows, column
+// by column (as tile_of).
+__device__ __forceinline__ void tile_in_group(int v, int tiles_m, int tiles_n, int &tm, int &tn) {
+  const int strip = v / (kGroupM * tiles_n);
+  const int first = strip * kGroupM;
+  const int rows = min(tiles_m - first, kGroupM);
+  const int in = v - strip * kGroupM * tiles_n;
+  tm = first + in % rows;
+  tn = in / rows;
+}
+
+#define TGEMM_FFN_SLOTS(TM, TN)                                                \
+  __shared__ __attribute__((aligned(1024))) uint8_t sA0[TM * kRowBytes];       \
+  __shared__ __attribute__((aligned(1024))) uint8_t sA1[TM * kRowBytes];       \
+  __shared__ __attribute__((aligned(1024))) uint8_t sB0[TN * kRowBytes];       \
+  __shared__ __attribute__((aligned(1024))) uint8_t sB1[TN * kRowBytes];       \
+  Slots slots;                                                                 \
+  slots.a[0] = (LDS_AS uint8_t *)sA0;                                          \
+  slots.a[1] = (LDS_AS uint8_t *)sA1;                                          \
+  slots.b[0] = (LDS_AS uint8_t *)sB0;                                          \
+  slots.b[1] = (LDS_AS uint8_t *)sB1;                                          \
+  slots.junk = nullptr;                                                        \
+  slots.stage = nullptr;                                                       \
+  if constexpr (kSlots<T, TM, TN> == 4) {                                      \
+    __shared__ __attribute__((aligned(1024))) uint8_t sA2[TM * kRowBytes];     \
+    __shared__ __attribute__((aligned(1024))) uint8_t sA3[TM * kRowBytes];     \
+    __shared__ __attribute__((aligned(1024))) uint8_t sB2[TN * kRowBytes];     \
+    __shared__ __attribute__((aligned(1024))) uint8_t sB3[TN * kRowBytes];     \
+    slots.a[2] = (LDS_AS uint8_t *)sA2;                                        \
+    slots.a[3] = (LDS_AS uint8_t *)sA3;                                        \
+    slots.b[2] = (LDS_AS uint8_t *)sB2;                                        \
+    slots.b[3] = (LDS_AS uint8_t *)sB3;                                        \
+  }
+
+template <class T, int TM, int TN, bool GATED>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void epilogue_kernel(const Args a, const Tail t) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  TGEMM_FFN_SLOTS(TM, TN)
+  int tm, tn;
+  tile_of((int)blockIdx.x, a.tiles_m * a.tiles_n, a.tiles_m, a.tiles_n, tm, tn);
+  using X = FfnExt<T::kDt, GATED, false>;
+  const X x{tm * TM, tn * (GATED ? TN / 2 : TN), t.half, nullptr, 0, t};
+  Kernel<T, TM, TN, false, X> k(a, slots, x);
+  k.run();
+#endif
+}
+
+template <class T, int TM, int TN, bool GATED>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void grouped_kernel(const Args a0, const Tail t0, const Groups g) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  TGEMM_FFN_SLOTS(TM, TN)
+  const int lane = threadIdx.x & 63;
+  const int total = total_units(g.offsets, g.groups, g.R, TM, g.tiles_n, lane);
+  if ((int)blockIdx.x >= total) return;
+  const Found f = find_unit(g.offsets, g.groups, g.R, xcd_order((int)blockIdx.x, total), TM, g.tiles_n, lane);
+  if (f.e < 0) return;
+  int tm, tn;
+  tile_in_group(f.unit, (f.hi - f.lo + TM - 1) / TM, g.tiles_n, tm, tn);
+  // The group's own product: its rows, its weight, its bias.
+  Args a = a0;
+  Tail t = t0;
+  a.M = f.hi - f.lo;
+  a.B += (size_t)f.e * (size_t)g.stride_b * 2;
+  a.C += (size_t)f.lo * a.ldc * 2;
+  if (!g.rows) a.A += (size_t)f.lo * a.lda * 2;
+  if (t.bias) t.bias += (size_t)f.e * (size_t)g.stride_bias * 2;
+  if (t.pre) t.pre += (size_t)f.lo * t.ldp * 2;
+  using X = FfnExt<T::kDt, GATED, true>;
+  const X x{tm * TM, tn * (GATED ? TN / 2 : TN), t.half, g.rows ? g.rows + f.lo : nullptr, g.src_rows, t};
+  Kernel<T, TM, TN, false, X> k(a, slots, x);
+  k.run();
+#endif
+}
+
+struct TnGroups {
+  const int32_t *offsets;
+  int R;
+};
+
+template <class T, int TM, int TN>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void grouped_tn_kernel(const Args a0, const TnGroups g) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  TGEMM_FFN_SLOTS(TM, TN)
+  const int tiles = a0.tiles_m * a0.tiles_n;
+  const int v = xcd_order((int)blockIdx.x, (int)gridDim.x);
+  const int e = v / tiles;
+  int tm, tn;
+  tile_in_group(v - e * tiles, a0.tiles_m, a0.tiles_n, tm, tn);
+  const Range r = group_rows(g.offsets, e, g.R);
+  const int lo = __builtin_amdgcn_readfirstlane(r.lo), n = __builtin_amdgcn_readfirstlane(r.hi - r.lo);
+  Args a = a0;
+  a.A += (size_t)lo * a.lda * 2;
+  a.B += (size_t)lo * a.ldb * 2;
+  a.C += (size_t)e * (size_t)a.M * (size_t)a.N * 2;
+  a.K = n;
+  a.ksteps = (n + 63) / 64;
+  Kernel<T, TM, TN, false, TnExt> k(a, slots, TnExt{tm * TM, tn * TN});
+  k.run();
+#endif
+}
+
+inline Args gemm_args(const Gemm &g) {
+  Args a{};
+  a.A = static_cast<const uint8_t *>(g.A);
+  a.B = static_cast<const uint8_t *>(g.B);
+  a.C = static_cast<uint8_t *>(g.C);
+  a.M = (int)g.M;
+  a.N = (int)(is_gated(g.act) ? g.N / 2 : g.N);  // output columns
+  a.K = (int)g.K;
+  a.lda = (int)g.lda;
+  a.ldb = (int)g.ldb;
+  a.ldc = (int)g.ldc;
+  a.ksteps = (int)((g.K + 63) / 64);
+  a.splits = 1;
+  return a;
+}
+inline Tail gemm_tail(const Gemm &g) {
+  return Tail{static_cast<const uint8_t *>(g.bias), static_cast<const uint8_t *>(g.residual),
+              static_cast<uint8_t *>(g.preact), (int)g.ldr, (int)g.ldp, g.act,
+              is_gated(g.act) ? (int)(g.N / 2) : 0};
+}
+
+// (A dispatch holds fewer than 2^32 work-items per dimension.)
+inline bool grid_ok(int64_t wgs) { return wgs <= (int64_t)(UINT32_MAX / kThreads); }
+
+template <class T, int TM, int TN, bool GATED>
+hipError_t launch_tile(const Gemm &g) {
+  Args a = gemm_args(g);
+  Tail t = gemm_tail(g);
+  constexpr int kCols = GATED ? TN / 2 : TN;
+  a.tiles_n = (a.N + kCols - 1) / kCols;
+  if (g.groups == 0) {
+    a.tiles_m = (int)((g.M + TM - 1) / TM);
+    const int64_t wgs = (int64_t)a.tiles_m * a.tiles_n;
+    if (!grid_ok(wgs)) return hipErrorInvalidConfiguration;
+    void *args[] = {&a, &t};
+    return hipLaunchKernel(reinterpret_cast<const void *>(&epilogue_kernel<T, TM, TN, GATED>), dim3((unsigned)wgs),
+                           dim3(kThreads), args, 0, g.stream);
+  }
+  if constexpr (T::kAK && !(TM == 256 && TN == 192)) {
+    // The most tiles the groups can have: each one's last may be partial.
+    const int64_t wgs = (g.M / TM + (g.groups < g.M ? g.groups : g.M)) * (int64_t)a.tiles_n;
+    if (!grid_ok(wgs)) return hipErrorInvalidConfiguration;
+    Groups gr{g.offsets, g.rows, (int)g.groups, (int)g.M, (int)g.src_rows, g.stride_b, g.stride_bias, a.tiles_n};
+    void *args[] = {&a, &t, &gr};
+    return hipLaunchKernel(reinterpret_cast<const void *>(&grouped_kernel<T, TM, TN, GATED>), dim3((unsigned)wgs),
+                           dim3(kThreads), args, 0, g.stream);
+  }
+  return hipErrorInvalidValue;
+}
+
+template <int DT, bool AK, bool BK>
+hipError_t launch_tiles(const Gemm &g, int tm, int tn) {
+  using T = Traits<DT, AK, BK>;
+  if constexpr (AK) {
+    if (is_gated(g.act)) {
+      if (tm == 256 && tn == 256) return launch_tile<T, 256, 256, true>(g);
+      if (tm == 128 && tn == 128) return launch_tile<T, 128, 128, true>(g);
+      if (tm == 64 && tn == 64) return launch_tile<T, 64, 64, true>(g);
+      return hipErrorInvalidValue;
+    }
+  }
+  if (tm == 256 && tn == 256) return launch_tile<T, 256, 256, false>(g);
+  if constexpr (BK)
+    if (tm == 256 && tn == 192) return launch_tile<T, 256, 192, false>(g);
+  if (tm == 128 && tn == 128) return launch_tile<T, 128, 128, false>(g);
+  if (tm == 64 && tn == 64) return launch_tile<T, 64, 64, false>(g);
+  return hipErrorInvalidValue;
+}
+
+template <int DT>
+hipError_t launch_layouts(const Gemm &g, int tm, int tn) {
+  const bool ak = !g.trans_a, bk = g.trans_b;
+  if (ak && bk) return launch_tiles<DT, true, true>(g, tm, tn);
+  if (ak) return launch_tiles<DT, true, false>(g, tm, tn);
+  if (bk) return launch_tiles<DT, false, true>(g, tm, tn);
+  return launch_tiles<DT, false, false>(g, tm, tn);
+}
+
+template <int DT, int TM, int TN>
+hipError_t launch_tn_tile(const GroupedTn &g) {
+  using T = Traits<DT, false, false>;
+  Args a{};
+  a.A = static_cast<const uint8_t *>(g.X);
+  a.B = static_cast<const uint8_t *>(g.Y);
+  a.C = static_cast<uint8_t *>(g.out);
+  a.M = (int)g.P;
+  a.N = (int)g.Q;
+  a.lda = (int)g.ldx;
+  a.ldb = (int)g.ldy;
+  a.ldc = (int)g.Q;
+  a.splits = 1;
+  a.tiles_m = (int)((g.P + TM - 1) / TM);
+  a.tiles_n = (int)((g.Q + TN - 1) / TN);
+  const int64_t wgs = g.groups * a.tiles_m * a.tiles_n;
+  if (!grid_ok(wgs)) return hipErrorInvalidConfiguration;
+  TnGroups gr{g.offsets, (int)g.R};
+  void *args[] = {&a, &gr};
+  return hipLaunchKernel(reinterpret_cast<const void *>(&grouped_tn_kernel<T, TM, TN>), dim3((unsigned)wgs),
+                         dim3(kThreads), args, 0, g.stream);
+}
+
+template <int DT>
+hipError_t launch_tn(const GroupedTn &g, int tm, int tn) {
+  if (tm == 256 && tn == 256) return launch_tn_tile<DT, 256, 256>(g);
+  if (tm == 128 && tn == 128) return launch_tn_tile<DT, 128, 128>(g);
+  if (tm == 64 && tn == 64) return launch_tn_tile<DT, 64, 64>(g);
+  return hipErrorInvalidValue;
+}
+
+}  // namespace
+}  // namespace ffn
+}  // namespace tgemm
