@@ -23,129 +23,191 @@ __device__ __forceinline__ float load_logit(const void *p, size_t i) {
   return x == x ? x : -kInf;
 }
 
+// The row's V logits of lane l (experts l, l + L, ...; -inf past the last),
+// loaded without a branch between them so that all are in flight at once.
+template <int DT, int L, int V>
+__device__ __forceinline__ void load_row(const void *p, size_t row, int E, int l, float (&x)[V]) {
+  using Raw = typename std::conditional<DT == 2, float, uint16_t>::type;
+  Raw raw[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) raw[v] = ((const Raw *)p)[row + min(v * L + l, E - 1)];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    float f;
+    if constexpr (DT == 2)
+      f = raw[v];
+    else
+      f = to_f32<DT>(raw[v]);
+    x[v] = v * L + l < E && f == f ? f : -kInf;
+  }
+}
+
 // exp(x - m) for x <= m, of the largest of a row; 1 where both are infinite.
 __device__ __forceinline__ float exp_below(float x, float m) { return x == m ? 1.0f : expf(x - m); }
 
+// Lane l's value from the lane D further on in its row of 16 (cyclic).
+template <int D>
+__device__ __forceinline__ int row_turn(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, 0x120 + D, 0xf, 0xf, false);
+}
+// All lanes of L (16 or 64) combined, in every lane; op commutes, so that all
+// lanes get the same bits.
+template <int L, class V, class Op>
+__device__ __forceinline__ V all_l(V v, Op op) {
+  static_assert(sizeof(V) == 4 && (L == 16 || L == 64), "one register, whole rows");
+  v = op(v, __builtin_bit_cast(V, row_turn<8>(__builtin_bit_cast(int, v))));
+  v = op(v, __builtin_bit_cast(V, row_turn<4>(__builtin_bit_cast(int, v))));
+  v = op(v, __builtin_bit_cast(V, row_turn<2>(__builtin_bit_cast(int, v))));
+  v = op(v, __builtin_bit_cast(V, row_turn<1>(__builtin_bit_cast(int, v))));
+  if constexpr (L == 64) {
+    v = op(v, __shfl_xor(v, 16, 64));
+    v = op(v, __shfl_xor(v, 32, 64));
+  }
+  return v;
+}
 template <int L>
 __device__ __forceinline__ float max_l(float v) {
-#pragma unroll
-  for (int d = 1; d < L; d <<= 1) v = fmaxf(v, __shfl_xor(v, d, L));
-  return v;
+  return all_l<L>(v, [](float a, float b) { return fmaxf(a, b); });
 }
-template <int L, class V>
-__device__ __forceinline__ V sum_l(V v) {
-#pragma unroll
-  for (int d = 1; d < L; d <<= 1) v += __shfl_xor(v, d, L);
-  return v;
+template <int L>
+__device__ __forceinline__ float sum_l(float v) {
+  return all_l<L>(v, [](float a, float b) { return a + b; });
+}
+template <int L>
+__device__ __forceinline__ uint32_t umax_l(uint32_t v) {
+  return all_l<L>(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
 }
 
-// A token takes L lanes of a wave, lane l the experts l, l + L, ...: V of
-// them, held in registers.
+// ---------------------------------------------------------------------------
+// The choice.  A token takes L lanes of a wave, lane l the experts l, l + L,
+// ...: V of them, held in registers.
+//
+// The keys are compared as 64-bit arithmetic gives them, but nearly always
+// 32 bits settle that, so the work is done on whole numbers that hold a
+// rounded key above the expert's index (31 bits in all; higher is better, so
+// the index is kept as its distance from the last): the next best below
+// `cur` is cur + max(v - cur) in wrapping unsigned arithmetic, which takes
+// one subtraction and half a three-way maximum a value, with nothing to
+// remove, and four row turns to join 16 lanes.  What the rounded keys leave
+// open -- two keys in a row closer than their errors, or two groups at the
+// cut -- sends the token through exact_choice.
+//  * 16-bit logits without a bias: the logit's own 16 bits in order; exact.
+//  * otherwise a key's place between the row's largest and least (at most
+//    kWindow below) in 31 - index bits; without a bias the logit itself,
+//    whose places are in order (only equal ones are open); with one the
+//    score + bias in 32 bits, off by at most kKeyError times max(1, |key|):
+//    2^-21 for a sigmoid (its exponential, sum and reciprocal, slopes below
+//    1, and the bias's sum: 5 half steps), 2^-19 for a softmax (also the
+//    row's sum of up to 1024: 30 half steps).
+// Measured at 32768 tokens, 256 binary32 logits, 8 groups, 8 choices of
+// biased sigmoids: 57 us with every key in 64 bits.
+// ---------------------------------------------------------------------------
 struct TopkArgs {
   const void *logits;
   const float *bias;
   float *weights;
   int32_t *ids;
   int T, E, ld, k, groups, used, per, renorm;
+  int shift;           // 2^shift lanes of a token share a group's scan
   uint32_t per_magic;  // expert -> group: __umulhi(e, per_magic)
   float scale;
 };
 
-// KEYED: keys are scores + bias in 64 bits, within the best groups; else the
-// logits themselves (both scores grow with the logit).
-template <int DT, int L, int V, int SCORE, bool KEYED>
-__global__ __launch_bounds__(256) void topk_kernel(const TopkArgs a) {
-  using Key = typename std::conditional<KEYED, double, float>::type;
-  constexpr int kTok = 256 / L;
-  __shared__ Key keys[KEYED ? kTok : 1][KEYED ? L * V : 1];
-  const int l = threadIdx.x & (L - 1), tok = threadIdx.x / L;
-  const int64_t t = (int64_t)blockIdx.x * kTok + tok;
-  const bool live = t < a.T;  // (the lanes of a dead token go along)
-  const size_t row = (size_t)(live ? t : 0) * a.ld;
+__device__ __forceinline__ int group_of(const TopkArgs &a, int e) {
+  return (int)(a.per == 1 ? (uint32_t)e : __umulhi((uint32_t)e, a.per_magic));
+}
 
-  Key key[V];
-  float x[V];
+// Place of expert e in a token's LDS row (its 32 runs start on other banks).
+__device__ __forceinline__ constexpr int skewed(int e) { return e + (e >> 5); }
+
+// Two largest of the keys of each group, by 2^shift lanes a group: lane l
+// works for group l >> shift.  Valid where that is below a.groups.
+template <int L, class Key>
+__device__ __forceinline__ Key group_score(const TopkArgs &a, const Key *keys, int l, int shift) {
+  const Key none = -(Key)kInf;
+  Key best = none, second = none;
+  const int share = 1 << shift, g = min(l >> shift, a.groups - 1), i0 = l & (share - 1);
+  for (int i = i0; i < a.per; i += 8 * share) {
+    Key s[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) s[u] = keys[skewed(g * a.per + min(i + u * share, a.per - 1))];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const Key w = i + u * share < a.per ? s[u] : none;
+      second = w < best ? (w > second ? w : second) : best;
+      best = w > best ? w : best;
+    }
+  }
+  for (int d = 1; d < share; d <<= 1) {
+    const Key ob = __shfl_xor(best, d, L), os = __shfl_xor(second, d, L);
+    const Key low = ob < best ? ob : best;
+    best = ob > best ? ob : best;
+    second = os > second ? os : second;
+    second = low > second ? low : second;
+  }
+  return second == none ? best : best + second;
+}
+
+// Orders LDS traffic between a wave's lanes for the compiler (the hardware
+// keeps a wave's LDS operations in order).
+__device__ __forceinline__ void lds_order() { asm volatile("" ::: "memory"); }
+
+// The k choices with every key in 64 bits; lane j returns the j-th (-1: none).
+// All L lanes of a token come here together; keys: the token's LDS row.
+template <int L, int V, int SCORE, bool BIAS>
+__device__ __forceinline__ int exact_choice(const TopkArgs &a, const float (&x)[V], float m, double *keys, int l) {
+  double key[V];
+  const double none = -(double)kInf;
+  double z = 0.0;
+  const bool scores = BIAS || a.groups > 1;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    if (!scores) {
+      key[v] = 0.0;
+    } else if constexpr (SCORE == kSoftmax) {
+      key[v] = x[v] == -kInf ? 0.0 : x[v] == m ? 1.0 : exp((double)x[v] - (double)m);
+      z += key[v];
+    } else {
+      key[v] = 1.0 / (1.0 + exp(-(double)x[v]));
+    }
+  }
+  if constexpr (SCORE == kSoftmax)
+#pragma unroll
+    for (int d = 1; d < L; d <<= 1) z += __shfl_xor(z, d, L);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int e = v * L + l;
-    x[v] = e < a.E ? load_logit<DT>(a.logits, row + e) : -kInf;
+    if constexpr (SCORE == kSoftmax)
+      if (scores) key[v] /= z;
+    if constexpr (BIAS)
+      if (e < a.E) key[v] += (double)a.bias[e];
+    if (x[v] == -kInf || !(key[v] == key[v])) key[v] = none;
   }
-  // Softmax over the row: its largest and the sum (when a score needs them).
-  float m = -kInf, z = 1.0f;
-  double zd = 1.0;
-  const bool whole = SCORE == kSoftmax && (KEYED || !a.renorm);
-  if (whole) {
+  if (a.groups > 1) {
+    lds_order();
 #pragma unroll
-    for (int v = 0; v < V; ++v) m = fmaxf(m, x[v]);
-    m = max_l<L>(m);
-    if constexpr (KEYED) {
-      zd = 0.0;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const double s = x[v] == -kInf ? 0.0 : x[v] == m ? 1.0 : exp((double)x[v] - (double)m);
-        key[v] = s;
-        zd += s;
-      }
-      zd = sum_l<L>(zd);
-      z = (float)zd;
-    } else {
-      z = 0.0f;
-#pragma unroll
-      for (int v = 0; v < V; ++v) z += x[v] == -kInf ? 0.0f : exp_below(x[v], m);
-      z = sum_l<L>(z);
+    for (int v = 0; v < V; ++v) keys[skewed(v * L + l)] = key[v];
+    lds_order();
+    const double score = group_score<L>(a, keys, l, 0);
+    int above = 0;
+    for (int g = 0; g < a.groups; ++g) {
+      const double o = __shfl(score, g, L);
+      above += o > score || (o == score && g < l);
     }
+    const uint64_t all = __ballot(l < a.groups && above < a.used);
+    const uint64_t mask = L == 64 ? all : (all >> ((threadIdx.x & 63) / L * L)) & ((1ull << (L & 63)) - 1);
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (!((mask >> (group_of(a, v * L + l) & 63)) & 1)) key[v] = none;
   }
-  if constexpr (KEYED) {
+  // Without a bias the score only grows with the logit: ties of scores that
+  // 64 bits no longer tell apart go by the logit.
+  if constexpr (!BIAS)
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int e = v * L + l;
-      double s;
-      if constexpr (SCORE == kSoftmax)
-        s = key[v] / zd;
-      else
-        s = 1.0 / (1.0 + exp(-(double)x[v]));
-      if (a.bias && e < a.E) s += (double)a.bias[e];
-      key[v] = x[v] == -kInf || !(s == s) ? -(double)kInf : s;
-    }
-    if (a.groups > 1) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) keys[tok][v * L + l] = key[v];
-      __syncthreads();
-      // Lane g: the two largest keys of group g.
-      double best = -(double)kInf, second = -(double)kInf;
-      if (l < a.groups) {
-        for (int i = 0; i < a.per; ++i) {
-          const double s = keys[tok][l * a.per + i];
-          second = fmax(second, fmin(s, best));
-          best = fmax(best, s);
-        }
-      }
-      const double score = second == -(double)kInf ? best : best + second;
-      int above = 0;
-      for (int g = 0; g < a.groups; ++g) {
-        const double o = __shfl(score, g, L);
-        above += o > score || (o == score && g < l);
-      }
-      // Bit g of the token's mask: group g stays.
-      const uint64_t all = __ballot(l < a.groups && above < a.used);
-      const uint64_t mask = L == 64 ? all : (all >> ((threadIdx.x & 63) / L * L)) & ((1ull << (L & 63)) - 1);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const uint32_t e = (uint32_t)(v * L + l);
-        const int g = (int)(a.per == 1 ? e : __umulhi(e, a.per_magic));
-        if (!((mask >> (g & 63)) & 1)) key[v] = -(double)kInf;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int v = 0; v < V; ++v) key[v] = x[v];
-  }
-
-  // k times the largest key, ties to the lowest expert; lane j keeps the
-  // j-th choice.
+    for (int v = 0; v < V; ++v) key[v] = key[v] == none ? none : (double)x[v];
   int mine = -1;
   for (int j = 0; j < a.k; ++j) {
-    Key best = -(Key)kInf;
+    double best = none;
     int at = 0x7fffffff;
 #pragma unroll
     for (int v = 0; v < V; ++v)
@@ -155,19 +217,164 @@ __global__ __launch_bounds__(256) void topk_kernel(const TopkArgs a) {
       }
 #pragma unroll
     for (int d = 1; d < L; d <<= 1) {
-      const Key ob = __shfl_xor(best, d, L);
+      const double ob = __shfl_xor(best, d, L);
       const int oa = __shfl_xor(at, d, L);
       if (ob > best || (ob == best && oa < at)) {
         best = ob;
         at = oa;
       }
     }
-    const bool none = at == 0x7fffffff;
-    if (l == j) mine = none ? -1 : at;
+    if (l == j) mine = at == 0x7fffffff ? -1 : at;
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if (at == v * L + l) key[v] = -(Key)kInf;
+      if (at == v * L + l) key[v] = none;
   }
+  return mine;
+}
+
+template <int DT, int L, int V, int SCORE, bool BIAS>
+__global__ __launch_bounds__(256) void topk_kernel(const TopkArgs a) {
+  constexpr int kTok = 256 / L, kE = L * V;
+  constexpr int kIdx = kE <= 256 ? 8 : kE <= 512 ? 9 : 10;  // bits of an index
+  constexpr uint32_t kLow = (1u << kIdx) - 1;
+  constexpr bool kRaw16 = DT != 2 && !BIAS;
+  constexpr float kWindow = BIAS ? 4.0f : 32.0f;
+  // Of a key, relative to max(1, |key|).
+  constexpr float kKeyError = SCORE == kSoftmax ? 0x1p-19f : 0x1p-21f;
+  constexpr float kPlaces = (float)((1 << (31 - kIdx)) - 64);
+  __shared__ double lds[kTok][skewed(kE - 1) + 1];
+  const int l = threadIdx.x & (L - 1), tok = threadIdx.x / L;
+  const int64_t t = (int64_t)blockIdx.x * kTok + tok;
+  const bool live = t < a.T;  // (the lanes of a dead token go along)
+  const size_t row = (size_t)(live ? t : 0) * a.ld;
+
+  float x[V], bias[BIAS ? V : 1];
+  if constexpr (BIAS)
+#pragma unroll
+    for (int v = 0; v < V; ++v) bias[v] = a.bias[min(v * L + l, a.E - 1)];
+  load_row<DT, L>(a.logits, row, a.E, l, x);
+  // The row's largest logit and the softmax's sum, when something needs them.
+  const bool scores = BIAS || a.groups > 1;
+  const bool whole = SCORE == kSoftmax && (scores || !a.renorm);
+  float m = -kInf, z = 1.0f;
+  if (whole) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) m = fmaxf(m, x[v]);
+    m = max_l<L>(m);
+  }
+  float key[V];  // scores + bias (-inf: cannot be chosen)
+  if (whole) {
+    z = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      key[v] = x[v] == -kInf ? 0.0f : exp_below(x[v], m);
+      z += key[v];
+    }
+    z = sum_l<L>(z);
+  }
+  if (scores) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if constexpr (SCORE == kSoftmax)
+        key[v] *= 1.0f / z;
+      else
+        key[v] = sigmoid_(x[v]);
+      if constexpr (BIAS) key[v] += bias[v];
+      if (x[v] == -kInf || !(key[v] == key[v])) key[v] = -kInf;
+    }
+  }
+  bool open = false;  // the token needs exact_choice
+
+  // Groups: x is masked where its group is dropped.
+  float y[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) y[v] = BIAS ? key[v] : x[v];
+  if (a.groups > 1) {
+    float *keys = (float *)lds[tok];
+#pragma unroll
+    for (int v = 0; v < V; ++v) keys[skewed(v * L + l)] = key[v];
+    lds_order();
+    const float score = group_score<L>(a, keys, l, a.shift);
+    const int g0 = l >> a.shift;
+    int above = 0;
+    for (int g = 0; g < a.groups; g += 8) {
+      float o[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) o[u] = __shfl(score, ((g + u) << a.shift) & (L - 1), L);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) above += g + u < a.groups && (o[u] > score || (o[u] == score && g + u < g0));
+    }
+    const bool is = g0 < a.groups, keep = is && above < a.used;
+    // The worst that stays against the best that goes.
+    const float worst = -max_l<L>(keep ? -score : -kInf), best = max_l<L>(is && !keep ? score : -kInf);
+    float most = 1.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) most = fmaxf(most, key[v] == -kInf ? 0.0f : fabsf(key[v]));
+    const float err = 2.0f * kKeyError * max_l<L>(most) * 1.01f;
+    open = best != -kInf && !(worst - best > 2.0f * err);
+    const uint64_t all = __ballot(keep && l == g0 << a.shift);
+    const uint64_t mask = L == 64 ? all : (all >> ((threadIdx.x & 63) / L * L)) & ((1ull << (L & 63)) - 1);
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (!((mask >> ((group_of(a, v * L + l) << a.shift) & 63)) & 1)) y[v] = -kInf;
+  }
+
+  // Keys over indices.
+  uint32_t q[V];
+  uint32_t gap = 1u << kIdx;  // two keys in a row this far apart are in order
+  if constexpr (kRaw16) {
+    gap = 0;  // equal logits are ties: the index settles them
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float w = y[v] + 0.0f;  // (-0 ties with 0)
+      const uint32_t f = __builtin_bit_cast(uint32_t, w);
+      // A bf16 or fp16 value in order: its binary32 bits, 16 of them (fp16:
+      // 19 hold its sign, exponent and fraction).
+      constexpr int kDrop = DT == 0 ? 16 : 13;
+      const uint32_t o = ((int32_t)f < 0 ? ~f : f | 0x80000000u) >> kDrop;
+      q[v] = y[v] == -kInf ? 0u : ((o + 1) << kIdx) | (kLow - (uint32_t)(v * L + l));
+    }
+  } else {
+    float hi = -kInf, lo = kInf;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      hi = fmaxf(hi, y[v]);
+      lo = y[v] == -kInf ? lo : fminf(lo, y[v]);
+    }
+    hi = max_l<L>(hi);
+    lo = fmaxf(-max_l<L>(-lo), hi - kWindow);
+    const float span = hi - lo;
+    const float per = span > 0.0f ? kPlaces / span : 0.0f;
+    // (An infinite or empty span has no places: what is chosen is then open.)
+    open = open || (hi != -kInf && !(span > 0.0f && span <= kWindow));
+    if constexpr (BIAS) {
+      // (4: the place's own two roundings and its and this line's cut.)
+      const float err = kKeyError * fmaxf(1.0f, fmaxf(fabsf(hi), fabsf(lo)));
+      gap = ((uint32_t)fminf(2.0f * err * per, 1e6f) + 4u) << kIdx;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const uint32_t place = (uint32_t)(fmaxf(y[v] - lo, 0.0f) * per);
+      q[v] = y[v] == -kInf ? 0u : ((place + 1) << kIdx) | (kLow - (uint32_t)(v * L + l));
+    }
+  }
+  int mine = -1;
+  uint32_t cur = 0x7fffffffu;
+  for (int j = 0; j <= a.k; ++j) {
+    uint32_t next = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const uint32_t d = q[v] - cur;
+      next = d > next ? d : next;
+    }
+    next = umax_l<L>(next) + cur;
+    next = cur == 0 ? 0 : next;  // none are left
+    if (j > 0 && next != 0) open = open || (cur | kLow) - (next | kLow) < gap;
+    if (l == j && j < a.k) mine = next == 0 ? -1 : (int)(kLow - (next & kLow));
+    cur = next;
+  }
+  if (!kRaw16 || a.groups > 1)
+    if (open) mine = exact_choice<L, V, SCORE, BIAS>(a, x, m, lds[tok], l);
 
   // Lane j: its choice's score and weight.
   float s = 0.0f, w;
@@ -189,16 +396,17 @@ __global__ __launch_bounds__(256) void topk_kernel(const TopkArgs a) {
 template <int DT, int L, int V>
 hipError_t launch_topk_lv(const Topk &t) {
   TopkArgs a{t.logits, t.bias, t.weights, t.ids, (int)t.T, (int)t.E, (int)t.ld, t.k, t.groups, t.used,
-             (int)(t.E / t.groups), t.renorm, 0, t.scale};
+             (int)(t.E / t.groups), t.renorm, 0, 0, t.scale};
+  while ((t.groups << (a.shift + 1)) <= L) ++a.shift;
   // ceil(2^32 / per): exact quotients for experts below 2^16 (not for per = 1).
   a.per_magic = a.per > 1 ? (uint32_t)((0x100000000ull + (uint64_t)a.per - 1) / (uint64_t)a.per) : 0u;
-  const bool keyed = t.bias != nullptr || t.groups > 1;
+  const bool bias = t.bias != nullptr;
   const int64_t wgs = (t.T + 256 / L - 1) / (256 / L);
   if (wgs > (int64_t)(UINT32_MAX / 256)) return hipErrorInvalidConfiguration;
   const void *fn =
-      t.score == kSoftmax ? (keyed ? reinterpret_cast<const void *>(&topk_kernel<DT, L, V, kSoftmax, true>)
+      t.score == kSoftmax ? (bias ? reinterpret_cast<const void *>(&topk_kernel<DT, L, V, kSoftmax, true>)
                                    : reinterpret_cast<const void *>(&topk_kernel<DT, L, V, kSoftmax, false>))
-                          : (keyed ? reinterpret_cast<const void *>(&topk_kernel<DT, L, V, kSigmoid, true>)
+                          : (bias ? reinterpret_cast<const void *>(&topk_kernel<DT, L, V, kSigmoid, true>)
                                    : reinterpret_cast<const void *>(&topk_kernel<DT, L, V, kSigmoid, false>));
   void *args[] = {&a};
   return hipLaunchKernel(fn, dim3((unsigned)wgs), dim3(256), args, 0, t.stream);
@@ -257,12 +465,9 @@ __global__ __launch_bounds__(256) void topk_grad_kernel(const TopkGradArgs a) {
   float d = 0.0f, base = 0.0f, m = -kInf, z = 1.0f;
   float x[V];
   if (dense) {
+    load_row<DT, L>(a.logits, row, a.E, l, x);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int e = v * L + l;
-      x[v] = e < a.E ? load_logit<DT>(a.logits, row + e) : -kInf;
-      m = fmaxf(m, x[v]);
-    }
+    for (int v = 0; v < V; ++v) m = fmaxf(m, x[v]);
     m = max_l<L>(m);
     z = 0.0f;
 #pragma unroll

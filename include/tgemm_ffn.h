@@ -171,11 +171,12 @@ TGEMM_API int gemm_grouped_tn(const tgemm_grouped_tn_args *args, hipStream_t str
  * A logit of -inf or NaN is masked: its expert is never chosen and takes no
  * part in the row's softmax.  s is the softmax of the row's logits or their
  * sigmoid; the keys are s + bias (bias: E binary32, or NULL), compared as
- * computed in 64 bits (without bias and groups, the logits themselves).  A key
- * of -inf or NaN is never chosen.  groups > 1 cuts the experts into that many
- * runs of E / groups; a group's score is the sum of its two largest keys (its
- * one key, where one is left), and only the groups_used best groups are
- * chosen from.  The choices are the k largest keys in falling order; ties go
+ * computed in 64 bits.  A key of -inf or NaN is never chosen.  groups > 1 cuts
+ * the experts into that many runs of E / groups; a group's score is the sum of
+ * its two largest keys (its one key, where one is left), and only the
+ * groups_used best groups are chosen from.  Without bias experts are then
+ * ordered by the logits themselves (as by s, without the ties that rounding
+ * makes).  The choices are the k largest keys in falling order; ties go
  * to the lowest index, of groups too.  weights are the chosen s, divided by
  * their sum + 1e-20 if renormalize, times scale.  Where fewer than k experts
  * can be chosen the last ids are -1 and their weights 0.

@@ -107,8 +107,7 @@ def topk(logits, k, score="softmax", bias=None, groups=1, used=1, renorm=True, s
         else:
             s = torch.tensor([1.0 / (1.0 + math.exp(-v)) if v > -700 else math.exp(max(v, -800.0)) for v in row.tolist()],
                              dtype=torch.float64)
-        plain = bias is None and groups == 1
-        key = row.clone() if plain else s if bias is None else s + bias.double()
+        key = s if bias is None else s + bias.double()
         key = torch.where(ok & ~torch.isnan(key), key, torch.full_like(key, -math.inf))
         if groups > 1:
             per = E // groups
@@ -117,9 +116,13 @@ def topk(logits, k, score="softmax", bias=None, groups=1, used=1, renorm=True, s
                 two = sorted((v for v in key[g * per:(g + 1) * per].tolist() if v > -math.inf), reverse=True)[:2]
                 sums.append(sum(two) if two else -math.inf)
             keep = sorted(range(groups), key=lambda g: (-sums[g], g))[:used]
-            for g in range(groups):
-                if g not in keep:
-                    key[g * per:(g + 1) * per] = -math.inf
+            dropped = [g for g in range(groups) if g not in keep]
+        else:
+            per, dropped = E, []
+        if bias is None:
+            key = row.clone()          # the order of the scores, without their ties
+        for g in dropped:
+            key[g * per:(g + 1) * per] = -math.inf
         best = [e for e in sorted(range(E), key=lambda e: (-key[e].item(), e)) if key[e] > -math.inf][:k]
         at = torch.tensor(best, dtype=torch.int64)
         if not len(best):
