@@ -356,9 +356,14 @@ int route_topk(const tgemm_route_args *p, hipStream_t stream) {
                       {"logits", p->logits, p->T, p->E, p->ld, elem, false, true},
                       {"bias", p->bias, 1, p->E, p->E, 4, false, false}};
   rc = check(fn, t, 4, 2);
-  if (rc == TGEMM_OK) rc = ensure_device(nullptr, nullptr);
   if (rc != TGEMM_OK) return rc;
-  ffn::Topk g{(int)p->dtype, p->T, p->E, p->logits, p->ld, p->bias, (int)p->k, (int)p->score, (int)p->groups,
+  // (The kernel takes up to 16 rows through one 31-bit resource.)
+  const int64_t ld = p->T == 1 ? p->E : p->ld;
+  if (16 * (uint64_t)ld * (uint64_t)elem > kOffsetLimit)
+    return fail(TGEMM_ETOOBIG, "%s: 16 row strides of logits must be below 2^31 bytes", fn);
+  rc = ensure_device(nullptr, nullptr);
+  if (rc != TGEMM_OK) return rc;
+  ffn::Topk g{(int)p->dtype, p->T, p->E, p->logits, ld, p->bias, (int)p->k, (int)p->score, (int)p->groups,
               (int)p->groups_used, (int)p->renormalize, (float)p->scale, p->weights, p->ids, stream};
   return launched(fn, ffn::launch_topk(g));
 }

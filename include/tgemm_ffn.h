@@ -185,7 +185,7 @@ TGEMM_API int gemm_grouped_tn(const tgemm_grouped_tn_args *args, hipStream_t str
  *            to the element)
  *   weights  T x k binary32;  ids  T x k int32, packed
  * Limits: 1 <= E <= 1024, k <= 64, groups <= 64 dividing E,
- * k <= groups_used E / groups.
+ * k <= groups_used E / groups; 16 rows of logits below 2^31 bytes.
  */
 typedef struct {
   int64_t dtype, T, E;

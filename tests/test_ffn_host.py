@@ -178,7 +178,7 @@ def top(**kw):
     (top(score=2), tg.EINVAL, "score"), (top(renormalize=2), tg.EINVAL, "renormalize"),
     (top(logits=0), tg.EINVAL, "logits"), (top(logits=P[0] + 2), tg.EALIGN, "logits"),
     (top(ld=32), tg.EINVAL, "stride of logits"), (top(ids=P[2]), tg.EINVAL, "overlaps"),
-    (top(T=1 << 30), tg.ETOOBIG, "T k"),
+    (top(T=1 << 30), tg.ETOOBIG, "T k"), (top(ld=1 << 26), tg.ETOOBIG, "16 row strides"),
 ])
 def test_route_topk_refuses(fields, code, word):
     refused("route_topk", code, word, **fields)
