@@ -52,25 +52,46 @@ struct FfnExt {
   int src_rows;
   Tail t;
 
-  // Rows [first, first + 64) of the wave tile (32 for 64 x 64 tiles) go
-  // through the wave's own LDS area as binary32, 16-byte chunk k of row r at
-  // place (k / 2 + k % 2 * half the chunks) ^ (r % 8): the writes (16 rows
-  // at one chunk) and the reads (a row's even chunks, then its odd ones)
-  // each spread over all banks.
+  // 64 rows of the wave tile at a time (32 for 64 x 64 tiles) go through the
+  // wave's own LDS area as binary32, 16-byte chunk k of row r at place (k / 2
+  // + k % 2 * half the chunks) ^ (r % 8): the writes (16 rows at one chunk)
+  // and the reads (a row's even chunks, then its odd ones) each spread over
+  // all banks.  A lane then takes pieces of 8 output columns, 64 pieces of
+  // the wave side by side, kBatch of them at once without a branch between,
+  // so that their LDS reads are in flight together; the residual's loads go
+  // two batches ahead, the first before the accumulators are even in LDS
+  // (one wave a SIMD has nothing else to hide them behind).
+  template <class K>
+  struct Shape {
+    static constexpr int kWM = K::kWM, kWN = K::kWN;
+    static constexpr int kRows = kWM < 64 ? kWM : 64;       // of one phase
+    static constexpr int kOutN = GATED ? kWN / 2 : kWN;     // output columns of the wave tile
+    static constexpr int kPer = kOutN / 8;                  // pieces of a row
+    static constexpr int kPieces = kRows * kPer / 64;       // pieces of a lane and phase
+    static constexpr int kBatch = kPieces % 4 == 0 ? 4 : kPieces % 2 == 0 ? 2 : 1;
+    static constexpr bool kOneColumn = 64 % kPer == 0;      // all of a lane's pieces are in one column
+    static_assert(kRows * kPer % 64 == 0, "whole passes");
+  };
+
   template <class K>
   __device__ __forceinline__ void store(K &k) const {
-    constexpr int kWM = K::kWM, kWN = K::kWN, kNBn = K::kNBn;
-    constexpr int kRows = kWM < 64 ? kWM : 64, kChunks = kWN / 4;
+    using S = Shape<K>;
+    constexpr int kWN = K::kWN, kNBn = K::kNBn, kChunks = kWN / 4, kRows = S::kRows;
     static_assert(K::kBlk == 16 && kChunks % 8 == 0 && kRows * kWN * 4 <= K::kSlotB && kRows * kWN * 4 <= K::kSlotA, "staging area");
     const int lane = k.lane;
     LDS_AS uint8_t *area = k.wave == 0   ? k.slots.a[0]
                            : k.wave == 1 ? k.slots.a[1]
                            : k.wave == 2 ? k.slots.b[0]
                                          : k.slots.b[1];
+    v4u r0[S::kBatch] = {}, r1[S::kBatch] = {};
+    if (t.res) {
+      load_res(k, 0, r0);
+      load_res(k, 1, r1);
+    }
     // Every wave's reads of the slots and loads into them are done.
     barrier();
 #pragma unroll
-    for (int ph = 0; ph < kWM / kRows; ++ph) {
+    for (int ph = 0; ph < K::kWM / kRows; ++ph) {
 #pragma unroll
       for (int j = 0; j < kRows / 16; ++j) {
         const int r = 16 * j + (lane & 15);
@@ -82,8 +103,30 @@ struct FfnExt {
         }
       }
       asm volatile("" ::: "memory");
-      with_act<GATED>(t.act, [&](auto act) { rows_out<decltype(act)::value, kRows>(k, area, ph * kRows); });
+      with_act<GATED>(t.act, [&](auto act) { rows_out<decltype(act)::value>(k, area, ph, r0, r1); });
       asm volatile("" ::: "memory");
+    }
+  }
+
+  // Piece of batch `batch` (of the whole wave tile), number b: its row and
+  // output column in the wave tile.
+  template <class K>
+  __device__ static __forceinline__ void piece(const K &k, int batch, int b, int &row, int &col) {
+    using S = Shape<K>;
+    const int idx = (batch * S::kBatch + b) * 64 + k.lane;
+    row = idx / S::kPer;
+    col = (idx - row * S::kPer) * 8;
+  }
+  template <class K, int N>
+  __device__ __forceinline__ void load_res(const K &k, int batch, v4u (&r)[N]) const {
+    const int mb = m0 + k.wave_m * K::kWM, nb = n0 + k.wave_n * Shape<K>::kOutN;
+#pragma unroll
+    for (int b = 0; b < N; ++b) {
+      int row, col;
+      piece(k, batch, b, row, col);
+      // (Past the edge: the last valid piece again, unused.)
+      const int m = min(mb + row, k.a.M - 1), n = min(nb + col, k.a.N - 8);
+      r[b] = *(const v4u *)(t.res + ((size_t)m * t.ldr + n) * 2);
     }
   }
 
@@ -96,72 +139,102 @@ struct FfnExt {
       v[4 + q] = hi[q];
     }
   }
+  __device__ __forceinline__ void add_bias(int n, float (&z)[8]) const {
+    float v[8];
+    unpack8<DT>(*(const v4u *)(t.bias + (size_t)n * 2), v);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) z[q] += v[q];
+  }
 
-  template <int ACT, int ROWS, class K>
-  __device__ __forceinline__ void rows_out(K &k, const LDS_AS uint8_t *area, int first) const {
-    constexpr int kWN = K::kWN, kOdd = kWN / 8;
-    constexpr int kOutN = GATED ? kWN / 2 : kWN;   // output columns of the wave tile
-    constexpr int kPer = kOutN / 8;                // 8-column pieces of a row
-    constexpr int kIter = ROWS * kPer / 64;
-    constexpr int kBatch = kIter % 4 == 0 ? 4 : kIter % 2 == 0 ? 2 : 1;
-    static_assert(ROWS * kPer % 64 == 0, "whole passes");
-    const int mb = m0 + k.wave_m * K::kWM + first, nb = n0 + k.wave_n * kOutN;
-    const int M = k.a.M, N = k.a.N;
-#pragma unroll 1
-    for (int it = 0; it < kIter; it += kBatch) {
-      v4u res[kBatch];
-      int row[kBatch], col[kBatch];
-      bool ok[kBatch];
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int idx = (it + b) * 64 + k.lane;
-        row[b] = idx / kPer;
-        col[b] = idx - row[b] * kPer;
-        ok[b] = mb + row[b] < M && nb + 8 * col[b] < N;
-        if (t.res && ok[b])
-          res[b] = *(const v4u *)(t.res + ((size_t)(mb + row[b]) * t.ldr + nb + 8 * col[b]) * 2);
+  template <int ACT, class K, int N>
+  __device__ __forceinline__ void rows_out(K &k, const LDS_AS uint8_t *area, int ph, v4u (&r0)[N], v4u (&r1)[N]) const {
+    using S = Shape<K>;
+    constexpr int kWN = K::kWN, kOdd = kWN / 8, kBatches = S::kPieces / N;
+    const int mb = m0 + k.wave_m * K::kWM, nb = n0 + k.wave_n * S::kOutN;
+    const int M = k.a.M, Nc = k.a.N;
+    float b0[8] = {}, b1[8] = {};
+    if constexpr (S::kOneColumn)
+      if (t.bias) {
+        int row, col;
+        piece(k, 0, 0, row, col);
+        const int n = min(nb + col, Nc - 8);
+        add_bias(n, b0);
+        if constexpr (GATED) add_bias(t.half + n, b1);
       }
+#pragma unroll 1
+    for (int i = 0; i < kBatches; ++i) {
+      const int batch = ph * kBatches + i;
+      v4u res[N];
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int m = mb + row[b], n = nb + 8 * col[b];
-        const LDS_AS uint8_t *lr = area + row[b] * (kWN * 4);
-        float z[8], u[8];
+      for (int b = 0; b < N; ++b) {
+        res[b] = r0[b];
+        r0[b] = r1[b];
+      }
+      if (t.res && batch + 2 < kBatches * (K::kWM / S::kRows)) load_res(k, batch + 2, r1);
+      float z[N][8], u[N][8];
+      int m[N], n[N];
+#pragma unroll
+      for (int b = 0; b < N; ++b) {
+        int row, col;
+        piece(k, batch, b, row, col);
+        m[b] = mb + row;
+        n[b] = nb + col;
+        row -= ph * S::kRows;
+        const LDS_AS uint8_t *lr = area + row * (kWN * 4);
         if constexpr (GATED) {
-          const int c = 4 * (col[b] >> 1) + (col[b] & 1);
-          read8(lr, row[b] & 7, c, kOdd, z);
-          read8(lr, row[b] & 7, c + 2, kOdd, u);
+          const int c = 4 * (col >> 4) + ((col >> 3) & 1);
+          read8(lr, row & 7, c, kOdd, z[b]);
+          read8(lr, row & 7, c + 2, kOdd, u[b]);
         } else {
-          read8(lr, row[b] & 7, col[b], kOdd, z);
+          read8(lr, row & 7, col >> 3, kOdd, z[b]);
         }
-        if (!ok[b]) continue;
-        if (t.bias) {
-          float bv[8];
-          unpack8<DT>(*(const v4u *)(t.bias + (size_t)n * 2), bv);
+      }
+      if (t.bias) {
 #pragma unroll
-          for (int q = 0; q < 8; ++q) z[q] += bv[q];
-          if constexpr (GATED) {
-            unpack8<DT>(*(const v4u *)(t.bias + (size_t)(t.half + n) * 2), bv);
+        for (int b = 0; b < N; ++b) {
+          if constexpr (S::kOneColumn) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) u[q] += bv[q];
+            for (int q = 0; q < 8; ++q) {
+              z[b][q] += b0[q];
+              if constexpr (GATED) u[b][q] += b1[q];
+            }
+          } else {
+            add_bias(min(n[b], Nc - 8), z[b]);
+            if constexpr (GATED) add_bias(t.half + min(n[b], Nc - 8), u[b]);
           }
         }
-        if (t.pre) {
-          uint8_t *p = t.pre + ((size_t)m * t.ldp + n) * 2;
-          *(v4u *)p = pack8<DT>(z);
-          if constexpr (GATED) *(v4u *)(p + (size_t)t.half * 2) = pack8<DT>(u);
+      }
+      if (t.pre) {
+#pragma unroll
+        for (int b = 0; b < N; ++b) {
+          uint8_t *p = t.pre + ((size_t)m[b] * t.ldp + n[b]) * 2;
+          const v4u zw = pack8<DT>(z[b]);
+          v4u uw;
+          if constexpr (GATED) uw = pack8<DT>(u[b]);
+          if (m[b] < M && n[b] < Nc) {
+            *(v4u *)p = zw;
+            if constexpr (GATED) *(v4u *)(p + (size_t)t.half * 2) = uw;
+          }
         }
+      }
+#pragma unroll
+      for (int b = 0; b < N; ++b) {
+        float rv[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          z[q] = act_fwd<ACT>(z[q]);
-          if constexpr (GATED) z[q] *= u[q];
+          z[b][q] = act_fwd<ACT>(z[b][q]);
+          if constexpr (GATED) z[b][q] *= u[b][q];
         }
         if (t.res) {
-          float rv[8];
           unpack8<DT>(res[b], rv);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) z[q] += rv[q];
+          for (int q = 0; q < 8; ++q) z[b][q] += rv[q];
         }
-        *(v4u *)(k.a.C + ((size_t)m * k.a.ldc + n) * 2) = pack8<DT>(z);
+      }
+#pragma unroll
+      for (int b = 0; b < N; ++b) {
+        const v4u w = pack8<DT>(z[b]);
+        if (m[b] < M && n[b] < Nc) *(v4u *)(k.a.C + ((size_t)m[b] * k.a.ldc + n[b]) * 2) = w;
       }
     }
   }
