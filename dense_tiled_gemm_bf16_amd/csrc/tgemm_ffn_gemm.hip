@@ -21,8 +21,9 @@ namespace {
 // Most rows of a weight that take the kernel for few rows.
 constexpr int64_t kFewRows = 64;
 
-// The shape with the least estimated time (as pick_shape), over groups of
-// about the same size, whose last row tile is half full on average.
+// The shape with the least estimated time (as pick_shape), over groups of any
+// sizes, whose last row tile is half full on average (256-row tiles: half of
+// the last ones are short tiles of 0.6 of the time, so 0.3 of a tile is lost).
 template <size_t NS>
 Shape pick_grouped(const Shape (&shapes)[NS], int64_t M, int64_t N, int64_t groups, int cus) {
   Shape best{};
@@ -30,7 +31,7 @@ Shape pick_grouped(const Shape (&shapes)[NS], int64_t M, int64_t N, int64_t grou
   const int64_t hit = std::min(groups, M);
   for (const Shape &s : shapes) {
     if (s.tn == 192) continue;
-    const double tiles = ((double)M / s.tm + 0.5 * (double)hit) * (double)((N + s.tn - 1) / s.tn);
+    const double tiles = ((double)M / s.tm + (s.tm == 256 ? 0.3 : 0.5) * (double)hit) * (double)((N + s.tn - 1) / s.tn);
     const double waves = tiles / cus < 1.0 ? 1.0 : tiles / cus + 0.5;
     const double t = waves * s.tm * s.tn / s.rel;
     if (best.tm == 0 || t < best_t) {

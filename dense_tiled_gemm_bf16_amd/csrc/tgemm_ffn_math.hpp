@@ -172,23 +172,20 @@ __device__ __forceinline__ int wave_scan(int v, int lane) {
   }
   return v;
 }
-__device__ __forceinline__ int group_units(const int32_t *offsets, int groups, int R, int e, int size, int times) {
-  if (e >= groups) return 0;
-  const Range r = group_rows(offsets, e, R);
-  return (r.hi - r.lo + size - 1) / size * times;
-}
-__device__ __forceinline__ int total_units(const int32_t *offsets, int groups, int R, int size, int times, int lane) {
+template <class F>
+__device__ __forceinline__ int sum_units(int groups, int lane, F units) {
   int sum = 0;
-  for (int e0 = 0; e0 < groups; e0 += 64) sum += group_units(offsets, groups, R, e0 + lane, size, times);
+  for (int e0 = 0; e0 < groups; e0 += 64) sum += units(e0 + lane);
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d, 64);
   return __builtin_amdgcn_readfirstlane(sum);
 }
-__device__ __forceinline__ Found find_unit(const int32_t *offsets, int groups, int R, int index, int size, int times,
-                                           int lane) {
+// units(e): of group e, 0 past the last.
+template <class F>
+__device__ __forceinline__ Found find_in(const int32_t *offsets, int groups, int R, int index, int lane, F units) {
   int base = 0;
   for (int e0 = 0; e0 < groups; e0 += 64) {
-    const int n = group_units(offsets, groups, R, e0 + lane, size, times);
+    const int n = units(e0 + lane);
     const int upto = wave_scan(n, lane);
     const uint64_t past = __ballot(index < base + upto);
     if (past) {
@@ -196,13 +193,27 @@ __device__ __forceinline__ Found find_unit(const int32_t *offsets, int groups, i
       const int e = e0 + l;
       const int before = base + __builtin_amdgcn_readlane(upto - n, l);
       // (Only offsets that are no offsets can leave the unit outside the group.)
-      if (index < before) return {-1, 0, 0, 0, 0};
+      if (index < before || e >= groups) return {-1, 0, 0, 0, 0};
       const Range r = group_rows(offsets, e, R);
       return {e, __builtin_amdgcn_readfirstlane(r.lo), __builtin_amdgcn_readfirstlane(r.hi), index - before, before};
     }
     base += __builtin_amdgcn_readlane(upto, 63);
   }
   return {-1, 0, 0, 0, base};
+}
+
+// Blocks of `size` rows, each `times` units.
+__device__ __forceinline__ int group_units(const int32_t *offsets, int groups, int R, int e, int size, int times) {
+  if (e >= groups) return 0;
+  const Range r = group_rows(offsets, e, R);
+  return (r.hi - r.lo + size - 1) / size * times;
+}
+__device__ __forceinline__ int total_units(const int32_t *offsets, int groups, int R, int size, int times, int lane) {
+  return sum_units(groups, lane, [&](int e) { return group_units(offsets, groups, R, e, size, times); });
+}
+__device__ __forceinline__ Found find_unit(const int32_t *offsets, int groups, int R, int index, int size, int times,
+                                           int lane) {
+  return find_in(offsets, groups, R, index, lane, [&](int e) { return group_units(offsets, groups, R, e, size, times); });
 }
 
 }  // namespace

@@ -43,7 +43,8 @@ struct Groups {
   int tiles_n;
 };
 
-template <int DT, bool GATED, bool GROUPED>
+// AREA: bytes of each of the four LDS areas (slots 0 and 1 of A and of B).
+template <int DT, bool GATED, bool GROUPED, int AREA>
 struct FfnExt {
   static constexpr bool kOn = true, kGated = GATED, kGather = GROUPED;
   int m0, n0;
@@ -68,7 +69,8 @@ struct FfnExt {
     static constexpr int kOutN = GATED ? kWN / 2 : kWN;     // output columns of the wave tile
     static constexpr int kPer = kOutN / 8;                  // pieces of a row
     static constexpr int kPieces = kRows * kPer / 64;       // pieces of a lane and phase
-    static constexpr int kBatch = kPieces % 4 == 0 ? 4 : kPieces % 2 == 0 ? 2 : 1;
+    // (Gated pieces hold both halves: four of them would spill.)
+    static constexpr int kBatch = kPieces % 4 == 0 && !GATED ? 4 : kPieces % 2 == 0 ? 2 : 1;
     static constexpr bool kOneColumn = 64 % kPer == 0;      // all of a lane's pieces are in one column
     static_assert(kRows * kPer % 64 == 0, "whole passes");
   };
@@ -77,7 +79,7 @@ struct FfnExt {
   __device__ __forceinline__ void store(K &k) const {
     using S = Shape<K>;
     constexpr int kWN = K::kWN, kNBn = K::kNBn, kChunks = kWN / 4, kRows = S::kRows;
-    static_assert(K::kBlk == 16 && kChunks % 8 == 0 && kRows * kWN * 4 <= K::kSlotB && kRows * kWN * 4 <= K::kSlotA, "staging area");
+    static_assert(K::kBlk == 16 && kChunks % 8 == 0 && kRows * kWN * 4 <= AREA, "staging area");
     const int lane = k.lane;
     LDS_AS uint8_t *area = k.wave == 0   ? k.slots.a[0]
                            : k.wave == 1 ? k.slots.a[1]
@@ -240,7 +242,23 @@ struct FfnExt {
   }
 };
 
-// The grouped product over rows: the plain epilogue.
+// Products with nothing to do but the rounding: the plain epilogue, straight
+// from the accumulators.  (An instance of its own: as a branch in FfnExt's it
+// made the compiler spill accumulators, and lose one.)
+struct PlainExt {
+  static constexpr bool kOn = true, kGated = false, kGather = true;
+  int m0, n0;
+  int half;
+  const int32_t *rows;
+  int src_rows;
+  Tail t;
+  template <class K>
+  __device__ __forceinline__ void store(K &k) const {
+    k.epilogue();
+  }
+};
+
+// The grouped product over rows: likewise.
 struct TnExt {
   static constexpr bool kOn = true, kGated = false, kGather = false;
   int m0, n0;
@@ -297,25 +315,47 @@ void epilogue_kernel(const Args a, const Tail t) {
   TGEMM_FFN_SLOTS(TM, TN)
   int tm, tn;
   tile_of((int)blockIdx.x, a.tiles_m * a.tiles_n, a.tiles_m, a.tiles_n, tm, tn);
-  using X = FfnExt<T::kDt, GATED, false>;
+  using X = FfnExt<T::kDt, GATED, false, (TM < TN ? TM : TN) * kRowBytes>;
   const X x{tm * TM, tn * (GATED ? TN / 2 : TN), t.half, nullptr, 0, t};
   Kernel<T, TM, TN, false, X> k(a, slots, x);
   k.run();
 #endif
 }
 
-template <class T, int TM, int TN, bool GATED>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
-void grouped_kernel(const Args a0, const Tail t0, const Groups g) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  TGEMM_FFN_SLOTS(TM, TN)
-  const int lane = threadIdx.x & 63;
-  const int total = total_units(g.offsets, g.groups, g.R, TM, g.tiles_n, lane);
-  if ((int)blockIdx.x >= total) return;
-  const Found f = find_unit(g.offsets, g.groups, g.R, xcd_order((int)blockIdx.x, total), TM, g.tiles_n, lane);
-  if (f.e < 0) return;
-  int tm, tn;
-  tile_in_group(f.unit, (f.hi - f.lo + TM - 1) / TM, g.tiles_n, tm, tn);
+// A group's rows are cut into tiles of TM rows; with 256-row tiles a last one
+// of at most 128 rows is a tile of 128 x TN of its own (about 0.6 of the
+// time), and those come after all the others, to fill the last wave of
+// workgroups.  (16 groups of 152 to 1152 rows, 2048 columns, K = 1536: 40 row
+// tiles, 9 of them short: 77 -> 69 us.)
+template <int TM>
+struct GroupTiles {
+  static constexpr int kShort = TM == 256 ? 128 : 0;  // rows of a short tile; 0: there are none
+  const Groups &g;
+  int lane;
+  // Units (tiles) of group e: whole ones, or the short one.
+  template <bool SHORT>
+  __device__ __forceinline__ int units(int e) const {
+    if (e >= g.groups) return 0;
+    const Range r = group_rows(g.offsets, e, g.R);
+    const int n = r.hi - r.lo, rest = n % TM;
+    const bool has = rest > 0 && rest <= kShort;
+    if (SHORT) return has ? g.tiles_n : 0;
+    return ((n + TM - 1) / TM - (has ? 1 : 0)) * g.tiles_n;
+  }
+  template <bool SHORT>
+  __device__ __forceinline__ int total() const {
+    return sum_units(g.groups, lane, [&](int e) { return units<SHORT>(e); });
+  }
+  template <bool SHORT>
+  __device__ __forceinline__ Found find(int index) const {
+    return find_in(g.offsets, g.groups, g.R, index, lane, [&](int e) { return units<SHORT>(e); });
+  }
+};
+
+// One tile of a group: M0 its first row in the group.
+template <class T, int TM, int TN, bool GATED, bool FUSED, int AREA>
+__device__ __forceinline__ void group_tile(const Args &a0, const Tail &t0, const Groups &g, const Slots &slots, const Found &f,
+                                           int m0, int n0) {
   // The group's own product: its rows, its weight, its bias.
   Args a = a0;
   Tail t = t0;
@@ -325,28 +365,78 @@ void grouped_kernel(const Args a0, const Tail t0, const Groups g) {
   if (!g.rows) a.A += (size_t)f.lo * a.lda * 2;
   if (t.bias) t.bias += (size_t)f.e * (size_t)g.stride_bias * 2;
   if (t.pre) t.pre += (size_t)f.lo * t.ldp * 2;
-  using X = FfnExt<T::kDt, GATED, true>;
-  const X x{tm * TM, tn * (GATED ? TN / 2 : TN), t.half, g.rows ? g.rows + f.lo : nullptr, g.src_rows, t};
+  using X = typename std::conditional<FUSED, FfnExt<T::kDt, GATED, true, AREA>, PlainExt>::type;
+  const X x{m0, n0, t.half, g.rows ? g.rows + f.lo : nullptr, g.src_rows, t};
   Kernel<T, TM, TN, false, X> k(a, slots, x);
   k.run();
+}
+
+template <class T, int TM, int TN, bool GATED, bool FUSED>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void grouped_kernel(const Args a0, const Tail t0, const Groups g) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  TGEMM_FFN_SLOTS(TM, TN)
+  constexpr int kArea = (TM < TN ? TM : TN) * kRowBytes, kCols = GATED ? TN / 2 : TN;
+  const GroupTiles<TM> tiles{g, (int)(threadIdx.x & 63)};
+  const int wg = (int)blockIdx.x, whole = tiles.template total<false>();
+  if (wg < whole) {
+    const Found f = tiles.template find<false>(xcd_order(wg, whole));
+    if (f.e < 0) return;
+    int tm, tn;
+    tile_in_group(f.unit, tiles.template units<false>(f.e) / g.tiles_n, g.tiles_n, tm, tn);
+    group_tile<T, TM, TN, GATED, FUSED, kArea>(a0, t0, g, slots, f, __builtin_amdgcn_readfirstlane(tm * TM),
+                                        __builtin_amdgcn_readfirstlane(tn * kCols));
+  } else if constexpr (GroupTiles<TM>::kShort > 0) {
+    const int shorts = tiles.template total<true>();
+    if (wg - whole >= shorts) return;
+    const Found f = tiles.template find<true>(xcd_order(wg - whole, shorts));
+    if (f.e < 0) return;
+    group_tile<T, GroupTiles<TM>::kShort, TN, GATED, FUSED, kArea>(a0, t0, g, slots, f, (f.hi - f.lo) / TM * TM, f.unit * kCols);
+  }
 #endif
 }
 
 struct TnGroups {
   const int32_t *offsets;
-  int R;
+  int R, groups;
 };
 
+// The group of rank r by falling rows, for at most 64 groups (lane l's group
+// is l); r itself with more.
+__device__ __forceinline__ int group_of_rank(const TnGroups &g, int r, int lane) {
+  if (g.groups > 64) return r;
+  const Range own = group_rows(g.offsets, min(lane, g.groups - 1), g.R);
+  const int n = lane < g.groups ? own.hi - own.lo : -1;
+  int rank = 0;
+  for (int e = 0; e < g.groups; ++e) {
+    const int o = __builtin_amdgcn_readlane(n, e);
+    rank += o > n || (o == n && e < lane);
+  }
+  return (int)__builtin_ctzll(__ballot(lane < g.groups && rank == r));
+}
+
+// A tile takes time with its group's rows, so tiles go out group by group,
+// most rows first, and every XCD (workgroups 8 apart share one) gets an eighth
+// of each group's tiles: consecutive ones of the group's order, which share
+// panels in its L2.  (16 groups of 152 to 1152 rows, 1536 x 2048: groups given
+// whole to an XCD 80 us, so 62 us.)
 template <class T, int TM, int TN>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void grouped_tn_kernel(const Args a0, const TnGroups g) {
 #if defined(__HIP_DEVICE_COMPILE__)
   TGEMM_FFN_SLOTS(TM, TN)
-  const int tiles = a0.tiles_m * a0.tiles_n;
-  const int v = xcd_order((int)blockIdx.x, (int)gridDim.x);
-  const int e = v / tiles;
+  const int lane = threadIdx.x & 63;
+  const int tiles = a0.tiles_m * a0.tiles_n, wg = (int)blockIdx.x;
+  const int rank = wg / tiles, i = wg - rank * tiles;
+  // XCD x = wg % 8 gets tiles / 8 of the group's tiles, or one more for the
+  // first tiles % 8 XCDs from that of the group's first workgroup on.
+  const int x = wg & 7, s = (wg - i) & 7, base = tiles >> 3, more = tiles & 7;
+  int v = x * base + (i >> 3);
+#pragma unroll
+  for (int o = 0; o < 7; ++o) v += o < x && ((o - s) & 7) < more;
+  const int e = group_of_rank(g, rank, lane);
   int tm, tn;
-  tile_in_group(v - e * tiles, a0.tiles_m, a0.tiles_n, tm, tn);
+  tile_in_group(v, a0.tiles_m, a0.tiles_n, tm, tn);
   const Range r = group_rows(g.offsets, e, g.R);
   const int lo = __builtin_amdgcn_readfirstlane(r.lo), n = __builtin_amdgcn_readfirstlane(r.hi - r.lo);
   Args a = a0;
@@ -404,8 +494,11 @@ hipError_t launch_tile(const Gemm &g) {
     if (!grid_ok(wgs)) return hipErrorInvalidConfiguration;
     Groups gr{g.offsets, g.rows, (int)g.groups, (int)g.M, (int)g.src_rows, g.stride_b, g.stride_bias, a.tiles_n};
     void *args[] = {&a, &t, &gr};
-    return hipLaunchKernel(reinterpret_cast<const void *>(&grouped_kernel<T, TM, TN, GATED>), dim3((unsigned)wgs),
-                           dim3(kThreads), args, 0, g.stream);
+    const void *fn = reinterpret_cast<const void *>(&grouped_kernel<T, TM, TN, GATED, true>);
+    if constexpr (!GATED)
+      if (g.act == kNone && !g.bias && !g.preact)
+        fn = reinterpret_cast<const void *>(&grouped_kernel<T, TM, TN, false, false>);
+    return hipLaunchKernel(fn, dim3((unsigned)wgs), dim3(kThreads), args, 0, g.stream);
   }
   return hipErrorInvalidValue;
 }
@@ -455,7 +548,7 @@ hipError_t launch_tn_tile(const GroupedTn &g) {
   a.tiles_n = (int)((g.Q + TN - 1) / TN);
   const int64_t wgs = g.groups * a.tiles_m * a.tiles_n;
   if (!grid_ok(wgs)) return hipErrorInvalidConfiguration;
-  TnGroups gr{g.offsets, (int)g.R};
+  TnGroups gr{g.offsets, (int)g.R, (int)g.groups};
   void *args[] = {&a, &gr};
   return hipLaunchKernel(reinterpret_cast<const void *>(&grouped_tn_kernel<T, TM, TN>), dim3((unsigned)wgs),
                          dim3(kThreads), args, 0, g.stream);

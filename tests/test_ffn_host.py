@@ -241,3 +241,24 @@ def test_the_binding_refuses_what_is_not_on_a_gpu():
             f()
     with pytest.raises(TypeError):
         tg.gemm_epilogue([[1.0]], x)
+
+
+def test_the_products_kernels_keep_their_accumulators_in_registers(tmp_path):
+    """No kernel of the products uses scratch memory: spilled accumulators cost
+    their speed, and the compiler has lost one of them on the way back."""
+    tools = "/opt/rocm/lib/llvm/bin"
+    if not os.path.exists(os.path.join(tools, "llvm-readelf")):
+        pytest.skip("no LLVM tools")
+    so = tmp_path / "lib.so"
+    so.write_bytes(open(ffn.LIB_PATH, "rb").read())
+    subprocess.run([os.path.join(tools, "llvm-objdump"), "--offloading", str(so)], capture_output=True, check=True,
+                   cwd=tmp_path)
+    seen = 0
+    for f in tmp_path.glob("lib.so.*gfx950*"):
+        notes = subprocess.run([os.path.join(tools, "llvm-readelf"), "--notes", str(f)], capture_output=True, text=True,
+                               check=True).stdout
+        for name, size in re.findall(r"\.name:\s+(\S+).*?\.private_segment_fixed_size:\s+(\d+)", notes, re.S):
+            if re.search(r"(epilogue|grouped|grouped_tn|rows)_kernel", name):
+                seen += 1
+                assert int(size) == 0, name
+    assert seen > 60
