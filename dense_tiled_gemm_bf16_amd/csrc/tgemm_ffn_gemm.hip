@@ -18,8 +18,15 @@ bool tile_supported(const Gemm &g, int tm, int tn) {
 
 namespace {
 
-// Most rows of a weight that take the kernel for few rows.
-constexpr int64_t kFewRows = 64;
+// Whether a product takes the kernel for few rows, where its layout does.  One
+// weight: up to 16 rows, one tile of it (4096 x 4096: 1 row 8.5 us, 64 x 64
+// tiles 13.0; 16 rows 10.2 and 13.2; 32 rows 19.4 and 13.4).  Groups: up to 10
+// rows on average (64 experts of 2048 x 2048 gated: 3.5 rows 85 us, 64 x 64
+// tiles 104; 9.4 rows 118 and 122; 16 rows 145 and 124).
+bool few_rows(const Gemm &g) {
+  if (g.trans_a || !g.trans_b) return false;
+  return g.groups ? g.M <= 10 * g.groups : g.M <= 16;
+}
 
 // The shape with the least estimated time (as pick_shape), over groups of any
 // sizes, whose last row tile is half full on average (256-row tiles: half of
@@ -47,9 +54,7 @@ Shape pick_grouped(const Shape (&shapes)[NS], int64_t M, int64_t N, int64_t grou
 hipError_t launch_gemm(const Gemm &g) {
   int tm = g.tile_m, tn = g.tile_n;
   if (tm == 0) {
-    const bool rows_ok = !g.trans_a && g.trans_b;
-    const int64_t rows = g.groups ? (g.M + g.groups - 1) / g.groups : g.M;
-    if (rows_ok && rows <= kFewRows) {
+    if (few_rows(g)) {
       tm = tn = 16;
     } else {
       Shape s;

@@ -164,38 +164,47 @@ struct Found {
   int unit;    // index inside the group
   int before;  // units of the groups before
 };
-__device__ __forceinline__ int wave_scan(int v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int u = __shfl_up(v, d, 64);
-    if (lane >= d) v += u;
-  }
+// Sums of lanes 0 .. l: inside rows of 16 lanes by row shifts (lanes shifted
+// in read 0), then the rows' totals handed on (row_bcast 15 to rows 1 and 3,
+// row_bcast 31 to rows 2 and 3).
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);
   return v;
 }
-template <class F>
-__device__ __forceinline__ int sum_units(int groups, int lane, F units) {
-  int sum = 0;
-  for (int e0 = 0; e0 < groups; e0 += 64) sum += units(e0 + lane);
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d, 64);
-  return __builtin_amdgcn_readfirstlane(sum);
+// Lane l's group e0 + l (empty past the last).
+__device__ __forceinline__ Range lane_rows(const int32_t *offsets, int groups, int R, int e) {
+  if (e >= groups) return {0, 0};
+  return group_rows(offsets, e, R);
 }
-// units(e): of group e, 0 past the last.
+// units(rows): of a group of so many rows (0 of none).
+template <class F>
+__device__ __forceinline__ int sum_units(const int32_t *offsets, int groups, int R, int lane, F units) {
+  int sum = 0;
+  for (int e0 = 0; e0 < groups; e0 += 64) {
+    const Range r = lane_rows(offsets, groups, R, e0 + lane);
+    sum += units(r.hi - r.lo);
+  }
+  return __builtin_amdgcn_readlane(wave_scan(sum), 63);
+}
 template <class F>
 __device__ __forceinline__ Found find_in(const int32_t *offsets, int groups, int R, int index, int lane, F units) {
   int base = 0;
   for (int e0 = 0; e0 < groups; e0 += 64) {
-    const int n = units(e0 + lane);
-    const int upto = wave_scan(n, lane);
+    const Range r = lane_rows(offsets, groups, R, e0 + lane);
+    const int n = units(r.hi - r.lo);
+    const int upto = wave_scan(n);
     const uint64_t past = __ballot(index < base + upto);
     if (past) {
       const int l = (int)__builtin_ctzll(past);
-      const int e = e0 + l;
       const int before = base + __builtin_amdgcn_readlane(upto - n, l);
       // (Only offsets that are no offsets can leave the unit outside the group.)
-      if (index < before || e >= groups) return {-1, 0, 0, 0, 0};
-      const Range r = group_rows(offsets, e, R);
-      return {e, __builtin_amdgcn_readfirstlane(r.lo), __builtin_amdgcn_readfirstlane(r.hi), index - before, before};
+      if (index < before || e0 + l >= groups) return {-1, 0, 0, 0, 0};
+      return {e0 + l, __builtin_amdgcn_readlane(r.lo, l), __builtin_amdgcn_readlane(r.hi, l), index - before, before};
     }
     base += __builtin_amdgcn_readlane(upto, 63);
   }
@@ -203,17 +212,12 @@ __device__ __forceinline__ Found find_in(const int32_t *offsets, int groups, int
 }
 
 // Blocks of `size` rows, each `times` units.
-__device__ __forceinline__ int group_units(const int32_t *offsets, int groups, int R, int e, int size, int times) {
-  if (e >= groups) return 0;
-  const Range r = group_rows(offsets, e, R);
-  return (r.hi - r.lo + size - 1) / size * times;
-}
 __device__ __forceinline__ int total_units(const int32_t *offsets, int groups, int R, int size, int times, int lane) {
-  return sum_units(groups, lane, [&](int e) { return group_units(offsets, groups, R, e, size, times); });
+  return sum_units(offsets, groups, R, lane, [&](int n) { return (n + size - 1) / size * times; });
 }
 __device__ __forceinline__ Found find_unit(const int32_t *offsets, int groups, int R, int index, int size, int times,
                                            int lane) {
-  return find_in(offsets, groups, R, index, lane, [&](int e) { return group_units(offsets, groups, R, e, size, times); });
+  return find_in(offsets, groups, R, index, lane, [&](int n) { return (n + size - 1) / size * times; });
 }
 
 }  // namespace

@@ -786,7 +786,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(const PlanArgs
 #pragma unroll
     for (int w = 0; w < kPlanWaves; ++w) total += cnt[w * a.E + tid];
   }
-  int upto = wave_scan(total, lane);
+  int upto = wave_scan(total);
   if (lane == 63) scan[wave] = upto;
   __syncthreads();
   int all = 0;

@@ -118,7 +118,8 @@ __global__ __launch_bounds__(256) void bias_sum_kernel(const BiasArgs a) {
   int first = 0, count;
   if constexpr (GROUPED) {
     first = total_units(a.offsets, e, a.M, kGradRows, 1, lane);
-    count = group_units(a.offsets, a.groups, a.M, e, kGradRows, 1);
+    const Range r = group_rows(a.offsets, e, a.M);
+    count = (r.hi - r.lo + kGradRows - 1) / kGradRows;
     // (Offsets that are no offsets may count more blocks than there are.)
     if (first < 0 || first > a.chunks) first = a.chunks;
     count = min(count, a.chunks - first);

@@ -2,15 +2,19 @@
 // tokens and small batches against weights stored K-contiguous (N x K).
 //
 // What bounds such a product is reading the weight once.  A workgroup takes
-// 16 NB rows of the weight (columns of C) and up to 16 MB rows of A, and its
-// eight waves divide K: wave w takes units of 64 K elements (a 128-byte line
-// of each row) w, w + 8, ...  Weights and rows of A go from memory straight
-// into the registers of v_mfma_f32_16x16x32 (lane l holds row l % 16, eight
-// K elements from 8 (l / 16)), no LDS between: each weight byte is used by
-// one wave only.  Four units are loaded ahead of their products, so a wave
-// has 8 NB KiB of weights in flight.  The waves' sums meet in LDS, are added
-// in wave order (the result does not depend on timing) and pass through the
-// epilogue.
+// 16 NB rows of the weight (columns of C) and up to 16 rows of A, and its W
+// waves divide K: wave w takes units of 64 K elements (a 128-byte line of
+// each row) w, w + W, ...  Weights and rows of A go from memory straight into
+// the registers of v_mfma_f32_16x16x32 (lane l holds row l % 16, eight K
+// elements from 8 (l / 16)), no LDS between: each weight byte is used by one
+// wave only.  A batch of units is loaded while the one before is multiplied,
+// and the bias and the residual before either.  The waves' sums meet in LDS,
+// are added in wave order (the result does not depend on timing) and pass
+// through the epilogue.
+//
+// More rows would mean reading A's rows in every workgroup from the L2: with
+// 48 rows, 8192 columns, K = 4096 a form of this kernel with up to 64 rows took
+// 22 us where the 64 x 64 tiles take 14, with 32 rows 13.4 as they do.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -55,24 +59,20 @@ __device__ __forceinline__ v4f mfma(const v4u &x, const v4u &y, const v4f &c) {
 }
 
 template <int DT>
-__device__ __forceinline__ void load4(const uint8_t *p, float (&v)[4]) {
-  const v2u w = *(const v2u *)p;
-  unpack2<DT>(w[0], v);
-  unpack2<DT>(w[1], v + 2);
-}
-template <int DT>
 __device__ __forceinline__ void store4(uint8_t *p, const float (&v)[4]) {
   *(v2u *)p = v2u{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
 }
 
-constexpr int kWaves = 8;
-constexpr int kThr = 64 * kWaves;
+constexpr int kTM = 16;
 
-template <int DT, int MB, int NB, bool GATED, bool GROUPED>
-__global__ __launch_bounds__(kThr) void rows_kernel(const RowsArgs a) {
-  constexpr int kTM = 16 * MB, kOutB = GATED ? NB / 2 : NB, kCols = 16 * kOutB;
-  constexpr int kU = MB * 2 + NB > 8 ? 2 : 4;  // units in flight a wave
-  __shared__ v4f part[kWaves][NB * MB][64];
+template <int DT, int W, int NB, bool GATED, bool GROUPED>
+__global__ __launch_bounds__(64 * W) void rows_kernel(const RowsArgs a) {
+  constexpr int kOutB = GATED ? NB / 2 : NB, kCols = 16 * kOutB;
+  static_assert(kOutB <= W, "an output piece a thread");
+  // Units of a batch; two batches are in registers, one on its way while the
+  // other is multiplied.
+  constexpr int kU = NB == 1 ? 4 : 2;
+  __shared__ v4f part[W][NB][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
 
@@ -80,14 +80,8 @@ __global__ __launch_bounds__(kThr) void rows_kernel(const RowsArgs a) {
   const uint8_t *A = a.A, *B = a.B, *bias = a.bias;
   int M = a.M, lo = 0, m0, n0;
   if constexpr (GROUPED) {
-    const int total = total_units(a.offsets, a.groups, a.M, kTM, a.tiles_n, lane);
-    const int wg = (int)blockIdx.x;
-    if (wg >= total) return;
-    const int xcd = wg & 7, base = total >> 3, rem = total & 7;
-    const Found f = find_unit(a.offsets, a.groups, a.M, xcd * base + min(xcd, rem) + (wg >> 3), kTM, a.tiles_n, lane);
+    const Found f = find_unit(a.offsets, a.groups, a.M, (int)blockIdx.x, kTM, a.tiles_n, lane);
     if (f.e < 0) return;
-    // Row tiles of one column block follow each other: they share its
-    // weights in the XCD's L2.
     M = f.hi - f.lo;
     lo = f.lo;
     const int tiles_m = (M + kTM - 1) / kTM;
@@ -105,7 +99,7 @@ __global__ __launch_bounds__(kThr) void rows_kernel(const RowsArgs a) {
   const int cols = min(a.N - n0, kCols);
   const auto rb = rsrc_of(B + (size_t)n0 * a.ldb * 2,
                           ((uint32_t)((GATED ? a.half : 0) + cols - 1) * (uint32_t)a.ldb + (uint32_t)a.K) * 2u);
-  uint32_t boff[NB], aoff[MB];
+  uint32_t boff[NB], aoff;
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     const int c = (GATED ? b >> 1 : b) * 16 + r;
@@ -115,110 +109,121 @@ __global__ __launch_bounds__(kThr) void rows_kernel(const RowsArgs a) {
   __amdgpu_buffer_rsrc_t ra;
   if (GROUPED && a.rows) {
     ra = rsrc_of(A, a.src_rows > 0 ? ((uint32_t)(a.src_rows - 1) * (uint32_t)a.lda + (uint32_t)a.K) * 2u : 0u);
-#pragma unroll
-    for (int b = 0; b < MB; ++b) {
-      const int m = m0 + 16 * b + r;
-      const int src = m < M ? a.rows[lo + m] : -1;
-      aoff[b] = src >= 0 && src < a.src_rows ? (uint32_t)src * (uint32_t)a.lda * 2u + 16u * (uint32_t)g : kOOB;
-    }
+    const int src = m0 + r < M ? a.rows[lo + m0 + r] : -1;
+    aoff = src >= 0 && src < a.src_rows ? (uint32_t)src * (uint32_t)a.lda * 2u + 16u * (uint32_t)g : kOOB;
   } else {
     ra = rsrc_of(A + (size_t)(lo + m0) * a.lda * 2,
                  ((uint32_t)(min(M - m0, kTM) - 1) * (uint32_t)a.lda + (uint32_t)a.K) * 2u);
-#pragma unroll
-    for (int b = 0; b < MB; ++b)
-      aoff[b] = m0 + 16 * b + r < M ? (uint32_t)(16 * b + r) * (uint32_t)a.lda * 2u + 16u * (uint32_t)g : kOOB;
+    aoff = m0 + r < M ? (uint32_t)r * (uint32_t)a.lda * 2u + 16u * (uint32_t)g : kOOB;
   }
 
-  v4f acc[NB][MB];
+  // This thread's piece of the output: lane l of wave ob holds row l % 16,
+  // columns 4 (l / 16) .. + 3 of output block ob.
+  const int m = m0 + r, c = 16 * wave + 4 * g, n = n0 + c;
+  const bool mine = wave < kOutB && m < M && c < cols;
+  const size_t row = (size_t)(lo + m);
+  v2u bias0 = {}, bias1 = {}, res = {};
+  if (mine) {
+    if (bias) {
+      bias0 = *(const v2u *)(bias + (size_t)n * 2);
+      if constexpr (GATED) bias1 = *(const v2u *)(bias + (size_t)(a.half + n) * 2);
+    }
+    if (a.res) res = *(const v2u *)(a.res + (row * a.ldr + n) * 2);
+  }
+
+  v4f acc[NB];
 #pragma unroll
-  for (int i = 0; i < NB; ++i)
-#pragma unroll
-    for (int j = 0; j < MB; ++j) acc[i][j] = v4f{};
+  for (int i = 0; i < NB; ++i) acc[i] = v4f{};
   const int units = (a.K + 63) >> 6;
-  for (int u0 = wave; u0 < units; u0 += kWaves * kU) {
-    v4u x[kU][2][NB], y[kU][2][MB];
+  struct Batch {
+    v4u x[kU][2][NB], y[kU][2];
+  };
+  // (K % 8 == 0: a lane's chunk is all inside K or all outside, where both
+  // operands read zeros; a unit past the last is all outside.  The weights'
+  // loads first: A's wait for its row's index.)
+  auto load = [&](Batch &f, int u0) {
 #pragma unroll
-    for (int i = 0; i < kU; ++i) {
-      const int u = u0 + kWaves * i;
+    for (int i = 0; i < kU; ++i)
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        // (K % 8 == 0: a lane's chunk is all inside K or all outside, where
-        // both operands read zeros; a unit past the last is all outside.)
+        const int u = u0 + W * i;
         const bool in = 64 * u + 32 * s + 8 * g < a.K;
-        const uint32_t at = (uint32_t)u * 128u + 64u * (uint32_t)s;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
-          x[i][s][b] = __builtin_amdgcn_raw_buffer_load_b128(rb, in ? boff[b] : kOOB, at, 0);
-#pragma unroll
-        for (int b = 0; b < MB; ++b)
-          y[i][s][b] = __builtin_amdgcn_raw_buffer_load_b128(ra, in ? aoff[b] : kOOB, at, 0);
+          f.x[i][s][b] = __builtin_amdgcn_raw_buffer_load_b128(rb, in ? boff[b] : kOOB, (uint32_t)u * 128u + 64u * (uint32_t)s, 0);
       }
-    }
+#pragma unroll
+    for (int i = 0; i < kU; ++i)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int u = u0 + W * i;
+        const bool in = 64 * u + 32 * s + 8 * g < a.K;
+        f.y[i][s] = __builtin_amdgcn_raw_buffer_load_b128(ra, in ? aoff : kOOB, (uint32_t)u * 128u + 64u * (uint32_t)s, 0);
+      }
+    __builtin_amdgcn_sched_barrier(0);  // (all on their way before the next products)
+  };
+  auto multiply = [&](const Batch &f) {
 #pragma unroll
     for (int i = 0; i < kU; ++i)
 #pragma unroll
       for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int n = 0; n < NB; ++n)
-#pragma unroll
-          for (int m = 0; m < MB; ++m) acc[n][m] = mfma<DT>(x[i][s][n], y[i][s][m], acc[n][m]);
+        for (int b = 0; b < NB; ++b) acc[b] = mfma<DT>(f.x[i][s][b], f.y[i][s], acc[b]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  Batch f0, f1;
+  constexpr int kStep = W * kU;
+  load(f0, wave);
+  for (int u0 = wave; u0 < units; u0 += 2 * kStep) {
+    load(f1, u0 + kStep);
+    multiply(f0);
+    if (u0 + kStep >= units) break;
+    load(f0, u0 + 2 * kStep);
+    multiply(f1);
   }
 #pragma unroll
-  for (int n = 0; n < NB; ++n)
-#pragma unroll
-    for (int m = 0; m < MB; ++m) part[wave][n * MB + m][lane] = acc[n][m];
+  for (int b = 0; b < NB; ++b) part[wave][b][lane] = acc[b];
   __syncthreads();
+  if (!mine) return;
 
-  // Lane l of block (n, m) holds row 16 m + l % 16, columns 4 (l / 16) .. + 3.
-  auto sum = [&](int blk, int l, float (&v)[4]) {
-    v4f s = part[0][blk][l];
+  auto sum = [&](int b, float (&v)[4]) {
+    v4f t = part[0][b][lane];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) s += part[w][blk][l];
+    for (int w = 1; w < W; ++w) t += part[w][b][lane];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] = s[q];
+    for (int q = 0; q < 4; ++q) v[q] = t[q];
   };
-  with_act<GATED>(a.act, [&](auto act_) {
-    constexpr int ACT = decltype(act_)::value;
-    for (int it = threadIdx.x; it < kOutB * MB * 64; it += kThr) {
-      const int l = it & 63, mb = (it >> 6) % MB, ob = (it >> 6) / MB;
-      const int m = m0 + 16 * mb + (l & 15), c = 16 * ob + 4 * (l >> 4);
-      if (m >= M || c >= cols) continue;
-      const int n = n0 + c;
-      const size_t row = (size_t)(lo + m);
-      float z[4], up[4], v[4];
-      sum((GATED ? 2 * ob : ob) * MB + mb, l, z);
-      if constexpr (GATED) sum((2 * ob + 1) * MB + mb, l, up);
-      if (bias) {
-        load4<DT>(bias + (size_t)n * 2, v);
+  auto add = [&](const v2u &w, float (&v)[4]) {
+    float t[4];
+    unpack2<DT>(w[0], t);
+    unpack2<DT>(w[1], t + 2);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) z[q] += v[q];
-        if constexpr (GATED) {
-          load4<DT>(bias + (size_t)(a.half + n) * 2, v);
+    for (int q = 0; q < 4; ++q) v[q] += t[q];
+  };
+  float z[4], up[4];
+  sum(GATED ? 2 * wave : wave, z);
+  if constexpr (GATED) sum(2 * wave + 1, up);
+  if (bias) {
+    add(bias0, z);
+    if constexpr (GATED) add(bias1, up);
+  }
+  if (a.pre) {
+    uint8_t *p = a.pre + (row * a.ldp + n) * 2;
+    store4<DT>(p, z);
+    if constexpr (GATED) store4<DT>(p + (size_t)a.half * 2, up);
+  }
+  with_act<GATED>(a.act, [&](auto act) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) up[q] += v[q];
-        }
-      }
-      if (a.pre) {
-        uint8_t *p = a.pre + (row * a.ldp + n) * 2;
-        store4<DT>(p, z);
-        if constexpr (GATED) store4<DT>(p + (size_t)a.half * 2, up);
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        z[q] = act_fwd<ACT>(z[q]);
-        if constexpr (GATED) z[q] *= up[q];
-      }
-      if (a.res) {
-        load4<DT>(a.res + (row * a.ldr + n) * 2, v);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) z[q] += v[q];
-      }
-      store4<DT>(a.C + (row * a.ldc + n) * 2, z);
+    for (int q = 0; q < 4; ++q) {
+      z[q] = act_fwd<decltype(act)::value>(z[q]);
+      if constexpr (GATED) z[q] *= up[q];
     }
   });
+  if (a.res) add(res, z);
+  store4<DT>(a.C + (row * a.ldc + n) * 2, z);
 }
 
-template <int DT, int MB, int NB, bool GATED>
+template <int DT, int W, int NB, bool GATED>
 hipError_t launch_one(const Gemm &g) {
   RowsArgs a{};
   a.A = static_cast<const uint8_t *>(g.A);
@@ -243,35 +248,32 @@ hipError_t launch_one(const Gemm &g) {
   a.src_rows = (int)g.src_rows;
   a.stride_b = g.stride_b;
   a.stride_bias = g.stride_bias;
-  constexpr int kCols = 16 * (GATED ? NB / 2 : NB), kTM = 16 * MB;
+  constexpr int kCols = 16 * (GATED ? NB / 2 : NB);
   a.tiles_n = (a.N + kCols - 1) / kCols;
   a.tiles_m = (int)((g.M + kTM - 1) / kTM);
   const int64_t tm = g.groups ? g.M / kTM + std::min(g.groups, g.M) : a.tiles_m;
   const int64_t wgs = tm * a.tiles_n;
-  if (wgs > (int64_t)(UINT32_MAX / kThr)) return hipErrorInvalidConfiguration;
+  if (wgs > (int64_t)(UINT32_MAX / (64 * W))) return hipErrorInvalidConfiguration;
   void *args[] = {&a};
-  const void *fn = g.groups ? reinterpret_cast<const void *>(&rows_kernel<DT, MB, NB, GATED, true>)
-                            : reinterpret_cast<const void *>(&rows_kernel<DT, MB, NB, GATED, false>);
-  return hipLaunchKernel(fn, dim3((unsigned)wgs), dim3(kThr), args, 0, g.stream);
+  const void *fn = g.groups ? reinterpret_cast<const void *>(&rows_kernel<DT, W, NB, GATED, true>)
+                            : reinterpret_cast<const void *>(&rows_kernel<DT, W, NB, GATED, false>);
+  return hipLaunchKernel(fn, dim3((unsigned)wgs), dim3(64 * W), args, 0, g.stream);
 }
 
-template <int DT, int MB>
-hipError_t launch_mb(const Gemm &g) {
-  if (is_gated(g.act)) return launch_one<DT, MB, 2, true>(g);
+template <int DT, int W>
+hipError_t launch_waves(const Gemm &g) {
+  if (is_gated(g.act)) return launch_one<DT, W, 2, true>(g);
   // One block of 16 columns a workgroup while that leaves no more than two
   // workgroups a CU.
-  return (g.N + 15) / 16 * std::max<int64_t>(g.groups, 1) <= 2 * g.cus ? launch_one<DT, MB, 1, false>(g)
-                                                                       : launch_one<DT, MB, 2, false>(g);
+  return (g.N + 15) / 16 * std::max<int64_t>(g.groups, 1) <= 2 * g.cus ? launch_one<DT, W, 1, false>(g)
+                                                                       : launch_one<DT, W, 2, false>(g);
 }
 
 template <int DT>
 hipError_t launch_dt(const Gemm &g) {
-  // Rows of a weight: all of them, or the groups' average (a group with more
-  // takes several row tiles).
-  const int64_t rows = g.groups ? (g.M + g.groups - 1) / g.groups : g.M;
-  if (rows <= 16) return launch_mb<DT, 1>(g);
-  if (rows <= 32) return launch_mb<DT, 2>(g);
-  return launch_mb<DT, 4>(g);
+  // Eight waves hold a CU's registers to themselves; with a short K four do,
+  // and more workgroups share it.
+  return g.K > 2048 ? launch_waves<DT, 8>(g) : launch_waves<DT, 4>(g);
 }
 
 }  // namespace

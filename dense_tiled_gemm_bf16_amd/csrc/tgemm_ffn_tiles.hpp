@@ -332,23 +332,21 @@ struct GroupTiles {
   static constexpr int kShort = TM == 256 ? 128 : 0;  // rows of a short tile; 0: there are none
   const Groups &g;
   int lane;
-  // Units (tiles) of group e: whole ones, or the short one.
+  // Units (tiles) of a group of n rows: whole ones, or the short one.
   template <bool SHORT>
-  __device__ __forceinline__ int units(int e) const {
-    if (e >= g.groups) return 0;
-    const Range r = group_rows(g.offsets, e, g.R);
-    const int n = r.hi - r.lo, rest = n % TM;
+  __device__ __forceinline__ int units(int n) const {
+    const int rest = n % TM;
     const bool has = rest > 0 && rest <= kShort;
     if (SHORT) return has ? g.tiles_n : 0;
     return ((n + TM - 1) / TM - (has ? 1 : 0)) * g.tiles_n;
   }
   template <bool SHORT>
   __device__ __forceinline__ int total() const {
-    return sum_units(g.groups, lane, [&](int e) { return units<SHORT>(e); });
+    return sum_units(g.offsets, g.groups, g.R, lane, [&](int n) { return units<SHORT>(n); });
   }
   template <bool SHORT>
   __device__ __forceinline__ Found find(int index) const {
-    return find_in(g.offsets, g.groups, g.R, index, lane, [&](int e) { return units<SHORT>(e); });
+    return find_in(g.offsets, g.groups, g.R, index, lane, [&](int n) { return units<SHORT>(n); });
   }
 };
 
@@ -383,7 +381,7 @@ void grouped_kernel(const Args a0, const Tail t0, const Groups g) {
     const Found f = tiles.template find<false>(xcd_order(wg, whole));
     if (f.e < 0) return;
     int tm, tn;
-    tile_in_group(f.unit, tiles.template units<false>(f.e) / g.tiles_n, g.tiles_n, tm, tn);
+    tile_in_group(f.unit, tiles.template units<false>(f.hi - f.lo) / g.tiles_n, g.tiles_n, tm, tn);
     group_tile<T, TM, TN, GATED, FUSED, kArea>(a0, t0, g, slots, f, __builtin_amdgcn_readfirstlane(tm * TM),
                                         __builtin_amdgcn_readfirstlane(tn * kCols));
   } else if constexpr (GroupTiles<TM>::kShort > 0) {
