@@ -258,7 +258,64 @@ struct PlainExt {
   }
 };
 
-// The grouped product over rows: likewise.
+// A gated activation alone: both values of an output lie in one lane's
+// accumulators (blocks i and i + 1), so it goes straight from them, as the
+// plain epilogue does.
+template <int DT, bool GROUPED>
+struct GatedExt {
+  static constexpr bool kOn = true, kGated = true, kGather = GROUPED;
+  int m0, n0;
+  int half;
+  const int32_t *rows;
+  int src_rows;
+  Tail t;
+
+  template <class K>
+  __device__ __forceinline__ void store(K &k) const {
+    with_act<true>(t.act, [&](auto act) { store_act<decltype(act)::value>(k); });
+  }
+  template <int ACT>
+  __device__ static __forceinline__ u32x2 value4(const f32x4 &g, const f32x4 &u) {
+    float y[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) y[r] = act_fwd<ACT>(g[r]) * u[r];
+    return u32x2{pack2<DT>(y[0], y[1]), pack2<DT>(y[2], y[3])};
+  }
+  template <int ACT, class K>
+  __device__ __forceinline__ void store_act(K &k) const {
+    const int q = k.lane >> 4;
+#pragma unroll
+    for (int j = 0; j < K::kNBm; ++j) {
+      const int m = m0 + k.wave_m * K::kWM + j * 16 + (k.lane & 15);
+      uint8_t *crow = k.a.C + (size_t)m * k.a.ldc * 2;
+      const int nb = n0 + k.wave_n * (K::kWN / 2);
+      if constexpr (K::kNBn == 2) {
+        const u32x2 x = value4<ACT>(k.acc[0][j], k.acc[1][j]);
+        const int n = nb + 4 * q;
+        if (m < k.a.M && n < k.a.N) *(u32x2 *)(crow + (size_t)n * 2) = x;
+      } else {
+        // Two blocks of outputs: lane swaps leave each lane 8 columns of them
+        // (as the plain epilogue's).
+#pragma unroll
+        for (int i = 0; i < K::kNBn; i += 4) {
+          const u32x2 x = value4<ACT>(k.acc[i][j], k.acc[i + 1][j]), y = value4<ACT>(k.acc[i + 2][j], k.acc[i + 3][j]);
+          uint32_t xo[2], yo[2];
+#pragma unroll
+          for (int d = 0; d < 2; ++d) {
+            const auto h = __builtin_amdgcn_permlane32_swap(x[d], y[d], false, false);
+            const auto r = __builtin_amdgcn_permlane16_swap(h[0], h[1], false, false);
+            xo[d] = r[0];
+            yo[d] = r[1];
+          }
+          const int n = nb + (i / 2) * 16 + 8 * q;
+          if (m < k.a.M && n < k.a.N) store_c(crow + (size_t)n * 2, u32x4{xo[0], xo[1], yo[0], yo[1]});
+        }
+      }
+    }
+  }
+};
+
+// The grouped product over rows: the plain epilogue.
 struct TnExt {
   static constexpr bool kOn = true, kGated = false, kGather = false;
   int m0, n0;
@@ -308,14 +365,17 @@ __device__ __forceinline__ void tile_in_group(int v, int tiles_m, int tiles_n, i
     slots.b[3] = (LDS_AS uint8_t *)sB3;                                        \
   }
 
-template <class T, int TM, int TN, bool GATED>
+// FUSED: with the operands of the epilogue (bias, residual, preact); else only
+// its activation, gated, or (grouped) none.
+template <class T, int TM, int TN, bool GATED, bool FUSED>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void epilogue_kernel(const Args a, const Tail t) {
 #if defined(__HIP_DEVICE_COMPILE__)
   TGEMM_FFN_SLOTS(TM, TN)
   int tm, tn;
   tile_of((int)blockIdx.x, a.tiles_m * a.tiles_n, a.tiles_m, a.tiles_n, tm, tn);
-  using X = FfnExt<T::kDt, GATED, false, (TM < TN ? TM : TN) * kRowBytes>;
+  using X = typename std::conditional<FUSED, FfnExt<T::kDt, GATED, false, (TM < TN ? TM : TN) * kRowBytes>,
+                                      GatedExt<T::kDt, false>>::type;
   const X x{tm * TM, tn * (GATED ? TN / 2 : TN), t.half, nullptr, 0, t};
   Kernel<T, TM, TN, false, X> k(a, slots, x);
   k.run();
@@ -363,7 +423,8 @@ __device__ __forceinline__ void group_tile(const Args &a0, const Tail &t0, const
   if (!g.rows) a.A += (size_t)f.lo * a.lda * 2;
   if (t.bias) t.bias += (size_t)f.e * (size_t)g.stride_bias * 2;
   if (t.pre) t.pre += (size_t)f.lo * t.ldp * 2;
-  using X = typename std::conditional<FUSED, FfnExt<T::kDt, GATED, true, AREA>, PlainExt>::type;
+  using Bare = typename std::conditional<GATED, GatedExt<T::kDt, true>, PlainExt>::type;
+  using X = typename std::conditional<FUSED, FfnExt<T::kDt, GATED, true, AREA>, Bare>::type;
   const X x{m0, n0, t.half, g.rows ? g.rows + f.lo : nullptr, g.src_rows, t};
   Kernel<T, TM, TN, false, X> k(a, slots, x);
   k.run();
@@ -478,13 +539,16 @@ hipError_t launch_tile(const Gemm &g) {
   Tail t = gemm_tail(g);
   constexpr int kCols = GATED ? TN / 2 : TN;
   a.tiles_n = (a.N + kCols - 1) / kCols;
+  const bool bare = !g.bias && !g.residual && !g.preact && (GATED || g.act == kNone);
   if (g.groups == 0) {
     a.tiles_m = (int)((g.M + TM - 1) / TM);
     const int64_t wgs = (int64_t)a.tiles_m * a.tiles_n;
     if (!grid_ok(wgs)) return hipErrorInvalidConfiguration;
     void *args[] = {&a, &t};
-    return hipLaunchKernel(reinterpret_cast<const void *>(&epilogue_kernel<T, TM, TN, GATED>), dim3((unsigned)wgs),
-                           dim3(kThreads), args, 0, g.stream);
+    const void *fn = reinterpret_cast<const void *>(&epilogue_kernel<T, TM, TN, GATED, true>);
+    if constexpr (GATED)
+      if (bare) fn = reinterpret_cast<const void *>(&epilogue_kernel<T, TM, TN, true, false>);
+    return hipLaunchKernel(fn, dim3((unsigned)wgs), dim3(kThreads), args, 0, g.stream);
   }
   if constexpr (T::kAK && !(TM == 256 && TN == 192)) {
     // The most tiles the groups can have: each one's last may be partial.
@@ -492,10 +556,8 @@ hipError_t launch_tile(const Gemm &g) {
     if (!grid_ok(wgs)) return hipErrorInvalidConfiguration;
     Groups gr{g.offsets, g.rows, (int)g.groups, (int)g.M, (int)g.src_rows, g.stride_b, g.stride_bias, a.tiles_n};
     void *args[] = {&a, &t, &gr};
-    const void *fn = reinterpret_cast<const void *>(&grouped_kernel<T, TM, TN, GATED, true>);
-    if constexpr (!GATED)
-      if (g.act == kNone && !g.bias && !g.preact)
-        fn = reinterpret_cast<const void *>(&grouped_kernel<T, TM, TN, false, false>);
+    const void *fn = bare ? reinterpret_cast<const void *>(&grouped_kernel<T, TM, TN, GATED, false>)
+                          : reinterpret_cast<const void *>(&grouped_kernel<T, TM, TN, GATED, true>);
     return hipLaunchKernel(fn, dim3((unsigned)wgs), dim3(kThreads), args, 0, g.stream);
   }
   return hipErrorInvalidValue;
