@@ -114,7 +114,6 @@ struct TopkArgs {
   int32_t *ids;
   int T, E, ld, k, groups, used, per, renorm;
   int picks;           // best keys to look at: k + 2, or k + 1
-  int turns;           // tokens of a lane, one after the other
   int shift;           // 2^shift lanes of a token share a group's scan
   uint32_t ends;       // bit v: a group ends with the v-th experts of all lanes (0: groups are no such runs)
   uint32_t per_magic;  // expert -> group: __umulhi(e, per_magic)
@@ -285,15 +284,15 @@ __global__ __launch_bounds__(256, 4) void topk_kernel(const TopkArgs a) {
   using Raw = typename std::conditional<DT == 2, uint32_t, uint16_t>::type;
   __shared__ double lds[kTok][skewed(kE - 1) + 1];
   const int l = threadIdx.x & (L - 1), tok = threadIdx.x / L;
-  // The tokens of this workgroup, kTok at a time, through a resource at the
-  // first: a row's loads past the last expert read the next row's, past the
+  // The tokens of this workgroup through a resource at the first: a row's
+  // loads past the last expert read the next row's, past the
   // end zeros.
-  const int64_t first = (int64_t)blockIdx.x * kTok * a.turns;
+  const int64_t first = (int64_t)blockIdx.x * kTok;
   const int64_t left = ((int64_t)a.T - 1 - first) * a.ld + a.E;
   const auto rs = __builtin_amdgcn_make_buffer_rsrc((void *)((const uint8_t *)a.logits + first * a.ld * sizeof(Raw)), 0,
                                                     (uint32_t)min(left * (int64_t)sizeof(Raw), (int64_t)0x7fffffff), 0x00020000);
 
-  // Per expert, for all tokens: `code`, its index as the low bits of a key;
+  // Per expert: `code`, its index as the low bits of a key;
   // `shift`, its place with a score of 0 (its bias; from 1 on), or far below
   // 0 if it is none or its bias bars it.
   const bool grouped = GROUPS == kRuns || (GROUPS == kAnyGroups && a.groups > 1);
@@ -332,240 +331,233 @@ __global__ __launch_bounds__(256, 4) void topk_kernel(const TopkArgs a) {
   const uint32_t gap = BIAS ? (((uint32_t)(2.0f * kScoreError * per) + 7u) << kIdx) : kOne;
   const uint32_t group_gap = (uint32_t)(4.0f * kScoreError * per) + 16u;
 
-  for (int turn = 0; turn < a.turns; ++turn) {
-    const int64_t t = first + turn * kTok + tok;
-    const bool live = t < a.T;  // (the lanes of a dead token go along)
-    const uint32_t off = ((uint32_t)(live ? turn * kTok + tok : 0) * (uint32_t)a.ld + (uint32_t)l) * (uint32_t)sizeof(Raw);
-    Raw raw[V];
+  const int64_t t = first + tok;
+  const bool live = t < a.T;  // (the lanes of a dead token go along)
+  const uint32_t off = ((uint32_t)(live ? tok : 0) * (uint32_t)a.ld + (uint32_t)l) * (uint32_t)sizeof(Raw);
+  Raw raw[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const uint32_t o = off + (uint32_t)(v * L * (int)sizeof(Raw));
+    if constexpr (DT == 2)
+      raw[v] = __builtin_amdgcn_raw_buffer_load_b32(rs, o, 0, 0);
+    else
+      raw[v] = __builtin_amdgcn_raw_buffer_load_b16(rs, o, 0, 0);
+  }
+  float x[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) x[v] = DT == 2 ? __builtin_bit_cast(float, (uint32_t)raw[v]) : to_f32<DT>(raw[v]);
+  // Scores, and for a softmax the row's largest logit and sum.
+  const int rest = a.E - l;  // expert v L + l is one if v L < rest
+  float m = -kInf, z = 1.0f, s[V];
+  if (SCORE == kSoftmax && (scores || !a.renorm)) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) m = fmaxf(m, v * L < rest ? x[v] : -kInf);
+    m = max_l<L>(m);
+    z = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const uint32_t o = off + (uint32_t)(v * L * (int)sizeof(Raw));
-      if constexpr (DT == 2)
-        raw[v] = __builtin_amdgcn_raw_buffer_load_b32(rs, o, 0, 0);
-      else
-        raw[v] = __builtin_amdgcn_raw_buffer_load_b16(rs, o, 0, 0);
+      // (Experts whose bias bars them stay in the sum.)
+      const float w = x[v] == m ? 1.0f : exp_(x[v] - m);
+      z += v * L < rest && x[v] > -kInf ? w : 0.0f;
+      s[v] = x[v] > -kInf ? w : __builtin_nanf("");
     }
-    float x[V];
+    z = sum_l<L>(z);
+  } else if (SCORE == kSigmoid && scores) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) x[v] = DT == 2 ? __builtin_bit_cast(float, (uint32_t)raw[v]) : to_f32<DT>(raw[v]);
-    // Scores, and for a softmax the row's largest logit and sum.
-    const int rest = a.E - l;  // expert v L + l is one if v L < rest
-    float m = -kInf, z = 1.0f, s[V];
-    if (SCORE == kSoftmax && (scores || !a.renorm)) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) m = fmaxf(m, v * L < rest ? x[v] : -kInf);
-      m = max_l<L>(m);
-      z = 0.0f;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        // (Experts whose bias bars them stay in the sum.)
-        const float w = x[v] == m ? 1.0f : exp_(x[v] - m);
-        z += v * L < rest && x[v] > -kInf ? w : 0.0f;
-        s[v] = x[v] > -kInf ? w : __builtin_nanf("");
-      }
-      z = sum_l<L>(z);
-    } else if (SCORE == kSigmoid && scores) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) s[v] = sigmoid_(x[v]);
-    }
-    bool open = !window;
+    for (int v = 0; v < V; ++v) s[v] = sigmoid_(x[v]);
+  }
+  bool open = !window;
 
-    // Keys over indices; first by score where groups or a bias go by it.
-    // Place 0 (a key below kOne) is for what cannot be chosen.
-    uint32_t q[V];
-    if (scores) {
-      const float per_s = SCORE == kSoftmax ? per / z : per;
+  // Keys over indices; first by score where groups or a bias go by it.
+  // Place 0 (a key below kOne) is for what cannot be chosen.
+  uint32_t q[V];
+  if (scores) {
+    const float per_s = SCORE == kSoftmax ? per / z : per;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      // (A masked logit's score is NaN, and the maximum then 0.  0 x makes
+      // it one for the sigmoid of -inf; +inf is held back from that.)
+      float at = shift[v];
+      if constexpr (SCORE == kSigmoid) at = fmaf(fminf(x[v], 0x1p100f), 0.0f, at);
+      const uint32_t place = (uint32_t)fmaxf(fmaf(s[v], per_s, at), 0.0f);
+      q[v] = (place << kIdx) + code[v];
+    }
+  }
+  uint32_t keep = ~0u, keep2 = ~0u;  // bit g: group g stays (keep2: from 32 on)
+  if (grouped) {
+    uint32_t score = 0;     // of group l >> gs: the sum of its two places
+    uint32_t odd = kOne;    // below kOne: a group has just one expert left
+    const int gs = GROUPS == kRuns ? 0 : a.shift, g0 = l >> gs;
+    const bool is = g0 < a.groups;
+    if constexpr (GROUPS == kRuns) {
+      // Groups are whole runs of v: two largest in each lane, then over
+      // the lanes.  Bit v of ends: a group ends with v.
+      uint32_t b1 = 0, b2 = 0;
+      int g = 0;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        // (A masked logit's score is NaN, and the maximum then 0.  0 x makes
-        // it one for the sigmoid of -inf; +inf is held back from that.)
-        float at = shift[v];
-        if constexpr (SCORE == kSigmoid) at = fmaf(fminf(x[v], 0x1p100f), 0.0f, at);
-        const uint32_t place = (uint32_t)fmaxf(fmaf(s[v], per_s, at), 0.0f);
-        q[v] = (place << kIdx) + code[v];
-      }
-    }
-    uint32_t keep = ~0u, keep2 = ~0u;  // bit g: group g stays (keep2: from 32 on)
-    if (grouped) {
-      uint32_t score = 0;     // of group l >> gs: the sum of its two places
-      uint32_t odd = kOne;    // below kOne: a group has just one expert left
-      const int gs = GROUPS == kRuns ? 0 : a.shift, g0 = l >> gs;
-      const bool is = g0 < a.groups;
-      if constexpr (GROUPS == kRuns) {
-        // Groups are whole runs of v: two largest in each lane, then over
-        // the lanes.  Bit v of ends: a group ends with v.
-        uint32_t b1 = 0, b2 = 0;
-        int g = 0;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          b2 = max(b2, min(b1, q[v]));
-          b1 = max(b1, q[v]);
-          if ((a.ends >> v) & 1) {
-            const uint32_t top = umax_l<L>(b1), next = umax_l<L>(b1 == top ? b2 : b1);
-            score = l == g ? (top >> kIdx) + (next >> kIdx) : score;
-            odd = min(odd, top < kOne ? kOne : next);
-            ++g;
-            b1 = b2 = 0;
-          }
-        }
-      } else {
-        uint32_t *keys = (uint32_t *)lds[tok];
-        lds_order();
-#pragma unroll
-        for (int v = 0; v < V; ++v) keys[skewed(v * L + l)] = q[v];
-        lds_order();
-        uint32_t top, next;
-        group_top2<L>(a, keys, l, a.shift, top, next);
-        score = (top >> kIdx) + (next >> kIdx);
-        odd = ~umax_l<L>(is && top >= kOne ? ~next : 0u);
-        lds_order();
-      }
-      // Groups before this one in the order: of distinct numbers in 16 lanes
-      // of their own, by turning the row; else one by one.
-      int above = 0;
-      if constexpr (GROUPS == kRuns && L == 16) {
-        above = ranks_above(is ? (score << 4) + (15u - (uint32_t)l) : 0u);
-      } else {
-        for (int g = 0; g < a.groups; g += 8) {
-          uint32_t o[8];
-#pragma unroll
-          for (int u = 0; u < 8; ++u) o[u] = __shfl(score, ((g + u) << gs) & (L - 1), L);
-#pragma unroll
-          for (int u = 0; u < 8; ++u) above += g + u < a.groups && (o[u] > score || (o[u] == score && g + u < g0));
+        b2 = max(b2, min(b1, q[v]));
+        b1 = max(b1, q[v]);
+        if ((a.ends >> v) & 1) {
+          const uint32_t top = umax_l<L>(b1), next = umax_l<L>(b1 == top ? b2 : b1);
+          score = l == g ? (top >> kIdx) + (next >> kIdx) : score;
+          odd = min(odd, top < kOne ? kOne : next);
+          ++g;
+          b1 = b2 = 0;
         }
       }
-      const bool stays = is && above < a.used;
-      // The worst that stays against the best that goes; a group with one
-      // expert left has no sum of two places.
-      const uint32_t worst = ~umax_l<L>(stays ? ~score : 0u), best = umax_l<L>(is && !stays ? score : 0u);
-      open = open || (odd < kOne && a.per > 1) || (a.used < a.groups && worst - best < group_gap);
-      const uint64_t all = __ballot(stays && l == g0 << gs);
-      const uint64_t mask = L == 64 ? all : (all >> ((threadIdx.x & 63) / L * L)) & ((1ull << (L & 63)) - 1);
-      keep = (uint32_t)mask;
-      keep2 = (uint32_t)(mask >> 32);
-    }
-    if constexpr (!BIAS) {
-      // By the logits.
-      if constexpr (kRaw16) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          // A bf16 or fp16 value in order: its binary32 bits, 16 of them
-          // (fp16: 19 hold its sign, exponent and fraction); -0 ties with 0.
-          constexpr int kDrop = DT == 0 ? 16 : 13;
-          const uint32_t f = __builtin_bit_cast(uint32_t, x[v] + 0.0f);
-          const uint32_t o = (f ^ (uint32_t)((int32_t)f >> 31 | (int32_t)0x80000000)) >> kDrop;
-          q[v] = (v * L < rest && x[v] > -kInf ? (o + 1) << kIdx : 0u) + code[v];
-        }
-      } else {
-        float hi = -kInf;
-#pragma unroll
-        for (int v = 0; v < V; ++v) hi = fmaxf(hi, v * L < rest ? x[v] : -kInf);
-        hi = max_l<L>(hi);
-        open = open || hi == kInf;
-        const float lo = hi == kInf || hi == -kInf ? 0.0f : hi - 32.0f;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const uint32_t place = (uint32_t)fminf(fmaxf((x[v] - lo) * (kPlaces / 32.0f), 0.0f), kPlaces);
-          q[v] = (v * L < rest && x[v] > -kInf ? (place + 1) << kIdx : 0u) + code[v];
-        }
-      }
-    }
-    if (grouped) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int g = GROUPS == kRuns ? __popc(a.ends & ((1u << v) - 1)) : group_of(a, v * L + l) << a.shift;
-        const uint32_t word = L == 64 && g >= 32 ? keep2 : keep;
-        q[v] = (word >> (g & 31)) & 1 ? q[v] : code[v];
-      }
-    }
-    // The k best and the one or two behind them, in falling order (all V L
-    // numbers are distinct, and there are more of them); mine: the l-th;
-    // step: the least step down between the first k + 1, last: the one
-    // after.
-    uint32_t mine32 = 0, cur = 0x7fffffffu, step = ~0u, last = ~0u;
-    for (int j = 0; j < a.picks; ++j) {
-      uint32_t next = 0;
-#pragma unroll
-      for (int v = 0; v < V; ++v) next = max(next, q[v] - cur);
-      next = umax_l<L>(next) + cur;
-      step = j > 0 ? min(step, last) : step;
-      last = j > 0 ? cur - next : ~0u;
-      mine32 = l == j ? next : mine32;
-      cur = next;
-    }
-    int mine = mine32 < kOne ? -1 : (int)(kLow - (mine32 & kLow));
-    const size_t row = (size_t)(live ? t : 0) * a.ld;
-    if (!kRaw16 || grouped) {
-      // (A step of whole places differs from that of keys by less than one.)
-      const uint32_t least_step = kRaw16 ? 0u : gap + kOne;
-      const bool close = step < least_step, near = last < least_step;
-      // The k + 1 best are settled among themselves (a lane each) unless the
-      // next is close to them too; without lanes for that all keys are.
-      open = open || (near && (close || a.picks < a.k + 2)) || (close && a.picks < a.k + 2);
-      if (open || close) {
-        const double zd = SCORE == kSoftmax && scores ? exact_sum<L>(x, rest, m) : 1.0;
-        if (open) {
-          mine = exact_choice<DT, L, SCORE, BIAS>(a, row, m, zd, lds[tok], l);
-        } else {
-          const float xm = mine >= 0 && l <= a.k ? load_logit<DT>(a.logits, row + mine) : -kInf;
-          const double key = xm == -kInf ? -(double)kInf : BIAS ? exact_key<SCORE, BIAS>(a, xm, mine, m, zd) : (double)xm;
-          int above = 0;
-          for (int j = 0; j <= a.k; ++j) {
-            const double o = __shfl(key, j, L);
-            const int at = __shfl(mine, j, L);
-            above += o > key || (o == key && at < mine);
-          }
-          // (Missing choices, all -1, stay behind the others.)
-          int *order = (int *)lds[tok];
-          lds_order();
-          if (l <= a.k) order[l] = -1;
-          lds_order();
-          if (l <= a.k && mine >= 0) order[above] = mine;
-          lds_order();
-          mine = l <= a.k ? order[l] : -1;
-          lds_order();
-        }
-      }
-    }
-    if (l >= a.k) mine = -1;
-
-    // Lane j: its choice's score and weight.
-    float sc = 0.0f, w;
-    const float xs = mine >= 0 ? load_logit<DT>(a.logits, row + mine) : -kInf;
-    if constexpr (SCORE == kSoftmax) {
-      const float mm = a.renorm ? max_l<L>(xs) : m;
-      sc = mine >= 0 ? exp_below(xs, mm) : 0.0f;
-      w = a.renorm ? sc / (sum_l<L>(sc) + 1e-20f) : sc / z;
     } else {
-      sc = mine >= 0 ? 1.0f / (1.0f + expf(-xs)) : 0.0f;
-      w = a.renorm ? sc / (sum_l<L>(sc) + 1e-20f) : sc;
+      uint32_t *keys = (uint32_t *)lds[tok];
+      lds_order();
+#pragma unroll
+      for (int v = 0; v < V; ++v) keys[skewed(v * L + l)] = q[v];
+      lds_order();
+      uint32_t top, next;
+      group_top2<L>(a, keys, l, a.shift, top, next);
+      score = (top >> kIdx) + (next >> kIdx);
+      odd = ~umax_l<L>(is && top >= kOne ? ~next : 0u);
+      lds_order();
     }
-    if (live && l < a.k) {
-      a.weights[(size_t)t * a.k + l] = mine >= 0 ? w * a.scale : 0.0f;
-      a.ids[(size_t)t * a.k + l] = mine;
+    // Groups before this one in the order: of distinct numbers in 16 lanes
+    // of their own, by turning the row; else one by one.
+    int above = 0;
+    if constexpr (GROUPS == kRuns && L == 16) {
+      above = ranks_above(is ? (score << 4) + (15u - (uint32_t)l) : 0u);
+    } else {
+      for (int g = 0; g < a.groups; g += 8) {
+        uint32_t o[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) o[u] = __shfl(score, ((g + u) << gs) & (L - 1), L);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) above += g + u < a.groups && (o[u] > score || (o[u] == score && g + u < g0));
+      }
     }
+    const bool stays = is && above < a.used;
+    // The worst that stays against the best that goes; a group with one
+    // expert left has no sum of two places.
+    const uint32_t worst = ~umax_l<L>(stays ? ~score : 0u), best = umax_l<L>(is && !stays ? score : 0u);
+    open = open || (odd < kOne && a.per > 1) || (a.used < a.groups && worst - best < group_gap);
+    const uint64_t all = __ballot(stays && l == g0 << gs);
+    const uint64_t mask = L == 64 ? all : (all >> ((threadIdx.x & 63) / L * L)) & ((1ull << (L & 63)) - 1);
+    keep = (uint32_t)mask;
+    keep2 = (uint32_t)(mask >> 32);
+  }
+  if constexpr (!BIAS) {
+    // By the logits.
+    if constexpr (kRaw16) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        // A bf16 or fp16 value in order: its binary32 bits, 16 of them
+        // (fp16: 19 hold its sign, exponent and fraction); -0 ties with 0.
+        constexpr int kDrop = DT == 0 ? 16 : 13;
+        const uint32_t f = __builtin_bit_cast(uint32_t, x[v] + 0.0f);
+        const uint32_t o = (f ^ (uint32_t)((int32_t)f >> 31 | (int32_t)0x80000000)) >> kDrop;
+        q[v] = (v * L < rest && x[v] > -kInf ? (o + 1) << kIdx : 0u) + code[v];
+      }
+    } else {
+      float hi = -kInf;
+#pragma unroll
+      for (int v = 0; v < V; ++v) hi = fmaxf(hi, v * L < rest ? x[v] : -kInf);
+      hi = max_l<L>(hi);
+      open = open || hi == kInf;
+      const float lo = hi == kInf || hi == -kInf ? 0.0f : hi - 32.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const uint32_t place = (uint32_t)fminf(fmaxf((x[v] - lo) * (kPlaces / 32.0f), 0.0f), kPlaces);
+        q[v] = (v * L < rest && x[v] > -kInf ? (place + 1) << kIdx : 0u) + code[v];
+      }
+    }
+  }
+  if (grouped) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int g = GROUPS == kRuns ? __popc(a.ends & ((1u << v) - 1)) : group_of(a, v * L + l) << a.shift;
+      const uint32_t word = L == 64 && g >= 32 ? keep2 : keep;
+      q[v] = (word >> (g & 31)) & 1 ? q[v] : code[v];
+    }
+  }
+  // The k best and the one or two behind them, in falling order (all V L
+  // numbers are distinct, and there are more of them); mine: the l-th;
+  // step: the least step down between the first k + 1, last: the one
+  // after.
+  uint32_t mine32 = 0, cur = 0x7fffffffu, step = ~0u, last = ~0u;
+  for (int j = 0; j < a.picks; ++j) {
+    uint32_t next = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) next = max(next, q[v] - cur);
+    next = umax_l<L>(next) + cur;
+    step = j > 0 ? min(step, last) : step;
+    last = j > 0 ? cur - next : ~0u;
+    mine32 = l == j ? next : mine32;
+    cur = next;
+  }
+  int mine = mine32 < kOne ? -1 : (int)(kLow - (mine32 & kLow));
+  const size_t row = (size_t)(live ? t : 0) * a.ld;
+  if (!kRaw16 || grouped) {
+    // (A step of whole places differs from that of keys by less than one.)
+    const uint32_t least_step = kRaw16 ? 0u : gap + kOne;
+    const bool close = step < least_step, near = last < least_step;
+    // The k + 1 best are settled among themselves (a lane each) unless the
+    // next is close to them too; without lanes for that all keys are.
+    open = open || (near && (close || a.picks < a.k + 2)) || (close && a.picks < a.k + 2);
+    if (open || close) {
+      const double zd = SCORE == kSoftmax && scores ? exact_sum<L>(x, rest, m) : 1.0;
+      if (open) {
+        mine = exact_choice<DT, L, SCORE, BIAS>(a, row, m, zd, lds[tok], l);
+      } else {
+        const float xm = mine >= 0 && l <= a.k ? load_logit<DT>(a.logits, row + mine) : -kInf;
+        const double key = xm == -kInf ? -(double)kInf : BIAS ? exact_key<SCORE, BIAS>(a, xm, mine, m, zd) : (double)xm;
+        int above = 0;
+        for (int j = 0; j <= a.k; ++j) {
+          const double o = __shfl(key, j, L);
+          const int at = __shfl(mine, j, L);
+          above += o > key || (o == key && at < mine);
+        }
+        // (Missing choices, all -1, stay behind the others.)
+        int *order = (int *)lds[tok];
+        lds_order();
+        if (l <= a.k) order[l] = -1;
+        lds_order();
+        if (l <= a.k && mine >= 0) order[above] = mine;
+        lds_order();
+        mine = l <= a.k ? order[l] : -1;
+        lds_order();
+      }
+    }
+  }
+  if (l >= a.k) mine = -1;
+
+  // Lane j: its choice's score and weight.
+  float sc = 0.0f, w;
+  const float xs = mine >= 0 ? load_logit<DT>(a.logits, row + mine) : -kInf;
+  if constexpr (SCORE == kSoftmax) {
+    const float mm = a.renorm ? max_l<L>(xs) : m;
+    sc = mine >= 0 ? exp_below(xs, mm) : 0.0f;
+    w = a.renorm ? sc / (sum_l<L>(sc) + 1e-20f) : sc / z;
+  } else {
+    sc = mine >= 0 ? 1.0f / (1.0f + expf(-xs)) : 0.0f;
+    w = a.renorm ? sc / (sum_l<L>(sc) + 1e-20f) : sc;
+  }
+  if (live && l < a.k) {
+    a.weights[(size_t)t * a.k + l] = mine >= 0 ? w * a.scale : 0.0f;
+    a.ids[(size_t)t * a.k + l] = mine;
   }
 }
 
 template <int DT, int L, int V, int GROUPS>
 hipError_t launch_topk_lv(const Topk &t) {
   TopkArgs a{t.logits, t.bias, t.weights, t.ids, (int)t.T, (int)t.E, (int)t.ld, t.k, t.groups, t.used,
-             (int)(t.E / t.groups), t.renorm, t.k + 1, 1, 0, 0, 0, t.scale};
+             (int)(t.E / t.groups), t.renorm, t.k + 1, 0, 0, 0, t.scale};
   // (Where lanes are left for the k + 1 best, and keys are rounded.)
   if (t.k + 1 <= L && (t.dtype == 2 || t.bias)) a.picks = t.k + 2;
   while ((t.groups << (a.shift + 1)) <= L) ++a.shift;
   if (GROUPS == kRuns)
     for (int v = a.per / L - 1; v < V; v += a.per / L) a.ends |= 1u << v;
-  // Several tokens a lane, once that leaves four workgroups a CU: what holds
-  // for all tokens is worked out once.  (A resource spans below 2^31 bytes.)
   const int64_t tokens = 256 / L;
-  while (a.turns < 4 && t.T >= tokens * a.turns * 2 * 1024 &&
-         tokens * a.turns * 2 * t.ld * (t.dtype == 2 ? 4 : 2) < (1 << 30))
-    a.turns *= 2;
   // ceil(2^32 / per): exact quotients for experts below 2^16 (not for per = 1).
   a.per_magic = a.per > 1 ? (uint32_t)((0x100000000ull + (uint64_t)a.per - 1) / (uint64_t)a.per) : 0u;
   const bool bias = t.bias != nullptr;
-  const int64_t wgs = (t.T + tokens * a.turns - 1) / (tokens * a.turns);
+  const int64_t wgs = (t.T + tokens - 1) / tokens;
   if (wgs > (int64_t)(UINT32_MAX / 256)) return hipErrorInvalidConfiguration;
   const void *fn =
       t.score == kSoftmax ? (bias ? reinterpret_cast<const void *>(&topk_kernel<DT, L, V, kSoftmax, true, GROUPS>)
