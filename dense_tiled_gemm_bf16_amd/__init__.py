@@ -100,12 +100,11 @@ def _torch():
 
 
 def _stream_ptr(stream, device):
-    torch = _torch()
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
+        return _torch()._C._cuda_getCurrentRawStream(device.index)
+    if stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-    return ctypes.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
 
 
 def _same_device(**named):
@@ -122,6 +121,9 @@ def _call(fn, device, stream, *args):
     """Call a C entry point with the tensors' device current (the library
     sets up and launches on the current device) and check its status."""
     torch = _torch()
+    if device.type == "cuda" and torch.cuda.current_device() == device.index:
+        check(fn(*args, _stream_ptr(stream, device)))
+        return
     with torch.cuda.device(device):
         check(fn(*args, _stream_ptr(stream, device)))
 
