@@ -147,19 +147,29 @@ int gemm_epilogue(const tgemm_epilogue_args *p, hipStream_t stream) {
   if (gated && p->trans_a) return fail(TGEMM_EINVAL, "%s: a gated activation takes A stored M x K (trans_a 0)", fn);
   if (p->M == 0 || p->N == 0) return TGEMM_OK;
   const int64_t out_n = gated ? p->N / 2 : p->N;
+  // K is split where that pays and the workspace holds the sums (a forced tile
+  // other than 64 x 64 goes without).
+  int splits = ffn::epilogue_splits(p->trans_a != 0, p->trans_b != 0, p->M, p->N, p->K);
+  if (!p->workspace || (uint64_t)splits * (uint64_t)p->M * (uint64_t)p->N * 4u > p->workspace_bytes ||
+      (g_tile_m != 0 && g_tile_m != 64))
+    splits = 1;
   const Tensor t[] = {
       {"C", p->C, p->M, out_n, p->ldc, 2, true, true},
       {"preact", p->preact, p->M, p->N, p->ldp, 2, true, false},
+      {"workspace", splits > 1 ? p->workspace : nullptr, splits > 1, (int64_t)splits * p->M * p->N,
+       (int64_t)splits * p->M * p->N, 4, false, false},
       {"A", p->A, p->K == 0 ? 0 : p->trans_a ? p->K : p->M, p->trans_a ? p->M : p->K, p->lda, 2, true, true},
       {"B", p->B, p->K == 0 ? 0 : p->trans_b ? p->N : p->K, p->trans_b ? p->K : p->N, p->ldb, 2, true, true},
       {"bias", p->bias, 1, p->N, p->N, 2, true, false},
       {"residual", p->residual, p->M, out_n, p->ldr, 2, true, false}};
-  static const Same same[] = {{0, 5}};
-  rc = check(fn, t, 6, 2, same, 1);
+  static const Same same[] = {{0, 6}};
+  rc = check(fn, t, 7, 3, same, 1);
   if (rc != TGEMM_OK) return rc;
+  if (splits > 1 && misaligned(p->workspace)) return fail(TGEMM_EALIGN, "%s: workspace is not 16-byte aligned", fn);
   // (An empty K is never read: its operands need no pointer and no stride. One row needs no stride.)
-  const int64_t lda = p->K == 0 ? 0 : t[2].rows == 1 ? t[2].cols : p->lda;
-  const int64_t ldb = p->K == 0 ? 0 : t[3].rows == 1 ? t[3].cols : p->ldb;
+  const Tensor &ta = t[3], &tb = t[4];
+  const int64_t lda = p->K == 0 ? 0 : ta.rows == 1 ? ta.cols : p->lda;
+  const int64_t ldb = p->K == 0 ? 0 : tb.rows == 1 ? tb.cols : p->ldb;
   const uint64_t a_span = (p->trans_a ? (uint64_t)(p->K + 63) / 64 * 64 : (uint64_t)tgemm::kTileM) * (uint64_t)lda * 2;
   if (a_span > kOffsetLimit) return fail(TGEMM_ETOOBIG, "%s: A too large for 31-bit offsets", fn);
   rc = check_b(fn, p->trans_b != 0, gated, p->N, p->K, ldb);
@@ -183,8 +193,16 @@ int gemm_epilogue(const tgemm_epilogue_args *p, hipStream_t stream) {
   g.C = p->C;
   g.ldc = p->ldc;
   g.act = (int)p->act;
+  g.ws = static_cast<float *>(p->workspace);
+  g.splits = splits;
   g.stream = stream;
   return run_gemm(fn, g);
+}
+
+uint64_t tgemm_epilogue_workspace_bytes(int64_t trans_a, int64_t trans_b, int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || K <= 0 || M > INT32_MAX || N > INT32_MAX || K > INT32_MAX) return 0;
+  const int splits = ffn::epilogue_splits(trans_a != 0, trans_b != 0, M, N, K);
+  return splits > 1 ? (uint64_t)splits * (uint64_t)M * (uint64_t)N * 4u : 0;
 }
 
 uint64_t tgemm_epilogue_backward_workspace_bytes(int64_t M, int64_t N, int64_t groups) {

@@ -191,7 +191,7 @@ PyObject *none() {
 
 typedef PyObject *const *Args;
 
-// a, b, bias, act, residual, preact, out
+// a, b, bias, act, residual, preact, out, workspace
 PyObject *epilogue(Args o) {
   const Tensor &a = tensor(o[0], "a"), &b = tensor(o[1], "b");
   On on(a, "a");
@@ -230,6 +230,13 @@ PyObject *epilogue(Args o) {
   const Tensor out = on.out(o[6], "out", t, {p.M, F});
   p.ldc = on.mat(out, "out", t, p.M, F);
   p.C = ptr(out);
+  const uint64_t need = tgemm_epilogue_workspace_bytes(p.trans_a, p.trans_b, p.M, p.N, p.K);
+  Tensor ws;
+  if (need) {
+    ws = on.workspace(o[7], need);
+    p.workspace = ptr(ws);
+    p.workspace_bytes = (uint64_t)ws.nbytes();
+  }
   check(gemm_epilogue(&p, on.stream()));
   return wrap(out);
 }
@@ -556,7 +563,7 @@ PyObject *set_error(PyObject *, PyObject *cls) {
 }
 
 #define TGEMM_ENTRY(NAME, F, N) {NAME, (PyCFunction)(void (*)(void))&entry<F, N>, METH_FASTCALL, nullptr}
-PyMethodDef kMethods[] = {TGEMM_ENTRY("gemm_epilogue", epilogue, 7),
+PyMethodDef kMethods[] = {TGEMM_ENTRY("gemm_epilogue", epilogue, 8),
                           TGEMM_ENTRY("epilogue_backward", epilogue_backward, 8),
                           TGEMM_ENTRY("gemm_grouped", grouped, 8),
                           TGEMM_ENTRY("gemm_grouped_tn", grouped_tn, 4),

@@ -49,10 +49,39 @@ Shape pick_grouped(const Shape (&shapes)[NS], int64_t M, int64_t N, int64_t grou
   return best;
 }
 
+constexpr int kCus = 256;  // compute units of an MI355X: the rule holds also where no device is
+constexpr int kMostSplits = 16;
+
 }  // namespace
+
+// K is split where 64 x 64 tiles leave at least half the compute units idle
+// and K is deep: as many splits as fill them once, of 8 slices of 64 or more.
+// us, NT with bias, gelu and residual but where noted, unsplit -> split:
+//   M     N     K                          M    N     K
+//   48    2048  2048   8.4 -> 7.9 (4)      48   4096  2048, swiglu  8.0 -> 9.1 (4)
+//   256   1024  4096  12.0 -> 10.1 (4)     512  512   2048   8.0 -> 9.1 (4)
+//   553   896   4016  19.9 -> 16.2 (2)     24   1024  8192  20.1 -> 8.8 (16)
+//   512   512   8192  23.3 -> 13.8 (4)     704  704   8192  24.4 -> 18.7 (2)
+// more splits than fill the chip lose (704 x 704 x 8192: 3 take 24.2), and so
+// do any where more than half of it is busy (1138 x 736 x 7296: 24.7 -> 29.8).
+// At up to 16 rows NT the kernel for few rows splits K among its waves, and
+// this split beats it from deeper on (16 x 1024: 4096 9.8 -> 8.0, 8192 16.8 ->
+// 8.8; one row: 4096 7.2 -> 7.5, 8192 11.5 -> 8.3).
+int epilogue_splits(bool trans_a, bool trans_b, int64_t M, int64_t N, int64_t K) {
+  const int64_t tiles = ((M + 63) / 64) * ((N + 63) / 64), slices = (K + 63) / 64;
+  const bool rows = !trans_a && trans_b && M <= 16;
+  if (tiles == 0 || tiles * 2 > kCus || slices <= (rows ? 64 : 32)) return 1;
+  const int64_t n = std::min<int64_t>({kCus / tiles, slices / 8, kMostSplits});
+  const int64_t each = (slices + n - 1) / n;
+  return (int)((slices + each - 1) / each);
+}
 
 hipError_t launch_gemm(const Gemm &g) {
   int tm = g.tile_m, tn = g.tile_n;
+  if (g.splits > 1) {
+    const hipError_t e = g.dtype == 1 ? launch_split_f16(g) : launch_split_bf16(g);
+    return e != hipSuccess ? e : launch_join(g);
+  }
   if (tm == 0) {
     if (few_rows(g)) {
       tm = tn = 16;

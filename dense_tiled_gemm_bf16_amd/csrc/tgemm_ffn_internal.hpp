@@ -37,6 +37,8 @@ struct Gemm {
   const int32_t *rows;  // A's row of each, or nullptr (row r itself)
   int64_t src_rows;     // rows of A
   int64_t stride_b, stride_bias;
+  float *ws;  // dense: room for `splits` planes of M x N sums, or nullptr
+  int splits;
   hipStream_t stream;
   int cus;
   int tile_m, tile_n;  // forced tile (16 x 16: the kernel for few rows), or 0, 0
@@ -45,6 +47,11 @@ hipError_t launch_gemm(const Gemm &g);       // tgemm_ffn_gemm.hip
 hipError_t launch_gemm_bf16(const Gemm &g, int tm, int tn);  // tgemm_ffn_gemm_bf16.hip
 hipError_t launch_gemm_f16(const Gemm &g, int tm, int tn);   // tgemm_ffn_gemm_f16.hip
 hipError_t launch_rows(const Gemm &g);       // tgemm_ffn_rows.hip: few rows for each weight
+hipError_t launch_split_bf16(const Gemm &g);  // the K split's partial sums, then
+hipError_t launch_split_f16(const Gemm &g);
+hipError_t launch_join(const Gemm &g);        // tgemm_ffn_rowops.hip: their sum and the epilogue
+// Splits of K for a dense product (1: none).
+int epilogue_splits(bool trans_a, bool trans_b, int64_t M, int64_t N, int64_t K);
 bool tile_supported(const Gemm &g, int tm, int tn);
 
 // out[e] = X_e^T Y_e over the rows of group e: P x Q, both 16-bit.

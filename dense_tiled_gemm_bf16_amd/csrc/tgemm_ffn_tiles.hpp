@@ -563,6 +563,43 @@ hipError_t launch_tile(const Gemm &g) {
   return hipErrorInvalidValue;
 }
 
+// The K split: workgroup w computes tile w % tiles over its range of slices and
+// leaves its sums in plane w / tiles of the workspace.
+template <class T, int TM, int TN>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void split_kernel(const Args a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  TGEMM_FFN_SLOTS(TM, TN)
+  Kernel<T, TM, TN, true> k(a, slots);
+  k.run();
+#endif
+}
+
+template <class T, int TM, int TN>
+hipError_t launch_split_tile(const Gemm &g) {
+  Args a = gemm_args(g);
+  a.N = (int)g.N;  // the product's columns, gated or not
+  a.tiles_m = (int)((g.M + TM - 1) / TM);
+  a.tiles_n = (int)((g.N + TN - 1) / TN);
+  a.ws = g.ws;
+  a.kq = (a.ksteps + g.splits - 1) / g.splits;  // (epilogue_splits leaves no split empty)
+  a.splits = g.splits;
+  const int64_t wgs = (int64_t)a.tiles_m * a.tiles_n * a.splits;
+  if (!grid_ok(wgs)) return hipErrorInvalidConfiguration;
+  void *args[] = {&a};
+  return hipLaunchKernel(reinterpret_cast<const void *>(&split_kernel<T, TM, TN>), dim3((unsigned)wgs), dim3(kThreads),
+                         args, 0, g.stream);
+}
+
+template <int DT>
+hipError_t launch_split(const Gemm &g) {
+  const bool ak = !g.trans_a, bk = g.trans_b;
+  if (ak && bk) return launch_split_tile<Traits<DT, true, true>, 64, 64>(g);
+  if (ak) return launch_split_tile<Traits<DT, true, false>, 64, 64>(g);
+  if (bk) return launch_split_tile<Traits<DT, false, true>, 64, 64>(g);
+  return launch_split_tile<Traits<DT, false, false>, 64, 64>(g);
+}
+
 template <int DT, bool AK, bool BK>
 hipError_t launch_tiles(const Gemm &g, int tm, int tn) {
   using T = Traits<DT, AK, BK>;

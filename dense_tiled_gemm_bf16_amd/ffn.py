@@ -30,7 +30,8 @@ SCORES = {"softmax": 0, "sigmoid": 1}
 # The argument structs of include/tgemm_ffn.h, field by field in order: all
 # are 8 bytes ("scale" a double, the rest integers or pointers).
 _FIELDS = {
-    "gemm_epilogue": "dtype trans_a trans_b M N K A lda B ldb bias residual ldr preact ldp C ldc act",
+    "gemm_epilogue": "dtype trans_a trans_b M N K A lda B ldb bias residual ldr preact ldp C ldc act workspace "
+                     "workspace_bytes",
     "gemm_epilogue_backward": "dtype M N dout ldd preact ldp act dz ldz dbias groups offsets workspace "
                               "workspace_bytes",
     "gemm_grouped": "dtype trans_b R N K groups offsets rows src_rows A lda B ldb stride_b bias preact ldp C ldc act",
@@ -67,6 +68,8 @@ def lib() -> ctypes.CDLL:
     L.tgemm_ffn_last_error.restype = ctypes.c_char_p
     L.tgemm_ffn_set_tile.argtypes = [ctypes.c_int, ctypes.c_int]
     L.tgemm_ffn_set_tile.restype = ctypes.c_int
+    L.tgemm_epilogue_workspace_bytes.argtypes = [i64] * 5
+    L.tgemm_epilogue_workspace_bytes.restype = ctypes.c_uint64
     for f in (L.tgemm_epilogue_backward_workspace_bytes, L.tgemm_route_plan_workspace_bytes):
         f.argtypes = [i64, i64, i64]
         f.restype = ctypes.c_uint64
@@ -140,7 +143,7 @@ def _score(score):
     return code
 
 
-def gemm_epilogue(a, b, bias=None, act="none", residual=None, preact=None, out=None, stream=None):
+def gemm_epilogue(a, b, bias=None, act="none", residual=None, preact=None, out=None, workspace=None, stream=None):
     """act(a @ b + bias) + residual for 2-D bfloat16 or float16 CUDA tensors.
 
     a (M,K) and b (K,N) as in gemm(): row-major or the transpose of a row-major
@@ -148,8 +151,11 @@ def gemm_epilogue(a, b, bias=None, act="none", residual=None, preact=None, out=N
     "relu", "gelu" (erf), "gelu_tanh", "silu", or gated: "swiglu", "geglu"
     take b = [gate | up] and give (M, N/2) (a row-major then).  preact (M,N), if
     given, receives a @ b + bias for epilogue_backward.  residual may be out.
+    workspace: for a K split, tgemm_epilogue_workspace_bytes bytes (with less
+    there is none); allocated when None.
     """
-    return _call("gemm_epilogue", a, stream, a, b, bias, _act(act), residual, preact, out)
+    return _call("gemm_epilogue", a, stream, a, b, bias, _act(act), residual, preact, out,
+                 workspace)
 
 
 def epilogue_backward(dout, preact, act, offsets=None, want_dbias=True, dz=None, dbias=None, workspace=None,

@@ -70,6 +70,10 @@ TGEMM_API int tgemm_ffn_set_tile(int tile_m, int tile_n);
  * may be NULL.  The residual may be C itself (same pointer and stride).
  * preact, if not NULL, receives Z rounded to the element type, M x N (the
  * activation takes the sums before that rounding).
+ * workspace: few output tiles under a deep K leave most of the chip idle; with
+ * tgemm_epilogue_workspace_bytes(trans_a, trans_b, M, N, K) bytes of it
+ * (16-byte aligned; 0: it would not be used) K is split over several
+ * workgroups a tile.  With less, or NULL, it is not.
  * Limits: as gemm_bf16; gated with trans_b, (N / 2 + 256) ldb 2 < 2^31.
  */
 typedef struct {
@@ -86,8 +90,11 @@ typedef struct {
   void *C;
   int64_t ldc;
   int64_t act;
+  void *workspace;
+  uint64_t workspace_bytes;
 } tgemm_epilogue_args;
 TGEMM_API int gemm_epilogue(const tgemm_epilogue_args *args, hipStream_t stream);
+TGEMM_API uint64_t tgemm_epilogue_workspace_bytes(int64_t trans_a, int64_t trans_b, int64_t M, int64_t N, int64_t K);
 
 /*
  * The epilogue's backward pass: dZ = dC * act'(Z) (gated: dG = dC U act'(G),

@@ -116,6 +116,69 @@ def test_chosen_tiles():
 
 
 @pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("M,N,K,act", [(1, 24, 4168, "gelu"), (72, 264, 4200, "silu"), (40, 1040, 2056, "none"),
+                                       (553, 136, 2568, "relu"), (130, 272, 8200, "gelu_tanh")])
+def test_split_k(layout, M, N, K, act):
+    if layout[0] == "t":
+        M = (M + 7) // 8 * 8  # rows of an A stored K x M are 16-byte multiples
+    assert ffn.lib().tgemm_epilogue_workspace_bytes(layout[0] == "t", layout[1] == "t", M, N, K) > 0
+    run_epilogue(M, N, K, BF16, layout, act, seed=M)
+    run_epilogue(M, N, K, F16, layout, act, bias=False, residual=False, preact=False, seed=M + 9)
+
+
+@pytest.mark.parametrize("layout", ["nt", "nn"])
+@pytest.mark.parametrize("act", ref.GATED)
+@pytest.mark.parametrize("M,N,K", [(3, 16, 4168), (100, 1040, 2568), (989, 352, 2056)])
+def test_split_k_gated(layout, act, M, N, K):
+    assert ffn.lib().tgemm_epilogue_workspace_bytes(0, layout[1] == "t", M, N, K) > 0
+    run_epilogue(M, N, K, BF16, layout, act, seed=M)
+    run_epilogue(M, N, K, F16, layout, act, bias=False, residual=False, preact=False, seed=M + 9)
+
+
+def test_split_k_workspaces():
+    """The sums stay within the bytes asked for; with a byte less K is not
+    split; calls of two streams and a replayed graph have the same bits."""
+    M, N, K = 100, 264, 4168
+    a, b, r, bias = rand(1, M, K).cuda(), rand(2, N, K, scale=0.02).cuda(), rand(3, M, N).cuda(), rand(4, N).cuda()
+    need = ffn.lib().tgemm_epilogue_workspace_bytes(0, 1, M, N, K)
+    ws = torch.full((need + 256,), 77, dtype=torch.uint8, device="cuda")
+
+    def run(**kw):
+        return tg.gemm_epilogue(a, b.t(), bias=bias, act="silu", residual=r, **kw)
+
+    want = run()
+    assert torch.equal(run(workspace=ws[:need]), want)
+    torch.cuda.synchronize()
+    assert bool((ws[need:] == 77).all()) and not bool((ws[:need] == 77).all())
+    ws.fill_(77)
+    short = run(workspace=ws[:need - 1])
+    torch.cuda.synchronize()
+    assert bool((ws == 77).all())
+    for y in (want, short):
+        yr, ty, _, _ = ref.epilogue(a.cpu(), b.t().cpu(), bias.cpu(), "silu", r.cpu(), BF16)
+        ref.assert_near(y, yr, ty)
+    out = r.clone()
+    assert torch.equal(tg.gemm_epilogue(a, b.t(), bias=bias, act="silu", residual=out, out=out), want)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [run(stream=streams[i % 2]) for i in range(8)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want) for y in got)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = run()
+    for i in range(3):
+        a.copy_(rand(20 + i, M, K))
+        want = run()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want), i
+    with pytest.raises(tg.TgemmError, match="overlaps"):
+        run(workspace=b.view(torch.uint8).view(-1))  # (a's bytes are fewer than the sums take)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
 @pytest.mark.parametrize("M", [8, 200])
 def test_empty_k(layout, M):
     run_epilogue(M, 24, 0, BF16, layout, "gelu", seed=5)

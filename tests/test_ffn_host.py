@@ -64,6 +64,11 @@ def epi(**kw):
     return base
 
 
+def deep(**kw):
+    """A call whose K is split."""
+    return epi(K=8192, lda=8192, ldb=8192, workspace_bytes=1 << 20, **kw)
+
+
 @pytest.mark.parametrize("fields,code,word", [
     (epi(dtype=2), tg.EINVAL, "element type"), (epi(trans_a=2), tg.EINVAL, "trans_a"),
     (epi(M=-1), tg.EINVAL, "negative"), (epi(M=1 << 31), tg.ETOOBIG, "below 2^31"),
@@ -82,6 +87,9 @@ def epi(**kw):
     (epi(lda=1 << 23, ldb=64), tg.ETOOBIG, "A too large"), (epi(ldb=1 << 23), tg.ETOOBIG, "B too large"),
     (epi(act=5, N=1 << 22, ldb=512, ldc=1 << 21), tg.ETOOBIG, "B too large"),
     (epi(lda=1 << 31), tg.ETOOBIG, "stride of A"),
+    (deep(workspace=P[3] + 4), tg.EALIGN, "workspace"), (deep(workspace=P[0] + 4096), tg.EINVAL, "workspace overlaps A"),
+    (deep(workspace=P[2]), tg.EINVAL, "C overlaps workspace"),
+    (deep(workspace=P[4] + 64, residual=P[4], ldr=32), tg.EINVAL, "workspace overlaps residual"),
 ])
 def test_epilogue_refuses(fields, code, word):
     refused("gemm_epilogue", code, word, **fields)
@@ -95,6 +103,7 @@ def test_null_argument_structs_are_refused():
 
 def test_nothing_to_do_needs_no_device():
     assert call("gemm_epilogue", **epi(M=0, A=0, C=0)) == tg.OK
+    assert call("gemm_epilogue", **deep(M=0, A=0, C=0, workspace=P[3])) == tg.OK
     assert call("gemm_grouped", dtype=0, trans_b=1, R=0, N=32, K=64, groups=4) == tg.OK
     assert call("gemm_grouped", dtype=0, trans_b=1, R=8, N=32, K=64, groups=0) == tg.OK
     assert call("gemm_grouped_tn", dtype=0, R=8, P=0, Q=8, groups=2) == tg.OK
@@ -220,6 +229,16 @@ def test_set_tile_refuses_unknown_tiles():
 
 def test_workspace_sizes():
     L = ffn.lib()
+    epilogue = L.tgemm_epilogue_workspace_bytes
+    assert epilogue(0, 1, 16, 32, 8192) == 16 * 16 * 32 * 4
+    assert epilogue(0, 0, 72, 1024, 2056) == 4 * 72 * 1024 * 4    # 33 slices, 8 or more a split
+    assert epilogue(0, 0, 72, 1024, 2048) == 0                    # not deep enough
+    assert epilogue(0, 1, 16, 32, 4096) == 0                      # few rows split K by themselves
+    assert epilogue(1, 1, 16, 32, 4096) == 8 * 16 * 32 * 4
+    assert epilogue(0, 1, 1024, 576, 1 << 20) == 0                # enough tiles without
+    assert epilogue(0, 1, 1024, 512, 1 << 20) == 2 * 1024 * 512 * 4
+    assert epilogue(0, 1, 0, 32, 8192) == epilogue(0, 1, 16, -8, 8192) == epilogue(0, 1, 16, 1 << 31, 8192) == 0
+    assert epilogue(0, 1, 16, 32, 1 << 31) == 0
     assert L.tgemm_epilogue_backward_workspace_bytes(128, 64, 0) == 2 * 64 * 4
     assert L.tgemm_epilogue_backward_workspace_bytes(129, 64, 5) == (3 + 5) * 64 * 4
     assert L.tgemm_epilogue_backward_workspace_bytes(2, 64, 5) == (1 + 2) * 64 * 4
