@@ -23,9 +23,17 @@ namespace {
 // tiles 13.0; 16 rows 10.2 and 13.2; 32 rows 19.4 and 13.4).  Groups: up to 10
 // rows on average (64 experts of 2048 x 2048 gated: 3.5 rows 85 us, 64 x 64
 // tiles 104; 9.4 rows 118 and 122; 16 rows 145 and 124).
+// Not where 64 x 64 tiles are between half and all of one a compute unit, which
+// then stream the weights at the same rate with fewer fixed costs: 6 of 64
+// gated experts of 2048 x 2048 (192 tiles) 14.8 us and 12.7, 8 (256) 15.8 and
+// 13.9, but 4 (128) 9.9 and 11.1, 12 (384) 21.5 and 23.8; one weight, 16 rows of
+// 16384 x 4096 (256 tiles) 38.7 and 30.8, 16384 x 1024 10.4 and 8.9, but one
+// row of 16384 x 2048 15.9 and 17.5, so from more than 8 rows on.
 bool few_rows(const Gemm &g) {
-  if (g.trans_a || !g.trans_b) return false;
-  return g.groups ? g.M <= 10 * g.groups : g.M <= 16;
+  if (g.trans_a || !g.trans_b || g.M > (g.groups ? 10 * g.groups : 16)) return false;
+  if (g.groups == 0 && g.M <= 8) return true;
+  const int64_t tiles = (g.N + 63) / 64 * (g.groups ? std::min(g.groups, g.M) : 1);
+  return 2 * tiles <= g.cus || tiles > g.cus;
 }
 
 // The shape with the least estimated time (as pick_shape), over groups of any
@@ -62,15 +70,18 @@ constexpr int kMostSplits = 16;
 //   256   1024  4096  12.0 -> 10.1 (4)     512  512   2048   8.0 -> 9.1 (4)
 //   553   896   4016  19.9 -> 16.2 (2)     24   1024  8192  20.1 -> 8.8 (16)
 //   512   512   8192  23.3 -> 13.8 (4)     704  704   8192  24.4 -> 18.7 (2)
-// more splits than fill the chip lose (704 x 704 x 8192: 3 take 24.2), and so
-// do any where more than half of it is busy (1138 x 736 x 7296: 24.7 -> 29.8).
+// More splits than fill the chip lose (704 x 704 x 8192: 3 take 24.2), and so
+// do any where more than half of it is busy (1138 x 736 x 7296: 24.7 -> 29.8) or
+// where the tiles read memory as fast as it goes, which depends on the columns
+// and rows of a slice (K = 4096: 48 x 6144 gated 14.3 -> 13.9, 48 x 7168 14.6 ->
+// 14.6, 48 x 8192 gated 14.9 -> 15.9).
 // At up to 16 rows NT the kernel for few rows splits K among its waves, and
 // this split beats it from deeper on (16 x 1024: 4096 9.8 -> 8.0, 8192 16.8 ->
 // 8.8; one row: 4096 7.2 -> 7.5, 8192 11.5 -> 8.3).
 int epilogue_splits(bool trans_a, bool trans_b, int64_t M, int64_t N, int64_t K) {
   const int64_t tiles = ((M + 63) / 64) * ((N + 63) / 64), slices = (K + 63) / 64;
   const bool rows = !trans_a && trans_b && M <= 16;
-  if (tiles == 0 || tiles * 2 > kCus || slices <= (rows ? 64 : 32)) return 1;
+  if (tiles == 0 || tiles * 2 > kCus || M + N > 28 * kCus || slices <= (rows ? 64 : 32)) return 1;
   const int64_t n = std::min<int64_t>({kCus / tiles, slices / 8, kMostSplits});
   const int64_t each = (slices + n - 1) / n;
   return (int)((slices + each - 1) / each);

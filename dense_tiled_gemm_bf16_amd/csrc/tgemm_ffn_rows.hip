@@ -260,20 +260,25 @@ hipError_t launch_one(const Gemm &g) {
   return hipLaunchKernel(fn, dim3((unsigned)wgs), dim3(64 * W), args, 0, g.stream);
 }
 
+// Weight rows that are read, if every row of A hits another group.
+int64_t weight_rows(const Gemm &g) { return g.N * (g.groups ? std::min(g.groups, g.M) : 1); }
+
 template <int DT, int W>
 hipError_t launch_waves(const Gemm &g) {
   if (is_gated(g.act)) return launch_one<DT, W, 2, true>(g);
   // One block of 16 columns a workgroup while that leaves no more than two
-  // workgroups a CU.
-  return (g.N + 15) / 16 * std::max<int64_t>(g.groups, 1) <= 2 * g.cus ? launch_one<DT, W, 1, false>(g)
-                                                                       : launch_one<DT, W, 2, false>(g);
+  // workgroups a CU (2 of 16 experts of 2048 x 1536: 5.3 us, with two blocks
+  // 5.9; 16 of 64 of 2048 x 1024: 17.2 and 13.5).
+  return weight_rows(g) <= 32 * g.cus ? launch_one<DT, W, 1, false>(g) : launch_one<DT, W, 2, false>(g);
 }
 
 template <int DT>
 hipError_t launch_dt(const Gemm &g) {
-  // Eight waves hold a CU's registers to themselves; with a short K four do,
-  // and more workgroups share it.
-  return g.K > 2048 ? launch_waves<DT, 8>(g) : launch_waves<DT, 4>(g);
+  // Eight waves a workgroup over a deep K of many weight rows, else four and
+  // more workgroups a CU.  One row, us with 4 and 8 waves: 32768 x 4096 64.3 and
+  // 56.3, 32768 x 2048 29.6 and 27.4, 32768 x 1024 15.4 and 15.9, 8192 x 4096
+  // 16.0 and 17.0; 64 gated experts of 2048 x 2048 114 and 100.
+  return g.K >= 2048 && weight_rows(g) > 32 * g.cus ? launch_waves<DT, 8>(g) : launch_waves<DT, 4>(g);
 }
 
 }  // namespace
