@@ -73,11 +73,21 @@ int check(const char *fn, const Tensor *t, int n, int outs, const Same *same = n
 
 bool bad16(int64_t dtype) { return dtype != TGEMM_DT_BF16 && dtype != TGEMM_DT_F16; }
 
+// Sizes leave the kernels' 32-bit indexes room for one step past the end.
+constexpr int64_t kSizeLimit = (int64_t)INT32_MAX - 4095;
+// The kernels look up their group among all of them, and each chunk of a plan
+// adds the counts of all the others: more would take seconds.
+constexpr int64_t kMostGroups = 65536, kMostChoices = (int64_t)1 << 26;
+
 int sizes(const char *fn, const int64_t *v, int n) {
   for (int i = 0; i < n; ++i)
     if (v[i] < 0) return fail(TGEMM_EINVAL, "%s: negative size (%lld)", fn, (ll)v[i]);
   for (int i = 0; i < n; ++i)
-    if (v[i] > INT32_MAX) return fail(TGEMM_ETOOBIG, "%s: sizes must be below 2^31 (%lld)", fn, (ll)v[i]);
+    if (v[i] >= kSizeLimit) return fail(TGEMM_ETOOBIG, "%s: sizes must be below 2^31 - 4096 (%lld)", fn, (ll)v[i]);
+  return TGEMM_OK;
+}
+int check_groups(const char *fn, int64_t groups) {
+  if (groups > kMostGroups) return fail(TGEMM_ETOOBIG, "%s: groups=%lld must be at most 65536", fn, (ll)groups);
   return TGEMM_OK;
 }
 
@@ -217,6 +227,7 @@ int gemm_epilogue_backward(const tgemm_epilogue_backward_args *p, hipStream_t st
   if (bad16(p->dtype)) return fail(TGEMM_EINVAL, "%s: no element type %lld", fn, (ll)p->dtype);
   const int64_t v[] = {p->M, p->N, p->groups};
   int rc = sizes(fn, v, 3);
+  if (rc == TGEMM_OK) rc = check_groups(fn, p->groups);
   if (rc == TGEMM_OK) rc = check_act(fn, p->act, p->N);
   if (rc != TGEMM_OK) return rc;
   const bool gated = ffn::is_gated((int)p->act), none = p->act == TGEMM_ACT_NONE;
@@ -253,6 +264,7 @@ int gemm_grouped(const tgemm_grouped_args *p, hipStream_t stream) {
   if (p->trans_b != 0 && p->trans_b != 1) return fail(TGEMM_EINVAL, "%s: trans_b must be 0 or 1", fn);
   const int64_t v[] = {p->R, p->N, p->K, p->groups, p->src_rows};
   int rc = sizes(fn, v, 5);
+  if (rc == TGEMM_OK) rc = check_groups(fn, p->groups);
   if (rc == TGEMM_OK) rc = check_act(fn, p->act, p->N);
   if (rc != TGEMM_OK) return rc;
   const bool gated = ffn::is_gated((int)p->act);
@@ -317,6 +329,7 @@ int gemm_grouped_tn(const tgemm_grouped_tn_args *p, hipStream_t stream) {
   if (bad16(p->dtype)) return fail(TGEMM_EINVAL, "%s: no element type %lld", fn, (ll)p->dtype);
   const int64_t v[] = {p->R, p->P, p->Q, p->groups};
   int rc = sizes(fn, v, 4);
+  if (rc == TGEMM_OK) rc = check_groups(fn, p->groups);
   if (rc != TGEMM_OK) return rc;
   if (p->P == 0 || p->Q == 0 || p->groups == 0) return TGEMM_OK;
   if (p->groups * p->P > INT32_MAX) return fail(TGEMM_ETOOBIG, "%s: groups * P must be below 2^31", fn);
@@ -351,7 +364,7 @@ static int check_route(const char *fn, int64_t dtype, int64_t T, int64_t E, int6
   if (renorm != 0 && renorm != 1) return fail(TGEMM_EINVAL, "%s: renormalize must be 0 or 1", fn);
   if (E < 1 || E > 1024) return fail(TGEMM_EINVAL, "%s: E=%lld must be 1 .. 1024", fn, (ll)E);
   if (k < 1 || k > 64 || k > E) return fail(TGEMM_EINVAL, "%s: k=%lld must be 1 .. 64 and at most E", fn, (ll)k);
-  if (T * k > INT32_MAX) return fail(TGEMM_ETOOBIG, "%s: T k must be below 2^31", fn);
+  if (T * k >= kSizeLimit) return fail(TGEMM_ETOOBIG, "%s: T k must be below 2^31 - 4096", fn);
   return TGEMM_OK;
 }
 
@@ -407,7 +420,8 @@ int route_topk_backward(const tgemm_route_backward_args *p, hipStream_t stream) 
 }
 
 uint64_t tgemm_route_plan_workspace_bytes(int64_t T, int64_t k, int64_t E) {
-  if (T <= 0 || k <= 0 || E <= 0 || E > 1024 || T > INT32_MAX || k > INT32_MAX || T * k > INT32_MAX) return 0;
+  if (T <= 0 || k <= 0 || E <= 0 || E > 1024 || T > kMostChoices || k > kMostChoices || T * k > kMostChoices)
+    return 0;
   return (uint64_t)ffn::plan_ws_ints(T * k, E) * 4u;
 }
 
@@ -420,7 +434,7 @@ int route_plan(const tgemm_route_plan_args *p, hipStream_t stream) {
   if (rc != TGEMM_OK) return rc;
   if (p->E < 1 || p->E > 1024) return fail(TGEMM_EINVAL, "%s: E=%lld must be 1 .. 1024", fn, (ll)p->E);
   if (p->k < 1) return fail(TGEMM_EINVAL, "%s: k=%lld must be at least 1", fn, (ll)p->k);
-  if (p->T * p->k > INT32_MAX) return fail(TGEMM_ETOOBIG, "%s: T k must be below 2^31", fn);
+  if (p->T * p->k > kMostChoices) return fail(TGEMM_ETOOBIG, "%s: T k must be at most 2^26", fn);
   const uint64_t need = tgemm_route_plan_workspace_bytes(p->T, p->k, p->E);
   const Tensor t[] = {{"offsets", p->offsets, 1, p->E + 1, p->E + 1, 4, false, true},
                       {"rows", p->rows, p->T, p->k, p->k, 4, false, true},
@@ -465,7 +479,7 @@ int expert_combine(const tgemm_expert_combine_args *p, hipStream_t stream) {
   const int64_t v[] = {p->T, p->D, p->R, p->k};
   int rc = sizes(fn, v, 4);
   if (rc != TGEMM_OK || p->T == 0 || p->D == 0) return rc;
-  if (p->T * p->k > INT32_MAX) return fail(TGEMM_ETOOBIG, "%s: T k must be below 2^31", fn);
+  if (p->T * p->k >= kSizeLimit) return fail(TGEMM_ETOOBIG, "%s: T k must be below 2^31 - 4096", fn);
   const Tensor t[] = {{"out", p->out, p->T, p->D, p->ldo, 2, true, true},
                       {"h", p->h, p->k == 0 ? 0 : p->R, p->D, p->ldh, 2, true, true},
                       {"slots", p->slots, p->T, p->k, p->k, 4, false, true},
@@ -488,7 +502,7 @@ int expert_combine_backward(const tgemm_expert_combine_backward_args *p, hipStre
   const int64_t v[] = {p->T, p->D, p->R, p->k};
   int rc = sizes(fn, v, 4);
   if (rc != TGEMM_OK || p->T == 0 || p->k == 0) return rc;
-  if (p->T * p->k > INT32_MAX) return fail(TGEMM_ETOOBIG, "%s: T k must be below 2^31", fn);
+  if (p->T * p->k >= kSizeLimit) return fail(TGEMM_ETOOBIG, "%s: T k must be below 2^31 - 4096", fn);
   const Tensor t[] = {{"dh", p->dh, p->R, p->D, p->ldg, 2, true, true},
                       {"dweights", p->dweights, p->T, p->k, p->k, 4, false, true},
                       {"dout", p->dout, p->T, p->D, p->ldd, 2, true, true},

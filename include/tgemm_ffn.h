@@ -19,7 +19,9 @@
  * TGEMM_DT_F32.  Sums are held in 32 bits; each output is rounded once, to
  * nearest even.  16-bit tensors are 16-byte aligned with row strides and
  * contiguous dimensions that are multiples of 8 (TGEMM_EALIGN otherwise).
- * An output may overlap no other argument, except where said.
+ * An output may overlap no other argument, except where said.  Sizes (and T k)
+ * are below 2^31 - 4096, row strides below 2^31, row groups at most 65536
+ * (TGEMM_ETOOBIG otherwise).
  *
  * Row groups: offsets is a device array of groups + 1 int32, and group e is
  * the rows offsets[e] .. offsets[e + 1] - 1 (none if that is empty).  The
@@ -231,7 +233,7 @@ TGEMM_API int route_topk_backward(const tgemm_route_backward_args *args, hipStre
  * int32) the token of each row (-1 behind the last), slots (T x k int32) the
  * row of each choice (-1 for an id outside 0 .. E - 1, which has none).
  * workspace: tgemm_route_plan_workspace_bytes(T, k, E) bytes, 16-byte
- * aligned (may be NULL if 0).  Limits: E <= 1024, T k < 2^31.
+ * aligned (may be NULL if 0).  Limits: E <= 1024, T k <= 2^26.
  */
 typedef struct {
   int64_t T, k, E;

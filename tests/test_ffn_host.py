@@ -193,6 +193,37 @@ def test_route_topk_refuses(fields, code, word):
     refused("route_topk", code, word, **fields)
 
 
+BIG = (1 << 31) - 4096  # (a multiple of 8)
+
+
+def test_sizes_leave_room_for_32_bit_indexes():
+    """The first size past the limit is refused; the last before it gets to
+    the next check."""
+    for size in (BIG, (1 << 31) - 8):
+        for name, fields in (("gemm_epilogue", epi(M=size)), ("gemm_epilogue", epi(N=size)),
+                             ("gemm_epilogue", epi(K=size)), ("gemm_epilogue_backward", bwd(M=size)),
+                             ("gemm_epilogue_backward", bwd(N=size)), ("gemm_grouped", grp(R=size)),
+                             ("gemm_grouped", grp(rows=P[6], src_rows=size)), ("gemm_grouped_tn", tn(R=size)),
+                             ("expert_gather", dict(R=8, D=size, src_rows=8, x=P[0], ldx=64, rows=P[1], out=P[2])),
+                             ("expert_combine", dict(dtype=0, T=1, D=8, R=1, k=size)),
+                             ("expert_combine_backward", dict(dtype=0, T=1, D=size, R=1, k=1))):
+            refused(name, tg.ETOOBIG, "sizes must be", **fields)
+    refused("expert_combine", tg.ETOOBIG, "T k", dtype=0, T=2, D=8, R=1, k=BIG // 2)
+    refused("expert_gather", tg.EINVAL, "out is NULL", R=8, D=BIG - 8, src_rows=8, x=P[0], ldx=BIG, rows=P[1], out=0)
+
+
+def test_groups_and_choices_are_limited():
+    refused("gemm_grouped", tg.ETOOBIG, "65536", **grp(groups=65537))
+    refused("gemm_grouped", tg.EINVAL, "C is NULL", **grp(groups=65536, C=0))
+    refused("gemm_grouped_tn", tg.ETOOBIG, "65536", **tn(groups=65537))
+    refused("gemm_epilogue_backward", tg.ETOOBIG, "65536", **bwd(groups=65537, offsets=P[5]))
+    plan = dict(T=(1 << 26) + 1, k=1, E=8, ids=P[0], offsets=P[1], rows=P[2], slots=P[3], workspace=P[4])
+    refused("route_plan", tg.ETOOBIG, "T k", **plan)
+    refused("route_plan", tg.EINVAL, "workspace bytes", **{**plan, "T": 1 << 26})
+    assert ffn.lib().tgemm_route_plan_workspace_bytes(1 << 26, 1, 8) == (1 << 14) * 8 * 4
+    assert ffn.lib().tgemm_route_plan_workspace_bytes((1 << 26) + 1, 1, 8) == 0
+
+
 def test_other_calls_refuse():
     r = dict(dtype=0, T=8, E=64, logits=P[0], ld=64, ids=P[1], dweights=P[2], k=4, scale=1.0, dlogits=P[3], ldo=64)
     refused("route_topk_backward", tg.EINVAL, "dlogits is NULL", **{**r, "dlogits": 0})
