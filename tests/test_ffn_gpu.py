@@ -547,6 +547,20 @@ def expert_inputs(dtype, T, E, D, H, act, seed=0):
             rand(seed + 3, E, N, dtype=dtype), rand(seed + 4, E, D, H, dtype=dtype, scale=0.09), rand(seed + 5, T, D, dtype=dtype))
 
 
+@pytest.mark.parametrize("counts,N,K", [([1, 0, 2, 0, 0, 3, 1, 1], 2048, 136), ([2, 1, 1], 4096, 2056), ([1] * 24, 2048, 200),
+                                        ([3, 0, 1, 0], 272, 2048)])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_grouped_few_rows_by_choice(counts, N, K, act):
+    """Numbers of experts hit that take 64 x 64 tiles, and the kernel for few
+    rows with four and with eight waves, by the library's own choice."""
+    run_grouped(counts, N, K, BF16, True, act, True, seed=len(counts))
+
+
+@pytest.mark.parametrize("M,N,K", [(16, 16384, 64), (9, 10240, 136), (8, 10240, 136), (5, 8264, 2048), (2, 24, 2048)])
+def test_few_rows_by_choice(M, N, K):
+    run_epilogue(M, N, K, BF16, "nt", "silu", seed=M)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("act", ["gelu_tanh", "swiglu"])
 @pytest.mark.parametrize("T,E,k", [(120, 5, 2), (3, 40, 3)])
@@ -572,6 +586,41 @@ def test_expert_layer_with_its_gradients(dtype, act, T, E, k):
                               ("dw2", w2.grad, 8), ("dlogits", logits.grad, 32)):
         close_on_the_whole(got[name], want, dtype, steps, name)
     assert torch.equal(got["fused"], got["h"]), "gathered rows give other results than their copies"
+
+
+def test_expert_layer_of_a_padded_batch():
+    """Tokens whose logits are all masked, tokens with one expert left, an
+    expert that nobody may choose, and memory that held NaN before: what has
+    no expert keeps its residual and has no gradient."""
+    T, E, k, D, H, act, dtype = 90, 6, 3, 72, 136, "swiglu", BF16
+    x, logits, w1, b1, w2, dy = expert_inputs(dtype, T, E, D, H, act, seed=7)
+    logits[:, 4] = -math.inf
+    logits[50:] = -math.inf
+    logits[60:] = float("nan")
+    logits[10:20, 1:] = -math.inf
+    nan = [torch.full((T * k, n), float("nan"), dtype=dtype, device="cuda") for n in (D, D, D, H, H, 2 * H, 2 * H)]
+    torch.cuda.synchronize()
+    del nan
+    got = expert_layer(*(t.cuda() for t in (x, logits, w1, b1, w2, dy)), k, act)
+    torch.cuda.synchronize()
+    xr, w1r, b1r, w2r = (t.double().requires_grad_() for t in (x, w1, b1, w2))
+    lr = torch.where(torch.isfinite(logits.double()), logits.double(), torch.zeros(())).requires_grad_()
+    _, ids = ref.topk(logits, k)
+    rows = []
+    for t in range(T):
+        y, chosen = xr[t], [int(e) for e in ids[t] if e >= 0]
+        if chosen:
+            v = torch.softmax(lr[t, chosen], 0)
+            y = y + sum(v[j] * (ref.layer(xr[t] @ w1r[e].t() + b1r[e], act) @ w2r[e].t()) for j, e in enumerate(chosen))
+        rows.append(y)
+    y = torch.stack(rows)
+    y.backward(dy.double())
+    for name, want, steps in (("y", y, 8), ("dx", xr.grad, 8), ("dw1", w1r.grad, 8), ("db1", b1r.grad, 8),
+                              ("dw2", w2r.grad, 8), ("dlogits", lr.grad, 32)):
+        close_on_the_whole(got[name], want, dtype, steps, name)
+    assert torch.equal(got["y"][50:].cpu(), x[50:]) and torch.equal(got["dx"][50:].cpu(), dy[50:])
+    assert not got["dlogits"][50:].any() and not got["dlogits"][:, 4].any()
+    assert not got["dw1"][4].any() and not got["db1"][4].any() and not got["dw2"][4].any()
 
 
 def test_the_same_inputs_give_the_same_bits():
