@@ -502,8 +502,9 @@ constexpr bool convert_ok(int pos, int J) {
 //    Tiles cover TN / 2 columns of each half; N is the columns of one half.
 //  * kGather: with `rows` given, row r of A is row rows[r] of the array at A
 //    (src_rows rows).
+//  * kPrefetch: 256-row tiles of K-contiguous operands prefetch into the L2.
 struct NoExt {
-  static constexpr bool kOn = false, kGated = false, kGather = false;
+  static constexpr bool kOn = false, kGated = false, kGather = false, kPrefetch = false;
 };
 
 template <class T, int TM, int TN, bool SPLIT = false, class EXT = NoExt>
@@ -577,7 +578,17 @@ struct Kernel {
   static constexpr bool kPfHead = kLastLoad >= kMfma;  // last load in the next slice's head
   static constexpr int kPfAt = kPfHead ? kLastLoad - kMfma + 1 : kLastLoad + 1;
   // (Not for fp6, which has its own K loop.)
-  static constexpr int kPfDist = T::kScaled && !T::kFp6 && !(T::kDt == kFp4 && T::kWholeK) ? 3 : 0;
+  // The feed-forward products of 256-row tiles (kPf16) prefetch as well: their
+  // operands come from memory, as in a model, where each layer has weights of
+  // its own, and a slice's loads have one slice (1.2 us) to land.  Inputs from
+  // memory: 4096 x 4096 x 8192 with gelu and residual 216 -> 201 us, 8192 x
+  // 2048 x 2048 72.0 -> 67.4 (2 slices ahead 217 and 72.4, 5 204 and 68.5);
+  // inputs left in the caches by the call before 191 -> 192.5 and 64.0 -> 65.2;
+  // a layer of 32 experts for 8192 tokens 809 -> 797.
+  // (Not with a K-major operand: 4000 x 3000 x 5000 NN 144.6 -> 146.5; with two
+  // the loaders leave no registers.)
+  static constexpr bool kPf16 = !T::kScaled && EXT::kPrefetch && kNS == 2 && T::kAK && T::kBK;
+  static constexpr int kPfDist = kPf16 || (T::kScaled && !T::kFp6 && !(T::kDt == kFp4 && T::kWholeK)) ? 3 : 0;
   static_assert(kPfDist == 0 || !kPfHead || kPfAt < kBarrierAt, "prefetch goes before the barrier it may pass");
   static_assert(kPfDist == 0 || kPfHead || kPfAt < kMfma, "prefetch position");
   static_assert(kPfDist == 0 || kFreeAt == kBarrierAt, "the prefetch placement assumes one barrier per slice");
@@ -967,12 +978,42 @@ struct Kernel {
     wait_vm_lgkm0<63>();
   }
 
+  // kPf16: the row whose line of each slice this lane prefetches.  Waves 0-1
+  // take an eighth of the A panel's rows (its share among the 8 tile columns of
+  // an XCD's block), waves 2-3 a quarter of B's (among the 4 tile rows); gathered
+  // rows and halves as the loaders take them.
+  __device__ __forceinline__ void prefetch_share(int tm, int tn) {
+    constexpr int kA = TM / 16, kB = TN / 8;  // rows of a wave
+    pf_off = kOOB;
+    if (wave < 2) {
+      const int s = kA * (2 * (tn & 7) + wave) + lane;
+      pf_rsrc = la.rsrc;
+      int row = lane < kA && m0 + s < a.M ? s : -1;
+      if constexpr (EXT::kGather)
+        if (x.rows && row >= 0) {
+          const int src = x.rows[m0 + s];
+          row = src < x.src_rows ? src : -1;
+        }
+      if (row >= 0) pf_off = (uint32_t)row * (uint32_t)a.lda * (uint32_t)kElem;
+    } else {
+      const int s = kB * (2 * (tm & 3) + wave - 2) + lane;
+      pf_rsrc = lb.rsrc;
+      const int c = EXT::kGated ? ((s >> 5) << 4) + (s & 15) : s;
+      int row = lane < kB && n0 + c < a.N ? c : -1;
+      if constexpr (EXT::kGated)
+        if (row >= 0 && ((s >> 4) & 1)) row += x.half;
+      if (row >= 0) pf_off = (uint32_t)row * (uint32_t)a.ldb * (uint32_t)kElem;
+    }
+  }
+
   // One dword of each 128-byte line of slice kt of this workgroup's share of
   // the A and B panels; out-of-range rows and slices past K load nothing.
   __device__ __forceinline__ void prefetch(int kt) {
     const bool ok = kt * kSliceK < kK;
+    // (kPf16: the uniform offset too stays inside the resource.)
+    const int ks = kPf16 && !ok ? 0 : kt;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(pf_rsrc, (LDS_AS void *)(slots.junk + wave * 256), 4,
-                                             ok ? pf_off : kOOB, (uint32_t)kt * T::kSliceBytes, 0, 0);
+                                             ok ? pf_off : kOOB, (uint32_t)ks * T::kSliceBytes, 0, 0);
   }
 
   // fp4, fp6: group g (chunks 2 g and 2 g + 1) of this wave's 128 rows into
@@ -1378,7 +1419,9 @@ struct Kernel {
       lb.init(a.B + ((size_t)n0 * a.ldb + k0) * kElem, min(a.N - n0, TN), K, a.ldb, kElem, kSliceK, wave, lane);
     else
       lb.init(a.B + (size_t)k0 * a.ldb * kElem, K, a.N, n0, a.ldb, wave, lane);
-    if constexpr (kPfDist > 0) {
+    if constexpr (kPf16) {
+      prefetch_share(m0 / TM, n0 / (EXT::kGated ? TN / 2 : TN));
+    } else if constexpr (kPfDist > 0) {
       // Waves 0-1 take 32 rows of the A panel (its share among the 8 tile
       // columns of an XCD's block), waves 2-3 take 64 rows of the B panel
       // (its share among the 4 tile rows).
