@@ -18,7 +18,9 @@ namespace {
 // A workgroup takes kGradRows rows of one group and 256 output columns: 32
 // threads of 8 columns side by side, 8 rows at a time.  Its column sums go to
 // a workspace row of their own, and a second kernel adds a group's rows in
-// order, so that the sums do not depend on timing (atomics would).
+// order, so that the sums do not depend on timing (atomics would).  dZ is
+// rounded once, to the type that the products behind it take.  4096 x 4096 of
+// gelu_tanh: 22.3 us for 100 MB (4.5 TB/s; a copy reaches 5.2), its sums 4.9 us.
 // ---------------------------------------------------------------------------
 struct GradArgs {
   const uint8_t *dout, *pre;
@@ -236,7 +238,10 @@ __global__ __launch_bounds__(256) void join_kernel(const JoinArgs a) {
 
 // ---------------------------------------------------------------------------
 // Rows to experts and back.  A wave takes one row (or 512 columns of one):
-// its index is the same for all lanes.
+// its index is the same for all lanes.  Rows of 2048 columns: 8192 gathered
+// from 4096 13.0 us (50 MB through memory and 17 again from the caches, 5.2
+// TB/s); 8192 tokens of 4 experts combined 28 us (168 MB, 6.0 TB/s, part of it
+// from the caches); the gradients of 4096 tokens of 2 experts 15.6 us (101 MB).
 // ---------------------------------------------------------------------------
 struct GatherArgs {
   const uint8_t *x;

@@ -4,9 +4,13 @@
 // (dense) or one weight for each group of rows (grouped), and the grouped
 // product over rows that gives each group's weight gradient.
 //
-// What bounds them is the K loop: a 256 x 256 tile at K = 4096 is 64 slices
-// of about 2 us each, and the epilogue's traffic (residual, values before
-// the activation) streams at the end of each tile.
+// What bounds them is the K loop: a 256 x 256 tile at K = 4096 is 64 slices of
+// about 1.2 us each, and the epilogue's traffic (residual, values before the
+// activation) streams at the end of each tile.  4096 x 4096 x 8192, inputs from
+// memory: 196 us with bias, gelu and residual (1.40 PFLOP/s), 185 without any
+// of them; the plain product 203, without the prefetch.  What the epilogue costs
+// there, inputs in the caches: through LDS 6 us, relu 3.5 more, gelu 8.5, the
+// residual 1.2, the values before the activation 1.5.
 //
 // The epilogue goes through LDS: the accumulators are indexed statically, so
 // work on them directly would be unrolled 512 times for every activation
