@@ -13,8 +13,9 @@
 // through the epilogue.
 //
 // Measured: one row of 4096 x 4096 with bias, silu and residual 8.0 us (33.5
-// MB, 4.2 TB/s); 37 tokens of 6 of 64 experts, 2048 x 2048 gated: 85 to 92 us
-// for 520 MB (5.7 to 6.1 TB/s), 2048 x 1024 42 to 45 us for 260 MB.
+// MB, 4.2 TB/s); 37 tokens of 6 of 64 experts, 53 of them hit, 2048 x 2048
+// gated: 85 to 92 us for 445 MB (4.8 to 5.2 TB/s, a copy's rate), 2048 x 1024 42
+// to 45 us for 222 MB.
 //
 // More rows would mean reading A's rows in every workgroup from the L2: with
 // 48 rows, 8192 columns, K = 4096 a form of this kernel with up to 64 rows took
