@@ -623,6 +623,48 @@ def test_expert_layer_of_a_padded_batch():
     assert not got["dw1"][4].any() and not got["db1"][4].any() and not got["dw2"][4].any()
 
 
+def test_offsets_past_32_bits():
+    """Outputs of more than 4 GiB: their last rows, and the moves between them."""
+    M, N, K = 262400, 8200, 64
+    x, w = rand(1, M, K), rand(2, 2, N, K, scale=0.1)
+    X, W = x.cuda(), w.cuda()
+    res, z, out = (torch.empty(M, N, dtype=BF16, device="cuda") for _ in range(3))
+    tail = rand(3, 70, N)
+    res[-70:] = tail.cuda()
+    assert out.numel() * 2 > 1 << 32
+    say("past 32 bits", M, N)
+    tg.gemm_epilogue(X, W[0].t(), act="relu", residual=res, preact=z, out=out)
+    torch.cuda.synchronize()
+    yr, ty, zr, tz = ref.epilogue(x[-70:], w[0].t(), None, "relu", tail, BF16)
+    ref.assert_near(out[-70:], yr, ty, "out")
+    ref.assert_near(z[-70:], zr, tz, "preact")
+    say("gradient")
+    dz, _ = tg.epilogue_backward(out, z, "relu", want_dbias=False, dz=res)
+    torch.cuda.synchronize()
+    assert torch.equal(dz[-70:], out[-70:] * (z[-70:] > 0))
+    say("grouped")
+    off = torch.tensor([0, M - 70, M], dtype=torch.int32, device="cuda")
+    tg.gemm_grouped(X, W.transpose(1, 2), off, act="relu", preact=z, out=out)
+    torch.cuda.synchronize()
+    yr, ty, zr, tz = ref.epilogue(x[-70:], w[1].t(), None, "relu", None, BF16)
+    ref.assert_near(out[-70:], yr, ty, "grouped out")
+    ref.assert_near(z[-70:], zr, tz, "grouped preact")
+    say("rows")
+    back = torch.arange(M - 1, -1, -1, dtype=torch.int32, device="cuda")
+    tg.expert_gather(out, back, out=z)
+    torch.cuda.synchronize()
+    assert torch.equal(z[:70], out[-70:].flip(0)) and torch.equal(z[-70:], out[:70].flip(0))
+    tg.expert_combine(z, back[:, None], out=res)
+    torch.cuda.synchronize()
+    assert torch.equal(res[-70:], out[-70:]) and torch.equal(res[:70], out[:70])
+    two = torch.full((M, 1), 2.0, device="cuda")
+    dh, dw = tg.expert_combine_backward(out, z, back[:, None], two, dh=res)
+    torch.cuda.synchronize()
+    assert torch.equal(dh[:70], 2 * out[-70:].flip(0)) and torch.equal(dh[-70:], 2 * out[:70].flip(0))
+    want = (out[-70:].double() ** 2).sum(1)   # sums of up to 8200 binary32 products, all positive
+    assert bool(((dw[-70:, 0].double() - want).abs() <= 8200 * 2.0 ** -24 * want + 1e-30).all())
+
+
 def test_the_same_inputs_give_the_same_bits():
     ins = [t.cuda() for t in expert_inputs(BF16, 300, 9, 136, 264, "swiglu", seed=3)]
     first = expert_layer(*ins, 2, "swiglu")

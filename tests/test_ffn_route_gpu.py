@@ -153,6 +153,29 @@ def test_many_tokens():
     assert float((w.sum(1) - 1).abs().max()) < 1e-6
 
 
+def test_logits_past_32_bits():
+    T, E, k = (1 << 24) + 21, 65, 3
+    tail = rand(1, 40, E)
+    x = torch.zeros(T, E, dtype=F32, device="cuda")
+    x[-40:] = tail.cuda()
+    assert x.numel() * 4 > 1 << 32
+    say("past 32 bits", T, E)
+    w, ids = tg.route_topk(x, k)
+    torch.cuda.synchronize()
+    wr, ir = ref.topk(tail, k)
+    assert torch.equal(ids[-40:].cpu().long(), ir)
+    assert float((w[-40:].cpu().double() - wr).abs().max()) < 1e-6
+    assert torch.equal(ids[:5].cpu().long(), torch.arange(k).expand(5, k))
+    g = torch.zeros(T, k, device="cuda")
+    g[-40:] = rand(2, 40, k).cuda()
+    d = tg.route_topk_backward(g, x, ids)
+    torch.cuda.synchronize()
+    t = tail.double().requires_grad_()
+    weights_of(t, ir, "softmax", True, 1.0).backward(g[-40:].cpu().double())
+    assert float((d[-40:].cpu().double() - t.grad).abs().max()) < 1e-6
+    assert not d[:1000].any()
+
+
 # --------------------------------------------------------------------------
 # The gradient
 # --------------------------------------------------------------------------
