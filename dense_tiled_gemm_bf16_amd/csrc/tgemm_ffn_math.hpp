@@ -78,7 +78,7 @@ __device__ __forceinline__ float sigmoid_(float z) { return __builtin_amdgcn_rcp
 template <int ACT>
 __device__ __forceinline__ float act_fwd(float z) {
   if constexpr (ACT == kRelu) {
-    return z > 0.0f ? z : (z != z ? z : 0.0f);
+    return z < 0.0f ? 0.0f : z;  // (NaN stays)
   } else if constexpr (ACT == kGelu || ACT == kGeglu) {
     const float q = exp_(-0.5f * z * z) * tail_shape(fabsf(z));
     return z * (z < 0.0f ? q : 1.0f - q);
