@@ -74,18 +74,28 @@ __device__ __forceinline__ float tail_shape(float x) {
 
 __device__ __forceinline__ float sigmoid_(float z) { return __builtin_amdgcn_rcpf(1.0f + exp_(-z)); }
 
+// Scales of exponents are folded into their polynomials: each instruction a value
+// is 0.9 us of a 4096 x 4096 output's epilogue.
+// exp(-z^2 / 2).
+__device__ __forceinline__ float bell(float z) { return __builtin_amdgcn_exp2f(z * -0.72134752044448170368f * z); }
+// sigmoid(2 u), u = sqrt(2 / pi) (z + 0.044715 z^3); zz = z^2.
+__device__ __forceinline__ float tanh_gate(float z, float zz) {
+  constexpr float c = (float)(-1.59576912160573071176 * 1.44269504088896340736);
+  constexpr float c3 = (float)(-1.59576912160573071176 * 1.44269504088896340736 * 0.044715);
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * fmaf(c3, zz, c)));
+}
+
 // act(z) of the activation ACT (the gated ones': of their gate).
 template <int ACT>
 __device__ __forceinline__ float act_fwd(float z) {
   if constexpr (ACT == kRelu) {
     return z < 0.0f ? 0.0f : z;  // (NaN stays)
   } else if constexpr (ACT == kGelu || ACT == kGeglu) {
-    const float q = exp_(-0.5f * z * z) * tail_shape(fabsf(z));
+    const float q = bell(z) * tail_shape(fabsf(z));
     return z * (z < 0.0f ? q : 1.0f - q);
   } else if constexpr (ACT == kGeluTanh) {
     // z (1 + tanh u) / 2 = z sigmoid(2 u).
-    const float u2 = 1.5957691216057308f * fmaf(0.044715f * z * z, z, z);
-    return z * sigmoid_(u2);
+    return z * tanh_gate(z, z * z);
   } else if constexpr (ACT == kSilu || ACT == kSwiglu) {
     return z * sigmoid_(z);
   } else {
@@ -100,14 +110,14 @@ __device__ __forceinline__ void act_both(float z, float &f, float &d) {
     f = act_fwd<kRelu>(z);
     d = z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
   } else if constexpr (ACT == kGelu || ACT == kGeglu) {
-    const float e = exp_(-0.5f * z * z);
+    const float e = bell(z);
     const float q = e * tail_shape(fabsf(z));
     const float cdf = z < 0.0f ? q : 1.0f - q;
     f = z * cdf;
     d = fmaf(z * 0.3989422804014327f, e, cdf);
   } else if constexpr (ACT == kGeluTanh) {
     const float zz = z * z;
-    const float s = sigmoid_(1.5957691216057308f * fmaf(0.044715f * zz, z, z));
+    const float s = tanh_gate(z, zz);
     f = z * s;
     // (Past |z| = 100 the derivative is 0 or 1; z^2 could overflow.)
     d = fmaf(f * (1.0f - s), 1.5957691216057308f * fmaf(0.134145f, fminf(zz, 1e4f), 1.0f), s);

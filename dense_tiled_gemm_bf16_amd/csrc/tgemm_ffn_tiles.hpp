@@ -9,7 +9,7 @@
 // activation) streams at the end of each tile.  4096 x 4096 x 8192, inputs from
 // memory: 196 us with bias, gelu and residual (1.40 PFLOP/s), 185 without any
 // of them; the plain product 203, without the prefetch.  What the epilogue costs
-// there, inputs in the caches: through LDS 6 us, relu 1.7 more, gelu 8.6 (about
+// there, inputs in the caches: through LDS 6 us, relu 1.7 more, gelu 8.2 (about
 // 0.9 for each VALU instruction a value), the residual 1.2, the values before the
 // activation 1.5.
 //
