@@ -153,6 +153,25 @@ def test_many_tokens():
     assert float((w.sum(1) - 1).abs().max()) < 1e-6
 
 
+@pytest.mark.parametrize("E,groups", [(64, 4), (48, 8), (480, 8)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_groups_whose_sums_nearly_tie(E, groups, score):
+    """Two groups whose scores agree to some 2^-24 at the cut, in both orders:
+    the sums in 64 bits decide."""
+    T, per = 60, E // groups
+    x = rand(1, T, E) - 6.0
+    f = torch.exp if score == "softmax" else torch.sigmoid
+    inverse = torch.log if score == "softmax" else torch.logit
+    a = rand(2, T, 2).double() * 0.3
+    b = a[:, 0] - 0.2
+    rest = inverse(f(a[:, 0]) + f(a[:, 1]) - f(b))
+    for t in range(T):
+        first, second = (0, 2) if t % 2 else (2, 0)
+        x[t, first * per:first * per + 2] = a[t].float()
+        x[t, second * per + 1], x[t, second * per + 3] = float(b[t]), float(rest[t])
+    check_topk(x, 2, score=score, groups=groups, groups_used=1)
+
+
 def test_logits_past_32_bits():
     T, E, k = (1 << 24) + 21, 65, 3
     tail = rand(1, 40, E)
