@@ -294,8 +294,8 @@ __global__ __launch_bounds__(256, 4) void topk_kernel(const TopkArgs a) {
                                                     (uint32_t)min(left * (int64_t)sizeof(Raw), (int64_t)0x7fffffff), 0x00020000);
 
   // Per expert: `code`, its index as the low bits of a key; `shift`, its place
-  // with a score of 0 (its bias; from 1 on), or far below 0 if it is none or its
-  // bias bars it.
+  // with a score of 0 (its bias; from 1 on), or so far below 0 if it is none or
+  // its bias bars it that a score of up to 1 leaves it there.
   const bool grouped = GROUPS == kRuns || (GROUPS == kAnyGroups && a.groups > 1);
   const bool scores = BIAS || grouped;
   uint32_t code[V];
@@ -357,10 +357,13 @@ __global__ __launch_bounds__(256, 4) void topk_kernel(const TopkArgs a) {
     z = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      // (Experts whose bias bars them stay in the sum.)
+      // (Experts whose bias bars them stay in the sum.  Past the last expert
+      // x is another row's or a gap's, and its exponential has no bound: no
+      // score there, or it would outweigh any shift.)
       const float w = x[v] == m ? 1.0f : exp_(x[v] - m);
-      z += v * L < rest && x[v] > -kInf ? w : 0.0f;
-      s[v] = x[v] > -kInf ? w : __builtin_nanf("");
+      const bool is = v * L < rest && x[v] > -kInf;
+      z += is ? w : 0.0f;
+      s[v] = is ? w : __builtin_nanf("");
     }
     z = sum_l<L>(z);
   } else if (SCORE == kSigmoid && scores) {

@@ -117,6 +117,58 @@ def test_masked_logits():
     check_topk(rand(2, 9, 48), 48, bias=bias, score="sigmoid")
 
 
+# Shifts of neighbouring rows: a softmax does not know a row's shift, so its
+# choice has to stand beside any other row.
+SHIFTS = torch.tensor([0.0, -6.0, -8.0, 5.0, -10.0, 0.0, -12.0, -20.0, 3.0, -200.0])
+
+
+def check_shifted(x, k, **how):
+    w, ids = check_topk(x, k, **how)
+    assert bool(((ids >= 0) & (ids < x.shape[1])).all())
+    return w, ids
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("E,groups,used,ks", [(48, 1, 1, (1, 6, 20)), (96, 1, 1, (4, 17)), (97, 1, 1, (8,)), (100, 1, 1, (8, 30)),
+                                              (127, 1, 1, (3,)), (160, 1, 1, (6,)), (250, 1, 1, (16, 17)), (300, 1, 1, (4,)),
+                                              (385, 1, 1, (8,)), (1000, 1, 1, (8,)), (48, 3, 2, (4,)), (96, 6, 3, (6,)),
+                                              (100, 20, 5, (8,)), (250, 10, 4, (8,)), (300, 60, 7, (9,)), (320, 64, 5, (8,)),
+                                              (576, 64, 64, (8,)), (1000, 8, 3, (8,))])
+def test_rows_of_different_scale_with_a_bias(dtype, E, groups, used, ks):
+    """Numbers of experts that leave lanes over, between rows whose logits lie
+    far above or below, in the last row, and in a row by itself."""
+    x = (rand(E, 30, E) + SHIFTS.repeat(3)[:, None]).to(dtype)
+    bias = rand(4, E, scale=0.1)
+    for k in ks:
+        for renorm in (True, False):
+            check_shifted(x, k, bias=bias, groups=groups, groups_used=used, renormalize=renorm)
+        check_shifted(x, k, bias=torch.zeros(E), groups=groups, groups_used=used)
+        check_shifted(x[4:5], k, bias=bias, groups=groups, groups_used=used)
+        check_shifted(x, k, score="sigmoid", bias=bias, groups=groups, groups_used=used)
+        check_shifted(x, k, groups=groups, groups_used=used, renormalize=False)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,used", [(48, 1, 1), (97, 1, 1), (300, 1, 1), (100, 20, 5), (320, 64, 5)])
+def test_a_biased_choice_beside_finite_padding(score, E, groups, used):
+    """Columns of a larger array whose other columns hold large numbers, and
+    rows that are all masked between rows that are not."""
+    x = rand(E, 21, E) + SHIFTS.repeat(3)[:21, None]
+    x[3], x[11], x[20] = -math.inf, float("nan"), -math.inf
+    bias = rand(4, E, scale=0.1)
+    how = dict(score=score, bias=bias, groups=groups, groups_used=used)
+    wr, ir = ref.topk(x, 6, score, bias, groups, used)
+    for pad in (60.0, 3e38, math.inf):
+        big = torch.full((21, E + 64), pad, device="cuda")
+        big[:, 8:8 + E] = x.cuda()
+        say("padding", score, E, groups, pad)
+        w, ids = tg.route_topk(big[:, 8:8 + E], 6, **{**how, "bias": bias.cuda()})
+        torch.cuda.synchronize()
+        assert torch.equal(ids.cpu().long(), ir)
+        ref.assert_near(w, wr, WEIGHT * wr.abs() + 2.0 ** -126, "weights")
+        check_topk(x, 6, **how)
+
+
 def test_rows_of_a_larger_array():
     big = torch.full((9, 60), float("nan"), device="cuda")
     x = rand(1, 9, 41)
