@@ -92,6 +92,23 @@ def source_of(kind: str) -> str:
     return QUANT_SRC if kind == "quant_mxfp8" else KERNEL_SRC
 
 
+def with_headers(src: str) -> list[str]:
+    """A source and the headers beside it that it includes, directly or not,
+    in the order they are met."""
+    import re
+    seen, todo = [], [src]
+    while todo:
+        path = os.path.normpath(todo.pop(0))
+        if path in seen:
+            continue
+        seen.append(path)
+        for name in re.findall(r'^\s*#include\s+"([^"]+)"', open(path).read(), re.M):
+            header = os.path.join(os.path.dirname(path), name)
+            if os.path.dirname(os.path.normpath(header)) == os.path.dirname(path):
+                todo.append(header)
+    return seen
+
+
 def traffic_file(name: str) -> str:
     return os.path.join(ROOT, "profiles", f"traffic_{name}.json")
 
@@ -100,12 +117,12 @@ def log(*a):
     print(*a, file=sys.stderr, flush=True)
 
 
-def kernel_source_hash(text: str | None = None, src: str = KERNEL_SRC) -> str:
-    """SHA-256 prefix of a kernel source's code: comments and blank lines
-    removed, so that a change to comments alone keeps a counter record."""
+def kernel_source_hash(src: str = KERNEL_SRC) -> str:
+    """SHA-256 prefix of a kernel source's code, headers of its own folder
+    included: comments and blank lines removed, so that a change to comments
+    alone keeps a counter record."""
     import re
-    if text is None:
-        text = open(src).read()
+    text = "\n".join(open(path).read() for path in with_headers(src))
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     lines = [re.sub(r"//.*", "", ln).rstrip() for ln in text.splitlines()]
     code = "\n".join(ln for ln in lines if ln.strip())
