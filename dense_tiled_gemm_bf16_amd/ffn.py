@@ -200,8 +200,9 @@ def route_topk(logits, k, score="softmax", bias=None, groups=1, groups_used=1, r
     the softmax or sigmoid of the logits; chosen are the largest score + bias
     (bias (E,) float32), with groups > 1 only from the groups_used groups whose
     two largest are highest; ties go to the lowest expert.  weights: the chosen
-    scores, divided by their sum if renormalize, times scale.  Logits of -inf
-    or NaN are never chosen; missing choices have id -1 and weight 0.
+    scores, divided by their sum if renormalize (sigmoid: their sum + 1e-20),
+    times scale.  Logits of -inf or NaN are never chosen; missing choices have
+    id -1 and weight 0.
     """
     return _call("route_topk", logits, stream, logits, k, _score(score), bias, groups, groups_used, renormalize, scale,
                  weights, ids)

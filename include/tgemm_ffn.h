@@ -186,9 +186,12 @@ TGEMM_API int gemm_grouped_tn(const tgemm_grouped_tn_args *args, hipStream_t str
  * groups_used best groups are chosen from.  Without bias experts are then
  * ordered by the logits themselves (as by s, without the ties that rounding
  * makes).  The choices are the k largest keys in falling order; ties go
- * to the lowest index, of groups too.  weights are the chosen s, divided by
- * their sum + 1e-20 if renormalize, times scale.  Where fewer than k experts
- * can be chosen the last ids are -1 and their weights 0.
+ * to the lowest index, of groups too.  weights are the chosen s times scale;
+ * with renormalize, scale times the softmax of the chosen logits (which is s
+ * over the sum of the chosen s, and holds also where a bias or groups leave
+ * only scores too small for binary32), or the chosen sigmoids divided by
+ * their sum + 1e-20.  Where fewer than k experts can be chosen the last ids
+ * are -1 and their weights 0.
  *
  *   logits   T x E, rows ld elements apart, TGEMM_DT_BF16, F16 or F32 (aligned
  *            to the element)

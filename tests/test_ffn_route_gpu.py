@@ -325,6 +325,46 @@ def test_gradient_of_masked_and_missing_choices():
     assert (dx == 0).all()
 
 
+def test_renormalised_weights_of_scores_too_small():
+    """A bias or groups that leave only experts whose scores are far below
+    1e-20: a softmax's weights are the softmax over the chosen logits all the
+    same, a sigmoid's their sigmoids over their sum + 1e-20.  The gradients go
+    by the same formulas."""
+    k, E = 4, 96
+    x = rand(1, 6, E)
+    x[:, 0] = torch.tensor([60.0, 100.0, 200.0, 0.0, 500.0, 80.0])
+    bias = torch.zeros(E)
+    bias[0] = -math.inf
+    w, ids = check_topk(x, k, bias=bias)
+    at = ids.cpu().long()
+    assert bool((at > 0).all())
+    # (p: 5 operations a term on numbers up to 1, and a sum of four.)
+    want = torch.softmax(x.double().gather(1, at), 1)
+    ref.assert_near(w, want, WEIGHT * want, "softmax")
+    dw = rand(2, 6, k)
+    p = x.double().requires_grad_()
+    torch.softmax(p.gather(1, at), 1).backward(dw.double())
+    mag = torch.zeros(6, E, dtype=torch.float64)
+    mag.scatter_(1, at, want * (dw.double().abs() + (want * dw.double().abs()).sum(1, keepdim=True)))
+    dx = tg.route_topk_backward(dw.cuda(), x.cuda(), ids)
+    ref.assert_near(dx, p.grad, 4 * WEIGHT * mag + 2.0 ** -126, "its gradient")
+
+    low = x[:, 1:] * 0.5 - 46.0                    # sigmoids of some 1e-20
+    w, ids = check_topk(low, k, score="sigmoid")
+    at = ids.cpu().long()
+    s = torch.exp(low.double()).gather(1, at)      # (1 + s is 1 here, to 1e-19)
+    want = s / (s.sum(1, keepdim=True) + 1e-20)
+    assert bool((want.sum(1) < 0.99).any())
+    ref.assert_near(w, want, WEIGHT * want, "sigmoid")
+    p = low.double().requires_grad_()
+    e = torch.exp(p).gather(1, at)
+    (e / (e.sum(1, keepdim=True) + 1e-20)).backward(dw.double())
+    mag = torch.zeros(6, E - 1, dtype=torch.float64)
+    mag.scatter_(1, at, want * (dw.double().abs() + (want * dw.double().abs()).sum(1, keepdim=True)))
+    dx = tg.route_topk_backward(dw.cuda(), low.cuda(), ids, score="sigmoid")
+    ref.assert_near(dx, p.grad, 4 * WEIGHT * mag + 2.0 ** -126, "its gradient")
+
+
 def test_gradient_in_place():
     x, dw = rand(1, 50, 64).cuda(), rand(2, 50, 4).cuda()
     _, ids = tg.route_topk(x, 4, renormalize=False)
