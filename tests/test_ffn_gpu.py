@@ -419,6 +419,22 @@ def test_grouped_weights_stored_k_by_n(size, tile):
         run_grouped(counts, 80, 72, BF16, False, "geglu", True, seed=size + 1)
 
 
+@pytest.mark.parametrize("size", [64, 128, 256])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("trans", [True, False])
+@pytest.mark.parametrize("act", ["none", "swiglu", "geglu"])
+def test_grouped_with_nothing_else(size, gather, trans, act, tile):
+    """No bias and no preact: the instances that store straight from the
+    accumulators.  Last tiles of up to half a tile's rows and of more, K of one
+    slice, of a few and of more than the prefetch looks ahead, N of several
+    tiles and a ragged one."""
+    tile(size, size)
+    N = 520 if act == "none" else 528
+    for i, (counts, K) in enumerate([([300, 0, 140, 256, 1, 520], 328), ([64, 129, 383, 5], 72), ([2, 0, 128], 584)]):
+        run_grouped(counts, N, K, F16 if i == 1 else BF16, trans, act, gather, bias=False, preact=False, seed=size + i)
+        run_grouped(counts[:3], 48, K, BF16 if i == 1 else F16, trans, act, gather, bias=False, preact=False, seed=i)
+
+
 def test_grouped_chosen_kernels():
     run_grouped([200, 1, 300, 77], 520, 264, BF16, True, "gelu", False, seed=1)
     run_grouped([20, 1, 33, 0, 17], 520, 264, BF16, True, "gelu", True, seed=2)
