@@ -312,3 +312,25 @@ def test_the_products_kernels_keep_their_accumulators_in_registers(tmp_path):
                 seen += 1
                 assert int(size) == 0, name
     assert seen > 60
+
+
+def test_the_k_splits_kernels_keep_their_accumulators_in_registers(tmp_path):
+    """The same of the K split: its products and the kernel that joins their
+    sums, which are no instances of the epilogue's."""
+    tools = "/opt/rocm/lib/llvm/bin"
+    if not os.path.exists(os.path.join(tools, "llvm-readelf")):
+        pytest.skip("no LLVM tools")
+    so = tmp_path / "lib.so"
+    so.write_bytes(open(ffn.LIB_PATH, "rb").read())
+    subprocess.run([os.path.join(tools, "llvm-objdump"), "--offloading", str(so)], capture_output=True, check=True,
+                   cwd=tmp_path)
+    seen = {"split": 0, "join": 0}
+    for f in tmp_path.glob("lib.so.*gfx950*"):
+        notes = subprocess.run([os.path.join(tools, "llvm-readelf"), "--notes", str(f)], capture_output=True, text=True,
+                               check=True).stdout
+        for name, size in re.findall(r"\.name:\s+(\S+).*?\.private_segment_fixed_size:\s+(\d+)", notes, re.S):
+            kind = re.search(r"\d(split|join)_kernel", name)
+            if kind:
+                seen[kind.group(1)] += 1
+                assert int(size) == 0, name
+    assert seen == {"split": 8, "join": 4}        # types and layouts; types, gated or not
