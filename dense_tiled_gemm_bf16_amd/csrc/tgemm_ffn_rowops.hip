@@ -19,7 +19,8 @@ namespace {
 // threads of 8 columns side by side, 8 rows at a time.  Its column sums go to
 // a workspace row of their own, and a second kernel adds a group's rows in
 // order, so that the sums do not depend on timing (atomics would).  dZ is
-// rounded once, to the type that the products behind it take.  4096 x 4096 of
+// rounded once, to the type that the products behind it take, after its columns
+// are summed.  4096 x 4096 of
 // gelu_tanh: 22.3 us for 100 MB (4.5 TB/s; a copy reaches 5.2), its sums 4.9 us.
 // ---------------------------------------------------------------------------
 struct GradArgs {
@@ -317,6 +318,9 @@ struct CombineGradArgs {
 };
 
 // One wave a choice: dh[slot] = weight dout[t], dweight = dout[t] . h[slot].
+// dh is rounded once, to the type that the two products behind it take; the dot
+// product stays in binary32.  (Choices that share a row write over one another:
+// a plan's do not.)
 template <int DT>
 __global__ __launch_bounds__(256) void combine_grad_kernel(const CombineGradArgs a) {
   const int lane = threadIdx.x & 63;

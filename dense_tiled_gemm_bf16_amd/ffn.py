@@ -211,8 +211,8 @@ def route_topk(logits, k, score="softmax", bias=None, groups=1, groups_used=1, r
 def route_topk_backward(dweights, logits, ids, score="softmax", renormalize=True, scale=1.0, dlogits=None,
                         stream=None):
     """The gradient of route_topk's weights with respect to the logits, from
-    dweights (T,k) float32, the logits and the ids it gave: dlogits (T,E) in
-    the logits' type."""
+    dweights (T,k) float32, the logits and the ids it gave (distinct in a
+    row): dlogits (T,E) in the logits' type, and may be logits."""
     return _call("route_topk_backward", logits, stream, dweights, logits, ids, _score(score), renormalize, scale, dlogits)
 
 
@@ -240,5 +240,6 @@ def expert_combine(h, slots, weights=None, residual=None, out=None, stream=None)
 
 def expert_combine_backward(dout, h, slots, weights, dh=None, dweights=None, stream=None):
     """Gradients of expert_combine: (dh (R,D), dweights (T,k) float32).  Rows
-    of dh that no slot names are not written."""
+    of dh that no slot names are not written; slots are to be distinct, as a
+    plan's are (a row that several name holds no sum of theirs)."""
     return _call("expert_combine_backward", dout, stream, dout, h, slots, weights, dh, dweights)

@@ -284,7 +284,9 @@ TGEMM_API int expert_combine(const tgemm_expert_combine_args *args, hipStream_t 
  * Its gradients: dh[slots[t][j]] = weights[t][j] dout[t] and dweights[t][j] =
  * dout[t] . h[slots[t][j]] (0 for a slot outside 0 .. R - 1); rows of dh that
  * no slot names are left as they were.  The slots of a plan name each row
- * once; a row named twice holds one of its values.
+ * once; of a row that several name each element is that of one of them (which
+ * one may differ from element to element and from call to call), while their
+ * dweights are right.
  */
 typedef struct {
   int64_t dtype, T, D, R, k;

@@ -449,6 +449,33 @@ def test_gather_combine_and_gradients(dtype, T, k, D, R):
     assert torch.equal(out.cpu(), torch.where(inside[:, None], x[rows.clamp(0, T - 1).long()], torch.tensor(3.0, dtype=dtype)))
 
 
+def test_a_row_named_by_several_slots():
+    """Elements of its gradient are each one of theirs, and their weights'
+    gradients are right; other rows are as ever."""
+    T, k, D, R = 40, 2, 1096, 50
+    dy, h, w = rand(1, T, D, dtype=BF16), rand(2, R, D, dtype=BF16), rand(3, T, k)
+    slots = torch.arange(T * k).view(T, k) % R
+    slots[:, 1] = torch.where(torch.arange(T) < 30, torch.full((T,), 7), torch.full((T,), -1))
+    slots = slots.to(torch.int32)
+    dh, dw = tg.expert_combine_backward(dy.cuda(), h.cuda(), slots.cuda(), w.cuda(),
+                                        dh=torch.zeros(R, D, dtype=BF16, device="cuda"))
+    torch.cuda.synchronize()
+    names = [[] for _ in range(R)]
+    for t in range(T):
+        for j in range(k):
+            if slots[t, j] >= 0:
+                names[int(slots[t, j])].append((w[t, j] * dy[t].float()).to(BF16))
+    assert len(names[7]) == 30
+    for r in range(R):
+        if names[r]:
+            assert bool((torch.stack(names[r]) == dh[r].cpu()).any(0).all()), r
+        else:
+            assert not dh[r].any()
+    ok = slots >= 0
+    terms = torch.where(ok[:, :, None], h.double()[slots.clamp(min=0).long()], torch.zeros(1, dtype=torch.float64)) * dy.double()[:, None]
+    ref.assert_near(dw, terms.sum(2), (D + 8) * 2.0 ** -24 * terms.abs().sum(2) + 1e-30, "dweights")
+
+
 def test_strided_rows_keep_what_is_around():
     T, k, D, R = 9, 2, 40, 18
     big = torch.full((R, D + 16), float("nan"), dtype=BF16, device="cuda")
