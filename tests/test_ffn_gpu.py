@@ -435,6 +435,60 @@ def test_grouped_with_nothing_else(size, gather, trans, act, tile):
         run_grouped(counts[:3], 48, K, BF16 if i == 1 else F16, trans, act, gather, bias=False, preact=False, seed=i)
 
 
+@pytest.mark.parametrize("size", [16, 64, 128, 256])
+@pytest.mark.parametrize("act", ["none", "silu", "swiglu"])
+def test_grouped_with_an_empty_k(size, act, tile):
+    """Nothing to sum: the bias through the activation, or zeros, in every row
+    of a group and none behind."""
+    tile(size, size)
+    counts, N = [3, 0, 140, 1], 48
+    off, used = groups_of(counts), sum(counts)
+    F = N // 2 if act in ref.GATED else N
+    bias = rand(1, 4, N)
+    for bs in (bias, None):
+        for trans in (True, False) if size != 16 else (True,):
+            b = torch.empty(4, N, 0, dtype=BF16, device="cuda").transpose(1, 2) if trans else torch.empty(4, 0, N, dtype=BF16, device="cuda")
+            out = torch.full((used + 2, F), 3.0, dtype=BF16, device="cuda")
+            say("grouped, K = 0", size, act, trans, bs is not None)
+            tg.gemm_grouped(torch.empty(used + 2, 0, dtype=BF16, device="cuda"), b, off.cuda(), bias=None if bs is None else bs.cuda(),
+                            act=act, out=out)
+            torch.cuda.synchronize()
+            assert (out[used:] == 3.0).all()
+            for e, n in enumerate(counts):
+                z = (torch.zeros(1, N) if bs is None else bs[e:e + 1]).double()
+                want = ref.layer(z, act)
+                tol = ref.layer_error(z, torch.zeros_like(z), act) + ref.rounding(want, BF16) * 1.001
+                lo = int(off[e])
+                ref.assert_near(out[lo:lo + n], want.expand(n, F), tol.expand(n, F), f"group {e}")
+
+
+def test_no_rows_at_all():
+    """Empty row sets: nothing is written but the gradients' zeros."""
+    off = torch.zeros(4, dtype=torch.int32, device="cuda")
+    rows = torch.empty(0, dtype=torch.int32, device="cuda")
+    x, y = (torch.empty(0, n, dtype=BF16, device="cuda") for n in (72, 136))
+    w = rand(1, 3, 72, 136).cuda()
+    out = torch.full((3, 72, 136), 3.0, dtype=BF16, device="cuda")
+    assert not tg.gemm_grouped_tn(x, y, off, out=out).any()
+    assert tg.gemm_grouped(x, w, off).shape == (0, 136)
+    assert tg.gemm_grouped(x, w, off, rows=rows).shape == (0, 136)
+    # Rows of a source that has none read zeros.
+    got = tg.gemm_grouped(x, w, torch.tensor([0, 2, 2, 5], dtype=torch.int32, device="cuda"),
+                          rows=torch.zeros(5, dtype=torch.int32, device="cuda"))
+    assert got.shape == (5, 136) and not got.any()
+    assert tg.expert_gather(x, rows).shape == (0, 72)
+    none = torch.empty(0, 2, dtype=torch.int32, device="cuda")
+    assert tg.expert_combine(x, none).shape == (0, 72)
+    slots = torch.zeros(6, 2, dtype=torch.int32, device="cuda")
+    res = rand(2, 6, 72).cuda()
+    assert torch.equal(tg.expert_combine(x, slots, residual=res), res)
+    dh, dw = tg.expert_combine_backward(res, x, slots, torch.ones(6, 2, device="cuda"))
+    torch.cuda.synchronize()
+    assert dh.shape == (0, 72) and not dw.any()
+    z, db = tg.epilogue_backward(y, y, "silu", offsets=off)
+    assert z.shape == (0, 136) and db.shape == (3, 136) and not db.any()
+
+
 def test_grouped_chosen_kernels():
     run_grouped([200, 1, 300, 77], 520, 264, BF16, True, "gelu", False, seed=1)
     run_grouped([20, 1, 33, 0, 17], 520, 264, BF16, True, "gelu", True, seed=2)
