@@ -76,7 +76,8 @@ bool bad16(int64_t dtype) { return dtype != TGEMM_DT_BF16 && dtype != TGEMM_DT_F
 // Sizes leave the kernels' 32-bit indexes room for one step past the end.
 constexpr int64_t kSizeLimit = (int64_t)INT32_MAX - 4095;
 // The kernels look up their group among all of them, and each chunk of a plan
-// adds the counts of all the others: more would take seconds.
+// adds the counts of all the others, so that its time grows with their square
+// (1024 experts: 2^22 choices 0.33 ms, 2^24 4.3, 2^26 67; 256: 0.12, 1.3, 17).
 constexpr int64_t kMostGroups = 65536, kMostChoices = (int64_t)1 << 26;
 
 int sizes(const char *fn, const int64_t *v, int n) {

@@ -57,7 +57,9 @@ Shape pick_grouped(const Shape (&shapes)[NS], int64_t M, int64_t N, int64_t grou
   return best;
 }
 
-constexpr int kCus = 256;  // compute units of an MI355X: the rule holds also where no device is
+// Compute units of an MI355X: the workspace's size is asked for on the host, where
+// there may be no device, and the call has to split as that said.
+constexpr int kCus = 256;
 constexpr int kMostSplits = 16;
 
 }  // namespace
@@ -71,10 +73,13 @@ constexpr int kMostSplits = 16;
 //   553   896   4016  19.9 -> 16.2 (2)     24   1024  8192  20.1 -> 8.8 (16)
 //   512   512   8192  23.3 -> 13.8 (4)     704  704   8192  24.4 -> 18.7 (2)
 // More splits than fill the chip lose (704 x 704 x 8192: 3 take 24.2), and so
-// do any where more than half of it is busy (1138 x 736 x 7296: 24.7 -> 29.8) or
-// where the tiles read memory as fast as it goes, which depends on the columns
-// and rows of a slice (K = 4096: 48 x 6144 gated 14.3 -> 13.9, 48 x 7168 14.6 ->
-// 14.6, 48 x 8192 gated 14.9 -> 15.9).
+// do any where more than half of it is busy (1138 x 736 x 7296: 24.7 -> 29.8).
+// The bound on M + N can only tell in one row of tiles with more than 7104
+// columns (or one column with as many rows), and goes by weights that the caches
+// hold (K = 4096: 48 x 6144 gated 14.3 -> 13.9, 48 x 7168 14.6 -> 14.6, 48 x
+// 8192 gated 14.9 -> 15.9).  Weights from beyond them would be read faster by
+// two splits there too: 48 x 8192 x 4096 gated 22.0 -> 20.5, 17 x 8192 x 2112
+// 12.1 -> 11.3, 64 x 8192 x 8192 43.1 -> 34.0, NN 48 x 7680 x 4096 26.5 -> 19.5.
 // At up to 16 rows NT the kernel for few rows splits K among its waves, and
 // this split beats it from deeper on (16 x 1024: 4096 9.8 -> 8.0, 8192 16.8 ->
 // 8.8; one row: 4096 7.2 -> 7.5, 8192 11.5 -> 8.3).
