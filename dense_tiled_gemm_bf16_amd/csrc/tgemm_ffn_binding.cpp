@@ -65,6 +65,15 @@ int64_t integer(PyObject *o, const char *name) {
   return v;
 }
 
+bool truth(PyObject *o, const char *name) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) {  // (an array of several values, say)
+    PyErr_Clear();
+    type_error(std::string(name) + " must be true or false");
+  }
+  return v == 1;
+}
+
 int dtype16(const Tensor &t, const char *name) {
   if (t.scalar_type() == ScalarType::BFloat16) return TGEMM_DT_BF16;
   if (t.scalar_type() == ScalarType::Half) return TGEMM_DT_F16;
@@ -274,7 +283,7 @@ PyObject *epilogue_backward(Args o) {
     p.offsets = on.packed<int32_t>(off, "offsets", ScalarType::Int, {p.groups + 1});
   }
   Tensor dbias, ws;
-  const bool want = PyObject_IsTrue(o[4]) == 1;
+  const bool want = truth(o[4], "want_dbias");
   if (want) {
     if (p.groups) {
       dbias = on.out(o[6], "dbias", t, {p.groups, p.N});
@@ -379,7 +388,7 @@ PyObject *topk(Args o) {
   if (o[3] != Py_None) p.bias = on.packed<float>(tensor(o[3], "bias"), "bias", ScalarType::Float, {p.E});
   p.groups = integer(o[4], "groups");
   p.groups_used = integer(o[5], "groups_used");
-  p.renormalize = PyObject_IsTrue(o[6]) == 1;
+  p.renormalize = truth(o[6], "renormalize");
   p.scale = PyFloat_AsDouble(o[7]);
   if (PyErr_Occurred()) {
     PyErr_Clear();
@@ -408,7 +417,7 @@ PyObject *topk_backward(Args o) {
   p.ids = on.packed<int32_t>(ids, "ids", ScalarType::Int, {p.T, p.k});
   p.dweights = on.packed<float>(dw, "dweights", ScalarType::Float, {p.T, p.k});
   p.score = integer(o[3], "score");
-  p.renormalize = PyObject_IsTrue(o[4]) == 1;
+  p.renormalize = truth(o[4], "renormalize");
   p.scale = PyFloat_AsDouble(o[5]);
   if (PyErr_Occurred()) {
     PyErr_Clear();

@@ -829,3 +829,18 @@ def test_the_binding_refuses():
         tg.route_topk(a.float(), 2, score="max")
     with pytest.raises(tg.TgemmError):
         tg.route_topk(a.float(), 17)
+
+
+def test_flags_that_are_no_truth_values_are_refused():
+    """An array of several values has no truth value: a TypeError, not a result
+    beside an error."""
+    x = rand(1, 8, 16).cuda()
+    several = torch.tensor([True, False])
+    ids = torch.zeros(8, 2, dtype=torch.int32, device="cuda")
+    for call, name in ((lambda: tg.epilogue_backward(x, x, "relu", want_dbias=several), "want_dbias"),
+                       (lambda: tg.route_topk(x, 2, renormalize=several), "renormalize"),
+                       (lambda: tg.route_topk_backward(torch.zeros(8, 2, device="cuda"), x, ids, renormalize=several), "renormalize")):
+        with pytest.raises(TypeError, match=name + " must be true or false"):
+            call()
+    dz, db = tg.epilogue_backward(x, x, "relu", want_dbias=torch.tensor(False))
+    assert db is None and dz.shape == x.shape
