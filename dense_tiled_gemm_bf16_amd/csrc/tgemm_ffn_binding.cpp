@@ -394,6 +394,8 @@ PyObject *topk(Args o) {
     PyErr_Clear();
     type_error("scale must be a number");
   }
+  // (More choices than experts are refused before memory is taken for them.)
+  if (p.k > p.E) check(route_topk(&p, on.stream()));
   const Tensor w = on.out(o[8], "weights", ScalarType::Float, {p.T, p.k}), ids = on.out(o[9], "ids", ScalarType::Int, {p.T, p.k});
   p.weights = on.packed<float>(w, "weights", ScalarType::Float, {p.T, p.k});
   p.ids = on.packed<int32_t>(ids, "ids", ScalarType::Int, {p.T, p.k});
@@ -441,6 +443,7 @@ PyObject *plan(Args o) {
   p.k = ids.size(1);
   p.E = integer(o[1], "experts");
   if (p.E < 0) value_error("experts must not be negative");
+  if (p.E > 1024) check(route_plan(&p, on.stream()));  // (refused before offsets for them are made)
   p.ids = on.packed<int32_t>(ids, "ids", t, {p.T, p.k});
   const Tensor off = on.out(o[2], "offsets", t, {p.E + 1}), rows = on.out(o[3], "rows", t, {p.T * p.k}),
                slots = on.out(o[4], "slots", t, {p.T, p.k});

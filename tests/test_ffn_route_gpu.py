@@ -500,3 +500,18 @@ def test_sigmoid_far_out():
     x = torch.linspace(-120, 120, 50).view(1, 50)
     check_topk(x, 50, score="sigmoid", renormalize=False)
     assert math.isclose(float(tg.route_topk(x.cuda(), 1, score="sigmoid")[0]), 1.0)
+
+
+def test_numbers_too_large_are_refused_before_memory_is_taken():
+    x = rand(1, 4, 32).cuda()
+    ids = torch.zeros(4, 2, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.max_memory_allocated()
+    for k in (33, 1 << 20, 1 << 40, (1 << 62) + 1):
+        with pytest.raises(tg.TgemmError):
+            tg.route_topk(x, k)
+    for experts in (1025, 1 << 20, 1 << 40, (1 << 63) - 1):
+        with pytest.raises(tg.TgemmError):
+            tg.route_plan(ids, experts)
+    assert torch.cuda.max_memory_allocated() == before
