@@ -106,7 +106,8 @@ __device__ __forceinline__ uint32_t umax_l(uint32_t v) {
 // all keys in 64 bits took 57 us, rounded keys with a lane-by-lane scan of
 // the groups in LDS 34 us (1640 VALU instructions a wave of 4 tokens), groups
 // as runs of registers 25 us (1235; 33.6 MB of logits, 1.4 TB/s).  8 tokens
-// take 4.8 us, the way through one wave.
+// take 4.8 us, the way through one wave.  More than 256 experts take a whole
+// wave a token: 8192 tokens of 384 in 8 groups 18.5 us, of 256 11.7.
 // ---------------------------------------------------------------------------
 struct TopkArgs {
   const void *logits;
