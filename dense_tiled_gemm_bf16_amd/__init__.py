@@ -346,5 +346,6 @@ def gemm_mxfp6_nt(a, b, scale_a, scale_b, fmt="e2m3", out=None, stream=None):
 # The feed-forward layers' operators (libtgemm_ffn.so; ffn.set_tile is their
 # tile override).
 from . import ffn  # noqa: E402
-from .ffn import (epilogue_backward, expert_combine, expert_combine_backward, expert_gather,  # noqa: E402,F401
-                  gemm_epilogue, gemm_grouped, gemm_grouped_tn, route_plan, route_topk, route_topk_backward)
+from .ffn import (dequantize_mxfp4, epilogue_backward, expert_combine, expert_combine_backward,  # noqa: E402,F401
+                  expert_gather, gemm_epilogue, gemm_grouped, gemm_grouped_tn, gemm_mxfp4_epilogue, gemm_mxfp4_grouped,
+                  layer_norm, layer_norm_backward, quantize_mxfp4, route_plan, route_topk, route_topk_backward)

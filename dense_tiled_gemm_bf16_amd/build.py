@@ -22,6 +22,8 @@ FFN_LIB = os.path.join(PKG, "libtgemm_ffn.so")
 FFN_SOURCES = [os.path.join(CSRC, "tgemm_ffn_gemm_bf16.hip"), os.path.join(CSRC, "tgemm_ffn_gemm_f16.hip"),
                os.path.join(CSRC, "tgemm_ffn_gemm.hip"), os.path.join(CSRC, "tgemm_ffn_rows.hip"),
                os.path.join(CSRC, "tgemm_ffn_rowops.hip"), os.path.join(CSRC, "tgemm_ffn_route.hip"),
+               os.path.join(CSRC, "tgemm_ffn_norm.hip"), os.path.join(CSRC, "tgemm_ffn_quant.hip"),
+               os.path.join(CSRC, "tgemm_ffn_mx_rows.hip"), os.path.join(CSRC, "tgemm_ffn_mx.hip"),
                os.path.join(CSRC, "tgemm_ffn_abi.cpp")]
 BINDING = os.path.join(PKG, "_ffn_binding.so")
 BINDING_SOURCE = os.path.join(CSRC, "tgemm_ffn_binding.cpp")

@@ -71,6 +71,7 @@ int check(const char *fn, const Tensor *t, int n, int outs, const Same *same = n
   return TGEMM_OK;
 }
 
+int elem_of(int64_t dtype) { return dtype == TGEMM_DT_F32 ? 4 : 2; }
 bool bad16(int64_t dtype) { return dtype != TGEMM_DT_BF16 && dtype != TGEMM_DT_F16; }
 
 // Sizes leave the kernels' 32-bit indexes room for one step past the end.
@@ -516,6 +517,298 @@ int expert_combine_backward(const tgemm_expert_combine_backward_args *p, hipStre
   ffn::CombineGrad g{(int)p->dtype, p->T, p->D, p->R, (int)p->k, p->dout, p->ldd, p->h, p->ldh, p->slots,
                      p->weights, p->dh, p->ldg, p->dweights, stream};
   return launched(fn, ffn::launch_combine_grad(g));
+}
+
+static int check_types(const char *fn, int64_t dtype, int64_t wdtype) {
+  if (dtype < TGEMM_DT_BF16 || dtype > TGEMM_DT_F32) return fail(TGEMM_EINVAL, "%s: no element type %lld", fn, (ll)dtype);
+  if (wdtype != dtype && wdtype != TGEMM_DT_F32)
+    return fail(TGEMM_EINVAL, "%s: the weight's type %lld must be the rows' or binary32", fn, (ll)wdtype);
+  return TGEMM_OK;
+}
+
+int layer_norm(const tgemm_layer_norm_args *p, hipStream_t stream) {
+  static const char fn[] = "layer_norm";
+  g_err[0] = '\0';
+  if (!p) return fail(TGEMM_EINVAL, "%s: args is NULL", fn);
+  int rc = check_types(fn, p->dtype, p->wdtype);
+  const int64_t v[] = {p->M, p->N};
+  if (rc == TGEMM_OK) rc = sizes(fn, v, 2);
+  if (rc != TGEMM_OK) return rc;
+  if (p->N < 8) return fail(TGEMM_EINVAL, "%s: N=%lld must be at least 8", fn, (ll)p->N);
+  if (!(p->eps >= 0.0 && p->eps <= 3e38)) return fail(TGEMM_EINVAL, "%s: eps must be finite and not negative", fn);
+  if (p->M == 0) return TGEMM_OK;
+  const int e = elem_of(p->dtype), w = elem_of(p->wdtype);
+  const Tensor t[] = {{"y", p->y, p->M, p->N, p->ldy, e, true, true},
+                      {"mean", p->mean, 1, p->M, p->M, 4, false, false},
+                      {"rstd", p->rstd, 1, p->M, p->M, 4, false, false},
+                      {"x", p->x, p->M, p->N, p->ldx, e, true, true},
+                      {"weight", p->weight, 1, p->N, p->N, w, true, false},
+                      {"bias", p->bias, 1, p->N, p->N, w, true, false}};
+  static const Same same[] = {{0, 3}};
+  rc = check(fn, t, 6, 3, same, 1);
+  if (rc == TGEMM_OK) rc = ensure_device(nullptr, nullptr);
+  if (rc != TGEMM_OK) return rc;
+  ffn::Norm g{(int)p->dtype, (int)p->wdtype, p->M, p->N, p->x, p->ldx, p->weight, p->bias, (float)p->eps, p->y, p->ldy,
+              p->mean, p->rstd, stream};
+  return launched(fn, ffn::launch_norm(g));
+}
+
+uint64_t tgemm_layer_norm_backward_workspace_bytes(int64_t M, int64_t N) {
+  if (M <= 0 || N <= 0 || M > INT32_MAX || N > INT32_MAX) return 0;
+  return ffn::norm_grad_ws_floats(M, N) * 4u;
+}
+
+int layer_norm_backward(const tgemm_layer_norm_backward_args *p, hipStream_t stream) {
+  static const char fn[] = "layer_norm_backward";
+  g_err[0] = '\0';
+  if (!p) return fail(TGEMM_EINVAL, "%s: args is NULL", fn);
+  int rc = check_types(fn, p->dtype, p->wdtype);
+  const int64_t v[] = {p->M, p->N};
+  if (rc == TGEMM_OK) rc = sizes(fn, v, 2);
+  if (rc != TGEMM_OK) return rc;
+  if (p->N < 8) return fail(TGEMM_EINVAL, "%s: N=%lld must be at least 8", fn, (ll)p->N);
+  if (p->M == 0 && !p->dweight && !p->dbias) return TGEMM_OK;
+  const int e = elem_of(p->dtype), w = elem_of(p->wdtype);
+  const uint64_t need = tgemm_layer_norm_backward_workspace_bytes(p->M, p->N);
+  if (need / 4 > (uint64_t)INT32_MAX) return fail(TGEMM_ETOOBIG, "%s: the sums need a workspace above 8 GiB", fn);
+  const Tensor t[] = {{"dx", p->dx, p->M, p->N, p->ldo, e, true, true},
+                      {"dweight", p->dweight, 1, p->N, p->N, w, true, false},
+                      {"dbias", p->dbias, 1, p->N, p->N, w, true, false},
+                      {"workspace", p->workspace, need > 0, (int64_t)(need / 4), (int64_t)(need / 4), 4, false, true},
+                      {"dy", p->dy, p->M, p->N, p->ldd, e, true, true},
+                      {"x", p->x, p->M, p->N, p->ldx, e, true, true},
+                      {"residual", p->residual, p->M, p->N, p->ldr, e, true, false},
+                      {"weight", p->weight, 1, p->N, p->N, w, true, false},
+                      {"mean", p->mean, 1, p->M, p->M, 4, false, true},
+                      {"rstd", p->rstd, 1, p->M, p->M, 4, false, true}};
+  static const Same same[] = {{0, 4}, {0, 5}, {0, 6}};
+  rc = check(fn, t, 10, 4, same, 3);
+  if (rc != TGEMM_OK) return rc;
+  if (need > 0 && misaligned(p->workspace)) return fail(TGEMM_EALIGN, "%s: workspace is not 16-byte aligned", fn);
+  if (p->workspace_bytes < need)
+    return fail(TGEMM_EINVAL, "%s: needs %llu workspace bytes, got %llu", fn, (unsigned long long)need,
+                (unsigned long long)p->workspace_bytes);
+  rc = ensure_device(nullptr, nullptr);
+  if (rc != TGEMM_OK) return rc;
+  ffn::NormGrad g{(int)p->dtype, (int)p->wdtype, p->M, p->N, p->dy, p->ldd, p->x, p->ldx, p->weight, p->mean, p->rstd,
+                  p->residual, p->ldr, p->dx, p->ldo, p->dweight, p->dbias, static_cast<float *>(p->workspace), stream};
+  return launched(fn, ffn::launch_norm_grad(g));
+}
+
+// Rows of MXFP4 elements: whole 16-byte pieces (32 elements each).
+static int check_bytes(const char *fn, const Tensor &t) {
+  if (t.p && t.rows > 1 && t.cols > 0 && t.ld % 16 != 0)
+    return fail(TGEMM_EALIGN, "%s: the row stride of %s (%lld bytes) must be a multiple of 16", fn, t.name, (ll)t.ld);
+  return TGEMM_OK;
+}
+
+int quantize_mxfp4(const tgemm_quantize_mxfp4_args *p, hipStream_t stream) {
+  static const char fn[] = "quantize_mxfp4";
+  g_err[0] = '\0';
+  if (!p) return fail(TGEMM_EINVAL, "%s: args is NULL", fn);
+  int rc = check_types(fn, p->dtype, p->dtype);
+  const int64_t v[] = {p->M, p->N};
+  if (rc == TGEMM_OK) rc = sizes(fn, v, 2);
+  if (rc != TGEMM_OK || p->M == 0 || p->N == 0) return rc;
+  const bool rows = p->q || p->scales, columns = p->qt || p->scalest;
+  if (!rows && !columns) return fail(TGEMM_EINVAL, "%s: q is NULL", fn);
+  if (rows && p->N % 32 != 0) return fail(TGEMM_EALIGN, "%s: N=%lld must be a multiple of 32", fn, (ll)p->N);
+  const int64_t blocks = (p->M + 31) / 32;
+  const Tensor t[] = {{"q", p->q, rows ? p->M : 0, p->N / 2, p->ldq, 1, true, true},
+                      {"scales", p->scales, rows, p->M * (p->N / 32), 0, 1, false, true},
+                      {"qt", p->qt, columns ? p->N : 0, blocks * 16, p->ldqt, 1, true, true},
+                      {"scalest", p->scalest, columns, p->N * blocks, 0, 1, false, true},
+                      {"x", p->x, p->M, p->N, p->ldx, elem_of(p->dtype), true, true}};
+  rc = check(fn, t, 5, 4);
+  if (rc == TGEMM_OK) rc = check_bytes(fn, t[0]);
+  if (rc == TGEMM_OK) rc = check_bytes(fn, t[2]);
+  if (rc == TGEMM_OK) rc = ensure_device(nullptr, nullptr);
+  if (rc != TGEMM_OK) return rc;
+  ffn::Quant g{(int)p->dtype, p->M, p->N, p->x, p->ldx, static_cast<uint8_t *>(p->q), p->ldq,
+               static_cast<uint8_t *>(p->scales), static_cast<uint8_t *>(p->qt), p->ldqt,
+               static_cast<uint8_t *>(p->scalest), stream};
+  return launched(fn, ffn::launch_quant_mxfp4(g));
+}
+
+int dequantize_mxfp4(const tgemm_dequantize_mxfp4_args *p, hipStream_t stream) {
+  static const char fn[] = "dequantize_mxfp4";
+  g_err[0] = '\0';
+  if (!p) return fail(TGEMM_EINVAL, "%s: args is NULL", fn);
+  int rc = check_types(fn, p->dtype, p->dtype);
+  const int64_t v[] = {p->M, p->N};
+  if (rc == TGEMM_OK) rc = sizes(fn, v, 2);
+  if (rc != TGEMM_OK || p->M == 0 || p->N == 0) return rc;
+  if (p->N % 32 != 0) return fail(TGEMM_EALIGN, "%s: N=%lld must be a multiple of 32", fn, (ll)p->N);
+  const Tensor t[] = {{"out", p->out, p->M, p->N, p->ldo, elem_of(p->dtype), true, true},
+                      {"q", p->q, p->M, p->N / 2, p->ldq, 1, true, true},
+                      {"scales", p->scales, 1, p->M * (p->N / 32), 0, 1, false, true}};
+  rc = check(fn, t, 3, 1);
+  if (rc == TGEMM_OK) rc = check_bytes(fn, t[1]);
+  if (rc == TGEMM_OK) rc = ensure_device(nullptr, nullptr);
+  if (rc != TGEMM_OK) return rc;
+  ffn::Dequant g{(int)p->dtype, p->M, p->N, static_cast<const uint8_t *>(p->q), p->ldq,
+                 static_cast<const uint8_t *>(p->scales), p->out, p->ldo, stream};
+  return launched(fn, ffn::launch_dequant_mxfp4(g));
+}
+
+static int run_mx(const char *fn, ffn::MxGemm &g) {
+  const int rc = ensure_device(&g.cus, nullptr);
+  if (rc != TGEMM_OK) return rc;
+  g.tile_m = g_tile_m;
+  g.tile_n = g_tile_n;
+  if (g.tile_m != 0 && !ffn::mx_tile_supported(g, g.tile_m, g.tile_n))
+    return fail(TGEMM_EINVAL, "%s: no %dx%d tile for this call (set by tgemm_ffn_set_tile)", fn, g.tile_m, g.tile_n);
+  return launched(fn, ffn::launch_mx(g));
+}
+
+// 31-bit offsets of a tile's rows of the weight (both halves at once if gated).
+static int check_mx_b(const char *fn, bool gated, int64_t N, int64_t ldb) {
+  const uint64_t rows = (gated ? (uint64_t)N / 2 : 0) + (uint64_t)tgemm::kTileN;
+  if (rows * (uint64_t)ldb > kOffsetLimit) return fail(TGEMM_ETOOBIG, "%s: B too large for 31-bit offsets", fn);
+  return TGEMM_OK;
+}
+
+uint64_t tgemm_mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || K <= 0 || M > INT32_MAX || N > INT32_MAX || K > INT32_MAX) return 0;
+  const int splits = ffn::mx_splits(M, N, K);
+  return splits > 1 ? (uint64_t)splits * (uint64_t)M * (uint64_t)N * 4u : 0;
+}
+
+int gemm_mxfp4_epilogue(const tgemm_mxfp4_epilogue_args *p, hipStream_t stream) {
+  static const char fn[] = "gemm_mxfp4_epilogue";
+  g_err[0] = '\0';
+  if (!p) return fail(TGEMM_EINVAL, "%s: args is NULL", fn);
+  if (bad16(p->dtype)) return fail(TGEMM_EINVAL, "%s: no element type %lld", fn, (ll)p->dtype);
+  const int64_t v[] = {p->M, p->N, p->K};
+  int rc = sizes(fn, v, 3);
+  if (rc == TGEMM_OK) rc = check_act(fn, p->act, p->N);
+  if (rc != TGEMM_OK) return rc;
+  if (p->K % 32 != 0) return fail(TGEMM_EALIGN, "%s: K=%lld must be a multiple of 32", fn, (ll)p->K);
+  if (p->M == 0 || p->N == 0) return TGEMM_OK;
+  const bool gated = ffn::is_gated((int)p->act);
+  const int64_t out_n = gated ? p->N / 2 : p->N, kb = p->K / 32;
+  int splits = ffn::mx_splits(p->M, p->N, p->K);
+  if (!p->workspace || (uint64_t)splits * (uint64_t)p->M * (uint64_t)p->N * 4u > p->workspace_bytes ||
+      (g_tile_m != 0 && g_tile_m != 64))
+    splits = 1;
+  const Tensor t[] = {
+      {"C", p->C, p->M, out_n, p->ldc, 2, true, true},
+      {"preact", p->preact, p->M, p->N, p->ldp, 2, true, false},
+      {"workspace", splits > 1 ? p->workspace : nullptr, splits > 1, (int64_t)splits * p->M * p->N, 0, 4, false, false},
+      {"A", p->A, p->K == 0 ? 0 : p->M, p->K / 2, p->lda, 1, true, true},
+      {"scale_A", p->scale_A, 1, p->M * kb, 0, 1, false, true},
+      {"B", p->B, p->K == 0 ? 0 : p->N, p->K / 2, p->ldb, 1, true, true},
+      {"scale_B", p->scale_B, 1, p->N * kb, 0, 1, false, true},
+      {"bias", p->bias, 1, p->N, p->N, 2, true, false},
+      {"residual", p->residual, p->M, out_n, p->ldr, 2, true, false}};
+  static const Same same[] = {{0, 8}};
+  rc = check(fn, t, 9, 3, same, 1);
+  if (rc == TGEMM_OK) rc = check_bytes(fn, t[3]);
+  if (rc == TGEMM_OK) rc = check_bytes(fn, t[5]);
+  if (rc != TGEMM_OK) return rc;
+  if (splits > 1 && misaligned(p->workspace)) return fail(TGEMM_EALIGN, "%s: workspace is not 16-byte aligned", fn);
+  // (An empty K is never read; one row needs no stride.)
+  const int64_t lda = p->K == 0 ? 0 : p->M == 1 ? p->K / 2 : p->lda, ldb = p->K == 0 ? 0 : p->N == 1 ? p->K / 2 : p->ldb;
+  if ((uint64_t)tgemm::kTileM * (uint64_t)lda > kOffsetLimit)
+    return fail(TGEMM_ETOOBIG, "%s: A too large for 31-bit offsets", fn);
+  rc = check_mx_b(fn, gated, p->N, ldb);
+  if (rc != TGEMM_OK) return rc;
+  ffn::MxGemm g{};
+  g.dtype = (int)p->dtype;
+  g.M = p->M;
+  g.N = p->N;
+  g.K = p->K;
+  g.A = p->A;
+  g.lda = lda;
+  g.SA = p->scale_A;
+  g.B = p->B;
+  g.ldb = ldb;
+  g.SB = p->scale_B;
+  g.bias = p->bias;
+  g.residual = p->residual;
+  g.ldr = p->ldr;
+  g.preact = p->preact;
+  g.ldp = p->ldp;
+  g.C = p->C;
+  g.ldc = p->ldc;
+  g.act = (int)p->act;
+  g.ws = static_cast<float *>(p->workspace);
+  g.splits = splits;
+  g.stream = stream;
+  return run_mx(fn, g);
+}
+
+int gemm_mxfp4_grouped(const tgemm_mxfp4_grouped_args *p, hipStream_t stream) {
+  static const char fn[] = "gemm_mxfp4_grouped";
+  g_err[0] = '\0';
+  if (!p) return fail(TGEMM_EINVAL, "%s: args is NULL", fn);
+  if (bad16(p->dtype)) return fail(TGEMM_EINVAL, "%s: no element type %lld", fn, (ll)p->dtype);
+  const int64_t v[] = {p->R, p->N, p->K, p->groups, p->src_rows};
+  int rc = sizes(fn, v, 5);
+  if (rc == TGEMM_OK) rc = check_groups(fn, p->groups);
+  if (rc == TGEMM_OK) rc = check_act(fn, p->act, p->N);
+  if (rc != TGEMM_OK) return rc;
+  if (p->K % 32 != 0) return fail(TGEMM_EALIGN, "%s: K=%lld must be a multiple of 32", fn, (ll)p->K);
+  if (p->R == 0 || p->N == 0 || p->groups == 0) return TGEMM_OK;
+  const bool gated = ffn::is_gated((int)p->act);
+  const int64_t out_n = gated ? p->N / 2 : p->N, kb = p->K / 32;
+  const int64_t src = p->rows ? p->src_rows : p->R;
+  const Tensor t[] = {
+      {"C", p->C, p->R, out_n, p->ldc, 2, true, true},
+      {"preact", p->preact, p->R, p->N, p->ldp, 2, true, false},
+      {"A", p->A, p->K == 0 ? 0 : src, p->K / 2, p->lda, 1, true, true},
+      {"scale_A", p->scale_A, 1, src * kb, 0, 1, false, true},
+      {"B", p->B, p->K == 0 ? 0 : p->N, p->K / 2, p->ldb, 1, true, true},
+      {"scale_B", p->scale_B, 1, p->N * kb, 0, 1, false, true},
+      {"bias", p->bias, p->groups, p->N, p->N, 2, true, false},
+      {"offsets", p->offsets, 1, p->groups + 1, p->groups + 1, 4, false, true},
+      {"rows", p->rows, 1, p->R, p->R, 4, false, false}};
+  rc = check(fn, t, 9, 2);
+  if (rc == TGEMM_OK) rc = check_bytes(fn, t[2]);
+  if (rc == TGEMM_OK) rc = check_bytes(fn, t[4]);
+  if (rc != TGEMM_OK) return rc;
+  const int64_t lda = p->K == 0 ? 0 : src == 1 ? p->K / 2 : p->lda, ldb = p->K == 0 ? 0 : p->N == 1 ? p->K / 2 : p->ldb;
+  if (p->K > 0 && p->groups > 1) {
+    if (p->stride_b < 0 || p->stride_sb < 0) return fail(TGEMM_EINVAL, "%s: stride_b or stride_sb is negative", fn);
+    if (p->stride_b % 16 != 0) return fail(TGEMM_EALIGN, "%s: stride_b must be a multiple of 16", fn);
+    if (p->stride_b > ((int64_t)1 << 40) || p->stride_sb > ((int64_t)1 << 40))
+      return fail(TGEMM_ETOOBIG, "%s: stride_b or stride_sb too large", fn);
+    const uint64_t n = (uint64_t)(p->groups - 1);
+    const uint64_t all = n * (uint64_t)p->stride_b + t[4].bytes(), alls = n * (uint64_t)p->stride_sb + t[5].bytes();
+    for (int i = 0; i < 2; ++i)
+      if (overlaps(t[i].p, t[i].bytes(), p->B, all) || overlaps(t[i].p, t[i].bytes(), p->scale_B, alls))
+        return fail(TGEMM_EINVAL, "%s: %s overlaps B or its scales", fn, t[i].name);
+  }
+  const uint64_t a_rows = p->rows ? (uint64_t)p->src_rows : (uint64_t)tgemm::kTileM;
+  if (a_rows * (uint64_t)lda > kOffsetLimit) return fail(TGEMM_ETOOBIG, "%s: A too large for 31-bit offsets", fn);
+  rc = check_mx_b(fn, gated, p->N, ldb);
+  if (rc != TGEMM_OK) return rc;
+  ffn::MxGemm g{};
+  g.dtype = (int)p->dtype;
+  g.M = p->R;
+  g.N = p->N;
+  g.K = p->K;
+  g.A = p->A;
+  g.lda = lda;
+  g.SA = p->scale_A;
+  g.B = p->B;
+  g.ldb = ldb;
+  g.SB = p->scale_B;
+  g.bias = p->bias;
+  g.preact = p->preact;
+  g.ldp = p->ldp;
+  g.C = p->C;
+  g.ldc = p->ldc;
+  g.act = (int)p->act;
+  g.groups = p->groups;
+  g.offsets = p->offsets;
+  g.rows = p->rows;
+  g.src_rows = src;
+  g.stride_b = p->K == 0 ? 0 : p->stride_b;
+  g.stride_sb = p->K == 0 ? 0 : p->stride_sb;
+  g.splits = 1;
+  g.stream = stream;
+  return run_mx(fn, g);
 }
 
 }  // extern "C"

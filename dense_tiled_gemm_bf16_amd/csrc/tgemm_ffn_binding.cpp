@@ -545,6 +545,292 @@ PyObject *combine_backward(Args o) {
   return tuple2(wrap(dh), wrap(dw));
 }
 
+// Element type of a norm's or a quantisation's rows.
+int dtype_any(const Tensor &t, const char *name) {
+  if (t.scalar_type() == ScalarType::Float) return TGEMM_DT_F32;
+  if (t.scalar_type() == ScalarType::BFloat16) return TGEMM_DT_BF16;
+  if (t.scalar_type() == ScalarType::Half) return TGEMM_DT_F16;
+  type_error(std::string(name) + " must be bfloat16, float16 or float32, got " + name_of(t.scalar_type()));
+}
+constexpr ScalarType kTypes[] = {ScalarType::BFloat16, ScalarType::Half, ScalarType::Float};
+// The type of a norm's weight and bias: x's or float32, one for both.
+ScalarType weight_type(PyObject *w, const char *name, ScalarType x) {
+  const ScalarType t = tensor(w, name).scalar_type();
+  if (t != x && t != ScalarType::Float)
+    type_error(std::string(name) + " must be " + name_of(x) + " or torch.float32, got " + name_of(t));
+  return t;
+}
+
+// x, weight, bias, eps, mean, rstd, out
+PyObject *norm(Args o) {
+  const Tensor &x = tensor(o[0], "x");
+  On on(x, "x");
+  tgemm_layer_norm_args p{};
+  p.dtype = dtype_any(x, "x");
+  matrix(x, "x");
+  const ScalarType t = x.scalar_type();
+  p.M = x.size(0);
+  p.N = x.size(1);
+  p.ldx = on.mat(x, "x", t, p.M, p.N);
+  p.x = ptr(x);
+  ScalarType wt = t;
+  if (o[1] != Py_None) {
+    wt = weight_type(o[1], "weight", t);
+    p.weight = on.packed(tensor(o[1], "weight"), "weight", wt, {p.N});
+  }
+  if (o[2] != Py_None) {
+    if (o[1] == Py_None) wt = weight_type(o[2], "bias", t);
+    p.bias = on.packed(tensor(o[2], "bias"), "bias", wt, {p.N});
+  }
+  p.wdtype = wt == t ? p.dtype : TGEMM_DT_F32;
+  p.eps = PyFloat_AsDouble(o[3]);
+  if (PyErr_Occurred()) {
+    PyErr_Clear();
+    type_error("eps must be a number");
+  }
+  if (o[4] != Py_None) p.mean = on.packed<float>(tensor(o[4], "mean"), "mean", ScalarType::Float, {p.M});
+  if (o[5] != Py_None) p.rstd = on.packed<float>(tensor(o[5], "rstd"), "rstd", ScalarType::Float, {p.M});
+  const Tensor out = on.out(o[6], "out", t, {p.M, p.N});
+  p.ldy = on.mat(out, "out", t, p.M, p.N);
+  p.y = ptr(out);
+  check(layer_norm(&p, on.stream()));
+  return wrap(out);
+}
+
+// dout, x, weight, mean, rstd, residual, want_dweight, dx, dweight, dbias, workspace
+PyObject *norm_backward(Args o) {
+  const Tensor &dy = tensor(o[0], "dout"), &x = tensor(o[1], "x");
+  On on(x, "x");
+  tgemm_layer_norm_backward_args p{};
+  p.dtype = dtype_any(x, "x");
+  matrix(x, "x");
+  const ScalarType t = x.scalar_type();
+  p.M = x.size(0);
+  p.N = x.size(1);
+  p.ldx = on.mat(x, "x", t, p.M, p.N);
+  p.x = ptr(x);
+  p.ldd = on.mat(dy, "dout", t, p.M, p.N);
+  p.dy = ptr(dy);
+  ScalarType wt = t;
+  if (o[2] != Py_None) {
+    wt = weight_type(o[2], "weight", t);
+    p.weight = on.packed(tensor(o[2], "weight"), "weight", wt, {p.N});
+  }
+  p.wdtype = wt == t ? p.dtype : TGEMM_DT_F32;
+  p.mean = on.packed<float>(tensor(o[3], "mean"), "mean", ScalarType::Float, {p.M});
+  p.rstd = on.packed<float>(tensor(o[4], "rstd"), "rstd", ScalarType::Float, {p.M});
+  if (o[5] != Py_None) {
+    const Tensor &r = tensor(o[5], "residual");
+    p.ldr = on.mat(r, "residual", t, p.M, p.N);
+    p.residual = ptr(r);
+  }
+  const Tensor dx = on.out(o[7], "dx", t, {p.M, p.N});
+  p.ldo = on.mat(dx, "dx", t, p.M, p.N);
+  p.dx = ptr(dx);
+  Tensor dw, db;
+  const bool want = truth(o[6], "want_dweight");
+  if (want) {
+    dw = on.out(o[8], "dweight", wt, {p.N});
+    p.dweight = on.packed(dw, "dweight", wt, {p.N});
+    db = on.out(o[9], "dbias", wt, {p.N});
+    p.dbias = on.packed(db, "dbias", wt, {p.N});
+  }
+  const Tensor ws = on.workspace(o[10], tgemm_layer_norm_backward_workspace_bytes(p.M, p.N));
+  p.workspace = ptr(ws);
+  p.workspace_bytes = (uint64_t)ws.nbytes();
+  check(layer_norm_backward(&p, on.stream()));
+  PyObject *a = wrap(dx), *b = want ? wrap(dw) : none(), *c = want ? wrap(db) : none();
+  PyObject *r = a && b && c ? PyTuple_Pack(3, a, b, c) : nullptr;
+  Py_XDECREF(a);
+  Py_XDECREF(b);
+  Py_XDECREF(c);
+  return r;
+}
+
+// x, rows, columns, q, scales, qt, scalest
+PyObject *quantize(Args o) {
+  const Tensor &x = tensor(o[0], "x");
+  On on(x, "x");
+  tgemm_quantize_mxfp4_args p{};
+  p.dtype = dtype_any(x, "x");
+  matrix(x, "x");
+  p.M = x.size(0);
+  p.N = x.size(1);
+  p.ldx = on.mat(x, "x", x.scalar_type(), p.M, p.N);
+  p.x = ptr(x);
+  const bool rows = truth(o[1], "rows"), columns = truth(o[2], "columns");
+  if (!rows && !columns) value_error("neither rows nor columns are wanted");
+  if (rows && p.N % 32) value_error("rows of x must be whole blocks of 32 values, got " + std::to_string(p.N));
+  const ScalarType b = ScalarType::Byte;
+  Tensor t[4];
+  int n = 0;
+  if (rows) {
+    t[0] = on.out(o[3], "q", b, {p.M, p.N / 2});
+    p.ldq = on.mat(t[0], "q", b, p.M, p.N / 2);
+    p.q = ptr(t[0]);
+    t[1] = on.out(o[4], "scales", b, {p.M, p.N / 32});
+    p.scales = on.packed(t[1], "scales", b, {p.M, p.N / 32});
+    n = 2;
+  }
+  if (columns) {
+    const int64_t blocks = (p.M + 31) / 32;
+    t[n] = on.out(o[5], "qt", b, {p.N, 16 * blocks});
+    p.ldqt = on.mat(t[n], "qt", b, p.N, 16 * blocks);
+    p.qt = ptr(t[n]);
+    t[n + 1] = on.out(o[6], "scalest", b, {p.N, blocks});
+    p.scalest = on.packed(t[n + 1], "scalest", b, {p.N, blocks});
+    n += 2;
+  }
+  check(quantize_mxfp4(&p, on.stream()));
+  PyObject *r = PyTuple_New(n);
+  for (int i = 0; r && i < n; ++i) {
+    PyObject *v = wrap(t[i]);
+    if (!v) {
+      Py_DECREF(r);
+      return nullptr;
+    }
+    PyTuple_SET_ITEM(r, i, v);
+  }
+  return r;
+}
+
+// q, scales, dtype (-1: out's, or bfloat16), out
+PyObject *dequantize(Args o) {
+  const Tensor &q = tensor(o[0], "q");
+  On on(q, "q");
+  tgemm_dequantize_mxfp4_args p{};
+  matrix(q, "q");
+  p.M = q.size(0);
+  p.N = 2 * q.size(1);
+  if (p.N % 32) value_error("rows of q must be whole blocks of 16 bytes, got " + std::to_string(q.size(1)));
+  p.ldq = on.mat(q, "q", ScalarType::Byte, p.M, p.N / 2);
+  p.q = ptr(q);
+  p.scales = on.packed(tensor(o[1], "scales"), "scales", ScalarType::Byte, {p.M, p.N / 32});
+  p.dtype = integer(o[2], "dtype");
+  if (p.dtype < 0) p.dtype = o[3] != Py_None ? dtype_any(tensor(o[3], "out"), "out") : TGEMM_DT_BF16;
+  const ScalarType t = kTypes[p.dtype];
+  const Tensor out = on.out(o[3], "out", t, {p.M, p.N});
+  p.ldo = on.mat(out, "out", t, p.M, p.N);
+  p.out = ptr(out);
+  check(dequantize_mxfp4(&p, on.stream()));
+  return wrap(out);
+}
+
+// The element type of an MXFP4 product: the one named, else that of the first
+// of these that is there, else bfloat16.
+int mx_dtype(PyObject *named, std::initializer_list<PyObject *> given) {
+  const int64_t d = integer(named, "dtype");
+  if (d == TGEMM_DT_F32) type_error("dtype must be torch.bfloat16 or torch.float16");
+  if (d >= 0) return (int)d;
+  for (PyObject *o : given)
+    if (o != Py_None) return dtype16(tensor(o, "out, bias, residual or preact"), "out, bias, residual or preact");
+  return TGEMM_DT_BF16;
+}
+
+// a, b, scale_a, scale_b, bias, act, residual, preact, out, dtype, workspace
+PyObject *mx_epilogue(Args o) {
+  const Tensor &a = tensor(o[0], "a"), &b = tensor(o[1], "b");
+  On on(a, "a");
+  matrix(a, "a");
+  matrix(b, "b");
+  const ScalarType u8 = ScalarType::Byte;
+  if (a.size(1) != b.size(1))
+    value_error("rows of a and b must be of one length, got " + shape_str(a.sizes()) + " and " + shape_str(b.sizes()));
+  if (a.size(1) % 16) value_error("rows of a and b must be whole blocks of 16 bytes, got " + std::to_string(a.size(1)));
+  tgemm_mxfp4_epilogue_args p{};
+  p.M = a.size(0);
+  p.K = 2 * a.size(1);
+  p.N = b.size(0);
+  p.lda = on.mat(a, "a", u8, p.M, p.K / 2);
+  p.A = ptr(a);
+  p.ldb = on.mat(b, "b", u8, p.N, p.K / 2);
+  p.B = ptr(b);
+  p.scale_A = on.packed(tensor(o[2], "scale_a"), "scale_a", u8, {p.M, p.K / 32});
+  p.scale_B = on.packed(tensor(o[3], "scale_b"), "scale_b", u8, {p.N, p.K / 32});
+  p.dtype = mx_dtype(o[9], {o[8], o[4], o[6], o[7]});
+  const ScalarType t = kTypes[p.dtype];
+  p.act = integer(o[5], "act");
+  const int64_t F = halved(p.N, p.act);
+  if (o[4] != Py_None) p.bias = on.packed(tensor(o[4], "bias"), "bias", t, {p.N});
+  if (o[6] != Py_None) {
+    const Tensor &r = tensor(o[6], "residual");
+    p.ldr = on.mat(r, "residual", t, p.M, F);
+    p.residual = ptr(r);
+  }
+  if (o[7] != Py_None) {
+    const Tensor &z = tensor(o[7], "preact");
+    p.ldp = on.mat(z, "preact", t, p.M, p.N);
+    p.preact = ptr(z);
+  }
+  const Tensor out = on.out(o[8], "out", t, {p.M, F});
+  p.ldc = on.mat(out, "out", t, p.M, F);
+  p.C = ptr(out);
+  const uint64_t need = tgemm_mxfp4_workspace_bytes(p.M, p.N, p.K);
+  Tensor ws;
+  if (need) {
+    ws = on.workspace(o[10], need);
+    p.workspace = ptr(ws);
+    p.workspace_bytes = (uint64_t)ws.nbytes();
+  }
+  check(gemm_mxfp4_epilogue(&p, on.stream()));
+  return wrap(out);
+}
+
+// a, b, scale_a, scale_b, offsets, rows, bias, act, preact, out, dtype
+PyObject *mx_grouped(Args o) {
+  const Tensor &a = tensor(o[0], "a"), &b = tensor(o[1], "b"), &sb = tensor(o[3], "scale_b"), &off = tensor(o[4], "offsets");
+  On on(a, "a");
+  matrix(a, "a");
+  const ScalarType u8 = ScalarType::Byte;
+  tgemm_mxfp4_grouped_args p{};
+  const int64_t S = a.size(0);
+  p.K = 2 * a.size(1);
+  if (a.size(1) % 16) value_error("rows of a and b must be whole blocks of 16 bytes, got " + std::to_string(a.size(1)));
+  p.lda = on.mat(a, "a", u8, S, p.K / 2);
+  p.A = ptr(a);
+  p.scale_A = on.packed(tensor(o[2], "scale_a"), "scale_a", u8, {S, p.K / 32});
+  if (b.dim() != 3) value_error("b must be (groups, N, K / 2)");
+  on.typed(b, "b", u8);
+  p.groups = b.size(0);
+  p.N = b.size(1);
+  if (b.size(2) != a.size(1))
+    value_error("rows of a and b must be of one length, got " + shape_str(a.sizes()) + " and " + shape_str(b.sizes()));
+  const int64_t s1 = b.stride(1), s2 = b.stride(2);
+  if ((s2 != 1 && p.K > 2) || (p.N > 1 && s1 < p.K / 2))
+    value_error("each b[e] must be row-major (strides " + shape_str(b.strides()) + ")");
+  p.ldb = std::max(s1, p.K / 2);
+  p.stride_b = b.stride(0);
+  p.B = ptr(b);
+  on.typed(sb, "scale_b", u8);
+  on.shaped(sb, "scale_b", {p.groups, p.N, p.K / 32});
+  if ((sb.stride(2) != 1 && p.K > 32) || (sb.stride(1) != p.K / 32 && p.N > 1 && p.K > 0))
+    value_error("each scale_b[e] must be contiguous (strides " + shape_str(sb.strides()) + ")");
+  p.stride_sb = sb.stride(0);
+  p.scale_B = ptr(sb);
+  p.act = integer(o[7], "act");
+  const int64_t F = halved(p.N, p.act);
+  p.offsets = on.packed<int32_t>(off, "offsets", ScalarType::Int, {p.groups + 1});
+  p.R = p.src_rows = S;
+  if (o[5] != Py_None) {
+    const Tensor &rows = tensor(o[5], "rows");
+    p.R = rows.numel();
+    p.rows = on.packed<int32_t>(rows, "rows", ScalarType::Int, {p.R});
+  }
+  p.dtype = mx_dtype(o[10], {o[9], o[6], o[8]});
+  const ScalarType t = kTypes[p.dtype];
+  if (o[6] != Py_None) p.bias = on.packed(tensor(o[6], "bias"), "bias", t, {p.groups, p.N});
+  if (o[8] != Py_None) {
+    const Tensor &z = tensor(o[8], "preact");
+    p.ldp = on.mat(z, "preact", t, p.R, p.N);
+    p.preact = ptr(z);
+  }
+  const Tensor out = on.out(o[9], "out", t, {p.R, F});
+  p.ldc = on.mat(out, "out", t, p.R, F);
+  p.C = ptr(out);
+  check(gemm_mxfp4_grouped(&p, on.stream()));
+  return wrap(out);
+}
+
 // Runs F with the number of arguments it takes; nothing it throws gets out.
 template <PyObject *(*F)(Args), int N>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
@@ -585,6 +871,12 @@ PyMethodDef kMethods[] = {TGEMM_ENTRY("gemm_epilogue", epilogue, 8),
                           TGEMM_ENTRY("expert_gather", gather, 3),
                           TGEMM_ENTRY("expert_combine", combine, 5),
                           TGEMM_ENTRY("expert_combine_backward", combine_backward, 6),
+                          TGEMM_ENTRY("layer_norm", norm, 7),
+                          TGEMM_ENTRY("layer_norm_backward", norm_backward, 11),
+                          TGEMM_ENTRY("quantize_mxfp4", quantize, 7),
+                          TGEMM_ENTRY("dequantize_mxfp4", dequantize, 4),
+                          TGEMM_ENTRY("gemm_mxfp4_epilogue", mx_epilogue, 11),
+                          TGEMM_ENTRY("gemm_mxfp4_grouped", mx_grouped, 11),
                           {"set_error", set_error, METH_O, nullptr},
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_ffn_binding", "Compiled part of ffn.py.", -1, kMethods,

@@ -185,5 +185,102 @@ struct CombineGrad {
 };
 hipError_t launch_combine_grad(const CombineGrad &c);
 
+// Layer norm over rows.
+struct Norm {
+  int dtype, wdtype;  // 0 bf16, 1 fp16, 2 fp32
+  int64_t M, N;
+  const void *x;
+  int64_t ldx;
+  const void *weight, *bias;  // or nullptr
+  float eps;
+  void *y;
+  int64_t ldy;
+  float *mean, *rstd;  // or nullptr
+  hipStream_t stream;
+};
+hipError_t launch_norm(const Norm &n);
+
+struct NormGrad {
+  int dtype, wdtype;
+  int64_t M, N;
+  const void *dy;
+  int64_t ldd;
+  const void *x;
+  int64_t ldx;
+  const void *weight;
+  const float *mean, *rstd;
+  const void *residual;
+  int64_t ldr;
+  void *dx;
+  int64_t ldo;
+  void *dweight, *dbias;
+  float *ws;
+  hipStream_t stream;
+};
+uint64_t norm_grad_ws_floats(int64_t M, int64_t N);
+hipError_t launch_norm_grad(const NormGrad &n);
+
+// MXFP4 rows and columns of x, and back.
+struct Quant {
+  int dtype;
+  int64_t M, N;
+  const void *x;
+  int64_t ldx;
+  uint8_t *q;
+  int64_t ldq;
+  uint8_t *scales;
+  uint8_t *qt;
+  int64_t ldqt;
+  uint8_t *scalest;
+  hipStream_t stream;
+};
+hipError_t launch_quant_mxfp4(const Quant &q);
+struct Dequant {
+  int dtype;
+  int64_t M, N;
+  const uint8_t *q;
+  int64_t ldq;
+  const uint8_t *scales;
+  void *out;
+  int64_t ldo;
+  hipStream_t stream;
+};
+hipError_t launch_dequant_mxfp4(const Dequant &q);
+
+// A validated product of MXFP4 operands with an epilogue, dense (groups == 0)
+// or grouped; as Gemm, strides of A and B in bytes.
+struct MxGemm {
+  int dtype;  // of C and the epilogue's operands: 0 bf16, 1 fp16
+  int64_t M, N, K;
+  const void *A;
+  int64_t lda;
+  const void *SA;
+  const void *B;
+  int64_t ldb;
+  const void *SB;
+  const void *bias;
+  const void *residual;
+  int64_t ldr;
+  void *preact;
+  int64_t ldp;
+  void *C;
+  int64_t ldc;
+  int act;
+  int64_t groups;
+  const int32_t *offsets;
+  const int32_t *rows;
+  int64_t src_rows;
+  int64_t stride_b, stride_sb;
+  float *ws;  // dense: room for `splits` planes of M x N sums, or nullptr
+  int splits;
+  hipStream_t stream;
+  int cus;
+  int tile_m, tile_n;
+};
+hipError_t launch_mx(const MxGemm &g);        // tgemm_ffn_mx.hip
+hipError_t launch_mx_rows(const MxGemm &g);   // tgemm_ffn_mx_rows.hip
+int mx_splits(int64_t M, int64_t N, int64_t K);
+bool mx_tile_supported(const MxGemm &g, int tm, int tn);
+
 }  // namespace ffn
 }  // namespace tgemm

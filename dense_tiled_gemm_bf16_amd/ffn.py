@@ -28,7 +28,7 @@ ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4, "swiglu": 5,
 SCORES = {"softmax": 0, "sigmoid": 1}
 
 # The argument structs of include/tgemm_ffn.h, field by field in order: all
-# are 8 bytes ("scale" a double, the rest integers or pointers).
+# are 8 bytes ("scale" and "eps" doubles, the rest integers or pointers).
 _FIELDS = {
     "gemm_epilogue": "dtype trans_a trans_b M N K A lda B ldb bias residual ldr preact ldp C ldc act workspace "
                      "workspace_bytes",
@@ -42,8 +42,17 @@ _FIELDS = {
     "expert_gather": "R D src_rows x ldx rows out ldo",
     "expert_combine": "dtype T D R k h ldh slots weights residual ldr out ldo",
     "expert_combine_backward": "dtype T D R k dout ldd h ldh slots weights dh ldg dweights",
+    "layer_norm": "dtype wdtype M N x ldx weight bias eps y ldy mean rstd",
+    "layer_norm_backward": "dtype wdtype M N dy ldd x ldx weight mean rstd residual ldr dx ldo dweight dbias workspace "
+                           "workspace_bytes",
+    "quantize_mxfp4": "dtype M N x ldx q ldq scales qt ldqt scalest",
+    "dequantize_mxfp4": "dtype M N q ldq scales out ldo",
+    "gemm_mxfp4_epilogue": "dtype M N K A lda scale_A B ldb scale_B bias residual ldr preact ldp C ldc act workspace "
+                           "workspace_bytes",
+    "gemm_mxfp4_grouped": "dtype R N K groups offsets rows src_rows A lda scale_A B ldb stride_b scale_B stride_sb bias "
+                          "preact ldp C ldc act",
 }
-_PACK = {n: struct.Struct("@" + "".join("d" if f == "scale" else "q" for f in s.split())).pack
+_PACK = {n: struct.Struct("@" + "".join("d" if f in ("scale", "eps") else "q" for f in s.split())).pack
          for n, s in _FIELDS.items()}
 
 _lib = None
@@ -72,6 +81,10 @@ def lib() -> ctypes.CDLL:
     L.tgemm_epilogue_workspace_bytes.restype = ctypes.c_uint64
     for f in (L.tgemm_epilogue_backward_workspace_bytes, L.tgemm_route_plan_workspace_bytes):
         f.argtypes = [i64, i64, i64]
+        f.restype = ctypes.c_uint64
+    L.tgemm_mxfp4_workspace_bytes.argtypes = [i64, i64, i64]
+    L.tgemm_layer_norm_backward_workspace_bytes.argtypes = [i64, i64]
+    for f in (L.tgemm_mxfp4_workspace_bytes, L.tgemm_layer_norm_backward_workspace_bytes):
         f.restype = ctypes.c_uint64
     _lib = L
     return L
@@ -243,3 +256,86 @@ def expert_combine_backward(dout, h, slots, weights, dh=None, dweights=None, str
     of dh that no slot names are not written; slots are to be distinct, as a
     plan's are (a row that several name holds no sum of theirs)."""
     return _call("expert_combine_backward", dout, stream, dout, h, slots, weights, dh, dweights)
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5, mean=None, rstd=None, out=None, stream=None):
+    """(x - mean) / sqrt(var + eps) * weight + bias over the rows of x (M,N),
+    bfloat16, float16 or float32; var is the mean squared difference.
+
+    weight and bias (N,) in x's type or both float32 (None: ones, zeros).  mean
+    and rstd (M,) float32, if given, receive each row's mean and 1 / sqrt(var +
+    eps), for layer_norm_backward.  out may be x.
+    """
+    return _call("layer_norm", x, stream, x, weight, bias, eps, mean, rstd, out)
+
+
+def layer_norm_backward(dout, x, weight, mean, rstd, residual=None, want_dweight=True, dx=None, dweight=None, dbias=None,
+                        workspace=None, stream=None):
+    """Gradients of layer_norm: (dx, dweight, dbias).
+
+    mean, rstd: as layer_norm left them; weight as there (None: ones).
+    residual (M,N), if given, is added to dx (a gradient that reaches x another
+    way).  dweight and dbias (N,) have the weight's type (x's without one); None
+    if not wanted.  dx may be dout, x or residual.  workspace: a uint8
+    tensor of tgemm_layer_norm_backward_workspace_bytes; allocated when None.
+    """
+    return _call("layer_norm_backward", x, stream, dout, x, weight, mean, rstd, residual, want_dweight, dx, dweight, dbias,
+                 workspace)
+
+
+def quantize_mxfp4(x, rows=True, columns=False, q=None, scales=None, qt=None, scalest=None, stream=None):
+    """MXFP4 operands of x (M,N), bfloat16, float16 or float32.
+
+    rows: (q (M,N/2), scales (M,N/32)), uint8, as gemm_mxfp4_nt and
+    gemm_mxfp4_epilogue take them, one scale per 32 values of a row.  columns:
+    (qt (N,P/2), scalest (N,P/32)), the same of x.t(), zeros behind its M
+    values up to P, M rounded up to 32: what the products of a backward pass
+    take.  Both, in one read of x: (q, scales, qt, scalest).  A block with an
+    infinity or a NaN becomes NaN.
+    """
+    return _call("quantize_mxfp4", x, stream, x, rows, columns, q, scales, qt, scalest)
+
+
+def _dtype(dtype):
+    torch = _torch()
+    code = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(dtype)
+    if code is None:
+        raise TypeError(f"dtype must be torch.bfloat16, torch.float16 or torch.float32, got {dtype!r}")
+    return code
+
+
+def dequantize_mxfp4(q, scales, dtype=None, out=None, stream=None):
+    """The values of MXFP4 rows q (M,N/2), scales (M,N/32): (M,N) in dtype
+    (torch.bfloat16 when None; out's if one is given), which holds each exactly
+    unless it is float16."""
+    return _call("dequantize_mxfp4", q, stream, q, scales, -1 if dtype is None else _dtype(dtype), out)
+
+
+def gemm_mxfp4_epilogue(a, b, scale_a, scale_b, bias=None, act="none", residual=None, preact=None, out=None, dtype=None,
+                        workspace=None, stream=None):
+    """act(a @ b.T + bias) + residual on MXFP4 operands: gemm_epilogue's epilogue on
+    gemm_mxfp4_nt's product, for any M from 1.
+
+    a (M,K/2), b (N,K/2): packed E2M1 bytes (uint8), rows of any stride that is a
+    multiple of 16; scale_a (M,K/32), scale_b (N,K/32): e8m0 bytes, contiguous.
+    bias, act, residual, preact as in gemm_epilogue, in dtype (bfloat16 or
+    float16; when None that of out, bias, residual or preact, else bfloat16).
+    workspace: for a K split, tgemm_mxfp4_workspace_bytes bytes (with less
+    there is none); allocated when None.
+    """
+    return _call("gemm_mxfp4_epilogue", a, stream, a, b, scale_a, scale_b, bias, _act(act), residual, preact, out,
+                 -1 if dtype is None else _dtype(dtype), workspace)
+
+
+def gemm_mxfp4_grouped(a, b, scale_a, scale_b, offsets, rows=None, bias=None, act="none", preact=None, out=None, dtype=None,
+                       stream=None):
+    """gemm_grouped on MXFP4 operands: out[r] = act(a[rows[r]] @ b[e].T + bias[e])
+    for each row r of group e.
+
+    a (S,K/2), scale_a (S,K/32); b (E,N,K/2), scale_b (E,N,K/32), each
+    scale_b[e] contiguous; offsets, rows, bias, act, preact, out as in
+    gemm_grouped, dtype as in gemm_mxfp4_epilogue.  Rows in no group are not
+    written.
+    """
+    return _call("gemm_mxfp4_grouped", a, stream, a, b, scale_a, scale_b, offsets, rows, bias, _act(act), preact, out,
+                 -1 if dtype is None else _dtype(dtype))

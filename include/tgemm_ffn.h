@@ -2,7 +2,8 @@
  * tgemm_ffn -- the operators of a model's feed-forward layers around the
  * dense products of tgemm.h, for AMD Instinct MI355X (gfx950): the product
  * with bias, activation and residual in its epilogue, the routing of tokens to
- * experts, and the experts' products, each with its backward pass.
+ * experts, the experts' products and the layer norm, each with its backward
+ * pass; and the products on 4-bit operands (MXFP4), with their quantisation.
  *
  * C ABI of the library libtgemm_ffn.so.  Conventions are those of tgemm.h:
  * row-major matrices, plain device pointers, the caller owns every buffer
@@ -15,8 +16,8 @@
  * tgemm_ffn_last_error() describes the failure of the calling thread.
  *
  * Arguments come in structs of 8-byte fields; a field that does not apply is
- * 0 or NULL.  Element types: TGEMM_DT_BF16, TGEMM_DT_F16 and, for logits,
- * TGEMM_DT_F32.  Sums are held in 32 bits; each output is rounded once, to
+ * 0 or NULL.  Element types: TGEMM_DT_BF16, TGEMM_DT_F16 and, for logits, norms
+ * and quantisation, TGEMM_DT_F32.  Sums are held in 32 bits; each output is rounded once, to
  * nearest even.  16-bit tensors are 16-byte aligned with row strides and
  * contiguous dimensions that are multiples of 8 (TGEMM_EALIGN otherwise).
  * An output may overlap no other argument, except where said.  Sizes (and T k)
@@ -301,6 +302,171 @@ typedef struct {
   float *dweights;
 } tgemm_expert_combine_backward_args;
 TGEMM_API int expert_combine_backward(const tgemm_expert_combine_backward_args *args, hipStream_t stream);
+
+/*
+ * Layer norm over rows of N values: y = (x - mean) * rstd * weight + bias with
+ * mean = sum(x) / N and rstd = 1 / sqrt(sum((x - mean)^2) / N + eps).
+ *
+ *   x, y     M x N of type dtype (BF16, F16 or F32); y may be x itself (same
+ *            pointer and stride)
+ *   weight, bias   N values of type wdtype (dtype or F32), or NULL: ones, zeros
+ *   mean, rstd     M binary32 each, for the backward pass, or NULL
+ * Sums are binary32, the variance's over differences from the mean.  Binary32
+ * tensors are 16-byte aligned too, with strides that are multiples of 8.
+ * N >= 8; eps finite and not negative (0: a row of equal values gives NaN or
+ * infinity, as the formula does).
+ */
+typedef struct {
+  int64_t dtype, wdtype, M, N;
+  const void *x;
+  int64_t ldx;
+  const void *weight;
+  const void *bias;
+  double eps;
+  void *y;
+  int64_t ldy;
+  float *mean;
+  float *rstd;
+} tgemm_layer_norm_args;
+TGEMM_API int layer_norm(const tgemm_layer_norm_args *args, hipStream_t stream);
+
+/*
+ * Its gradients.  With g = dy * weight and h = (x - mean) * rstd:
+ *   dx = rstd * (g - mean(g) - h * mean(g * h)) + residual
+ *   dweight = column sums of dy * h, dbias = column sums of dy (type wdtype;
+ *   either may be NULL; M = 0: zeros)
+ * mean, rstd: as layer_norm gave them.  residual (M x N of dtype, or NULL): a
+ * gradient that reaches x another way.  dx may be dy, x or residual itself
+ * (same pointer and stride).
+ * workspace: tgemm_layer_norm_backward_workspace_bytes(M, N) bytes, 16-byte
+ * aligned; its sums are added in a fixed order.
+ */
+typedef struct {
+  int64_t dtype, wdtype, M, N;
+  const void *dy;
+  int64_t ldd;
+  const void *x;
+  int64_t ldx;
+  const void *weight;
+  const float *mean;
+  const float *rstd;
+  const void *residual;
+  int64_t ldr;
+  void *dx;
+  int64_t ldo;
+  void *dweight;
+  void *dbias;
+  void *workspace;
+  uint64_t workspace_bytes;
+} tgemm_layer_norm_backward_args;
+TGEMM_API int layer_norm_backward(const tgemm_layer_norm_backward_args *args, hipStream_t stream);
+TGEMM_API uint64_t tgemm_layer_norm_backward_workspace_bytes(int64_t M, int64_t N);
+
+/*
+ * MXFP4, as gemm_mxfp4_nt takes it (tgemm.h): OCP E2M1 elements, two a byte
+ * (element 2 i in the low nibble of byte i), one e8m0 scale byte per 32
+ * consecutive elements of a row.  Rows of element bytes are 16-byte aligned,
+ * ld bytes apart (a multiple of 16); scales are packed, in any alignment.
+ *
+ * Quantisation of x (M x N of type dtype: BF16, F16 or F32) along its rows,
+ * along its columns, or both in one read of it:
+ *   q   M x N / 2 bytes, scales M x N / 32: x's rows (or NULL, both)
+ *   qt  N x P / 2 bytes, scalest N x P / 32, P = M rounded up to 32: x's
+ *       columns, as rows, zeros behind the M values (or NULL, both)
+ * A block's scale 2^e is the least power of two with max|x| <= 6 * 2^e, e
+ * clamped to -127 .. 127 (-127 for zeros), stored as e + 127; an element is
+ * x * 2^-e rounded once, to nearest even, its sign kept (zeros' too).  A block
+ * that holds an infinity or a NaN has the scale byte 255 (a NaN: every product
+ * with it is one) and elements 0.
+ * N % 32 == 0 with q, N % 8 == 0 without.
+ */
+typedef struct {
+  int64_t dtype, M, N;
+  const void *x;
+  int64_t ldx;
+  void *q;
+  int64_t ldq;
+  void *scales;
+  void *qt;
+  int64_t ldqt;
+  void *scalest;
+} tgemm_quantize_mxfp4_args;
+TGEMM_API int quantize_mxfp4(const tgemm_quantize_mxfp4_args *args, hipStream_t stream);
+
+/*
+ * What MXFP4 rows stand for: out[m][n] = element * 2^(scale - 127), M x N of
+ * type dtype (BF16 and F32 hold every value exactly, F16 rounds to nearest even);
+ * NaN where the scale byte is 255.  N % 32 == 0.
+ */
+typedef struct {
+  int64_t dtype, M, N;
+  const void *q;
+  int64_t ldq;
+  const void *scales;
+  void *out;
+  int64_t ldo;
+} tgemm_dequantize_mxfp4_args;
+TGEMM_API int dequantize_mxfp4(const tgemm_dequantize_mxfp4_args *args, hipStream_t stream);
+
+/*
+ * gemm_epilogue on MXFP4 operands: C = act(Z) + residual, Z = A . B^T + bias,
+ * A M x K and B N x K as above (lda, ldb in bytes), C, bias, residual and
+ * preact of type dtype (BF16 or F16).  K % 32 == 0.
+ * workspace: for a K split, tgemm_mxfp4_workspace_bytes(M, N, K) bytes,
+ * 16-byte aligned; with less, or NULL, there is none.
+ * Limits: 256 lda < 2^31 and 256 ldb < 2^31; gated, (N / 2 + 256) ldb < 2^31.
+ */
+typedef struct {
+  int64_t dtype, M, N, K;
+  const void *A;
+  int64_t lda;
+  const void *scale_A;
+  const void *B;
+  int64_t ldb;
+  const void *scale_B;
+  const void *bias;
+  const void *residual;
+  int64_t ldr;
+  void *preact;
+  int64_t ldp;
+  void *C;
+  int64_t ldc;
+  int64_t act;
+  void *workspace;
+  uint64_t workspace_bytes;
+} tgemm_mxfp4_epilogue_args;
+TGEMM_API int gemm_mxfp4_epilogue(const tgemm_mxfp4_epilogue_args *args, hipStream_t stream);
+TGEMM_API uint64_t tgemm_mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/*
+ * gemm_grouped on MXFP4 operands: for each row r of group e, C[r] = act(A[s] .
+ * B_e^T + bias_e) with s = rows[r], or r if rows is NULL.  A and its scales
+ * have src_rows rows (R if rows is NULL); an s outside them reads zeros.  B_e
+ * is N x K at B + e stride_b bytes (a multiple of 16), its scales at scale_B +
+ * e stride_sb bytes.
+ * Limits: with rows, src_rows lda < 2^31; else 256 lda < 2^31; B_e as in
+ * gemm_mxfp4_epilogue.
+ */
+typedef struct {
+  int64_t dtype, R, N, K, groups;
+  const int32_t *offsets;
+  const int32_t *rows;
+  int64_t src_rows;
+  const void *A;
+  int64_t lda;
+  const void *scale_A;
+  const void *B;
+  int64_t ldb, stride_b;
+  const void *scale_B;
+  int64_t stride_sb;
+  const void *bias;
+  void *preact;
+  int64_t ldp;
+  void *C;
+  int64_t ldc;
+  int64_t act;
+} tgemm_mxfp4_grouped_args;
+TGEMM_API int gemm_mxfp4_grouped(const tgemm_mxfp4_grouped_args *args, hipStream_t stream);
 
 #ifdef __cplusplus
 }
