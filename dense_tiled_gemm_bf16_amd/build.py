@@ -23,6 +23,7 @@ FFN_SOURCES = [os.path.join(CSRC, "tgemm_ffn_gemm_bf16.hip"), os.path.join(CSRC,
                os.path.join(CSRC, "tgemm_ffn_gemm.hip"), os.path.join(CSRC, "tgemm_ffn_rows.hip"),
                os.path.join(CSRC, "tgemm_ffn_rowops.hip"), os.path.join(CSRC, "tgemm_ffn_route.hip"),
                os.path.join(CSRC, "tgemm_ffn_norm.hip"), os.path.join(CSRC, "tgemm_ffn_quant.hip"),
+               os.path.join(CSRC, "tgemm_ffn_mx_bf16.hip"), os.path.join(CSRC, "tgemm_ffn_mx_f16.hip"),
                os.path.join(CSRC, "tgemm_ffn_mx_rows.hip"), os.path.join(CSRC, "tgemm_ffn_mx.hip"),
                os.path.join(CSRC, "tgemm_ffn_abi.cpp")]
 BINDING = os.path.join(PKG, "_ffn_binding.so")

@@ -278,7 +278,13 @@ struct MxGemm {
   int tile_m, tile_n;
 };
 hipError_t launch_mx(const MxGemm &g);        // tgemm_ffn_mx.hip
-hipError_t launch_mx_rows(const MxGemm &g);   // tgemm_ffn_mx_rows.hip
+hipError_t launch_mx_rows(const MxGemm &g);   // tgemm_ffn_mx_rows.hip: few rows for each weight
+hipError_t launch_mx_bf16(const MxGemm &g, int tm);  // tgemm_ffn_mx_bf16.hip: tiles of tm x tm
+hipError_t launch_mx_f16(const MxGemm &g, int tm);   // tgemm_ffn_mx_f16.hip
+// Whether every row's scales start on a dword.
+inline bool mx_scales_aligned(const MxGemm &g) {
+  return g.K % 128 == 0 && ((uintptr_t)g.SA | (uintptr_t)g.SB | (uintptr_t)(g.groups ? g.stride_sb : 0)) % 4 == 0;
+}
 int mx_splits(int64_t M, int64_t N, int64_t K);
 bool mx_tile_supported(const MxGemm &g, int tm, int tn);
 

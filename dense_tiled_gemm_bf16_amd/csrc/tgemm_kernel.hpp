@@ -130,6 +130,7 @@ struct Traits {
   static constexpr int kSliceBytes = 128;                  // global bytes of a row per K slice (fp6: line stage)
   static constexpr int kPitch = kSliceBytes;               // LDS bytes of a slot row
   static constexpr bool kAK = AK, kBK = BK;
+  static constexpr bool kOutF16 = DT == kF16;  // C is fp16, else bf16
 };
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void *base, uint32_t bytes) {
@@ -268,19 +269,19 @@ struct PanelLoader {
   }
 
   // The same for a panel whose row r (of the tile) is row row_of(r) of an
-  // array of `rows` rows at X: negative or past the array, zeros.  16-bit
-  // elements.  (The resource spans the array, so that of a gathered panel
+  // array of `rows` rows at X: negative or past the array, zeros.  Elements
+  // of E bytes.  (The resource spans the array, so that of a gathered panel
   // has to fit 31-bit offsets as a whole.)
-  template <class F>
+  template <int E, class F>
   __device__ __forceinline__ void init_rows(const uint8_t *X, int K, int ld, int wave, int lane, int rows, F row_of) {
     slice_bytes = 128;
-    rsrc = make_rsrc(X, rows > 0 && K > 0 ? ((uint32_t)(rows - 1) * (uint32_t)ld + (uint32_t)K) * 2u : 0u);
+    rsrc = make_rsrc(X, rows > 0 && K > 0 ? ((uint32_t)(rows - 1) * (uint32_t)ld + (uint32_t)K) * (uint32_t)E : 0u);
 #pragma unroll
-    for (int p = 0; p < 2; ++p) kcol[p] = ((lane & 7) ^ swz(8 * p + (lane >> 3))) * 8;
+    for (int p = 0; p < 2; ++p) kcol[p] = ((lane & 7) ^ swz(8 * p + (lane >> 3))) * (16 / E);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int64_t g = row_of(wave * 8 * NI + i * 8 + (lane >> 3));
-      off[i] = g >= 0 && g < rows ? (uint32_t)g * (uint32_t)ld * 2u + (uint32_t)kcol[i & 1] * 2u : kOOB;
+      off[i] = g >= 0 && g < rows ? (uint32_t)g * (uint32_t)ld * (uint32_t)E + (uint32_t)kcol[i & 1] * (uint32_t)E : kOOB;
     }
   }
 
@@ -510,7 +511,8 @@ struct NoExt {
 template <class T, int TM, int TN, bool SPLIT = false, class EXT = NoExt>
 struct Kernel {
   static_assert(!SPLIT || !T::kScaled, "the K split is for the 16-bit kinds");
-  static_assert(!EXT::kOn || (!SPLIT && !T::kScaled), "extensions are for the 16-bit kinds without a K split");
+  static_assert(!EXT::kOn || (!SPLIT && (!T::kScaled || (T::kDt == kFp4 && T::kWholeK))),
+                "extensions are for the 16-bit kinds without a K split and for fp4 with aligned scales");
   static constexpr int kNS = kSlots<T, TM, TN>;
   static constexpr int kElem = T::kElem;
   static constexpr int kWM = TM / 2, kWN = TN / 2;   // wave tile (2 x 2 waves)
@@ -689,6 +691,25 @@ struct Kernel {
   static constexpr int kStageBytes = kA4 ? 2 * 512 * 32 : T::kDt == kFp4 ? 3 * 512 * 16 : 512 * 32;
   static constexpr int kChunkStride = 16;  // row bytes between consecutive chunks
   uint32_t st_off;
+  static constexpr bool kStRows = kA4 && EXT::kGather;
+  uint32_t st_rows[4];  // kStRows: the offsets of all four load instructions' rows
+  // What an extension says of its rows (the others have none).
+  __device__ __forceinline__ bool ext_rows() const {
+    if constexpr (EXT::kGather) return x.rows != nullptr;
+    return false;
+  }
+  __device__ __forceinline__ int ext_row(int r) const {
+    if constexpr (EXT::kGather) return x.rows[r];
+    return -1;
+  }
+  __device__ __forceinline__ int ext_src_rows() const {
+    if constexpr (EXT::kGather) return x.src_rows;
+    return 0;
+  }
+  __device__ __forceinline__ int ext_half() const {
+    if constexpr (EXT::kGated) return x.half;
+    return 0;
+  }
   // fp4 (rows not dword-aligned): lane l = 16 g + r converts row r of
   // blocks 4 g .. 4 g + 3 (x blocks 0-7, then y blocks 0-7): sh4, the byte
   // shift of those rows inside a dword (16 rows apart, so the same for all
@@ -1063,9 +1084,15 @@ struct Kernel {
   // its slot after the next barrier and published by the one after.
   __device__ __forceinline__ void load_group4(int g) {
     const __amdgpu_buffer_rsrc_t r = (wave >> 1) ? rss[1] : rss[0];
+    if constexpr (kStRows) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      sv4[i] = __builtin_amdgcn_raw_buffer_load_b128(r, st_off, (uint32_t)(2 * kChunkStride * g + 32 * i * a.kb), 0);
+      for (int i = 0; i < 4; ++i) sv4[i] = __builtin_amdgcn_raw_buffer_load_b128(r, st_rows[i], (uint32_t)(2 * kChunkStride * g), 0);
+    } else {
+      const int step = EXT::kGated && wave < 2 ? 16 : 32;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        sv4[i] = __builtin_amdgcn_raw_buffer_load_b128(r, st_off, (uint32_t)(2 * kChunkStride * g + step * i * a.kb), 0);
+    }
   }
   __device__ __forceinline__ void store_group4(int g) {
     // The bytes stage_group would have written: chunk q of row 32 i + r of
@@ -1394,7 +1421,7 @@ struct Kernel {
       ;  // fp6 sets up its own loads (run6)
     else if constexpr (EXT::kGather) {
       if (x.rows)
-        la.init_rows(a.A, a.K, a.lda, wave, lane, x.src_rows, [&](int r) -> int64_t {
+        la.template init_rows<kElem>(a.A, a.K, a.lda, wave, lane, x.src_rows, [&](int r) -> int64_t {
           return r < min(a.M - m0, TM) ? x.rows[m0 + r] : -1;
         });
       else
@@ -1409,7 +1436,7 @@ struct Kernel {
       // LDS row r: block r / 16; the resource starts at the tile's first
       // column of the first half and ends with its last of the second.
       const int cols = min(a.N - n0, TN / 2);
-      lb.init_rows(a.B + (size_t)n0 * a.ldb * kElem, a.K, a.ldb, wave, lane, x.half + cols, [&](int r) -> int64_t {
+      lb.template init_rows<kElem>(a.B + (size_t)n0 * a.ldb * kElem, a.K, a.ldb, wave, lane, x.half + cols, [&](int r) -> int64_t {
         const int c = ((r >> 5) << 4) + (r & 15);
         return c < cols ? c + ((r >> 4) & 1 ? x.half : 0) : -1;
       });
@@ -1439,9 +1466,12 @@ struct Kernel {
       // byte, so in the same page).
 #pragma unroll
       for (int op = 0; op < 2; ++op) {
-        const uintptr_t start = (uintptr_t)(op ? a.SA + (size_t)m0 * a.kb : a.SB + (size_t)n0 * a.kb);
+        const bool gather = EXT::kGather && op && ext_rows();
+        const uintptr_t start = (uintptr_t)(op ? a.SA + (gather ? (size_t)0 : (size_t)m0 * a.kb) : a.SB + (size_t)n0 * a.kb);
         const uint32_t mis = (uint32_t)(start & 3);
-        const int rows_valid = op ? min(a.M - m0, TM) : min(a.N - n0, TN);
+        const int rows_valid = gather ? ext_src_rows()
+                               : op   ? min(a.M - m0, TM)
+                                      : (EXT::kGated ? ext_half() + min(a.N - n0, TN / 2) : min(a.N - n0, TN));
         rss[op] = make_rsrc((const void *)(start - mis), (mis + (uint32_t)rows_valid * (uint32_t)a.kb + 3) & ~3u);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -1453,10 +1483,27 @@ struct Kernel {
         }
         if constexpr (kA4) {
           if (op == (wave >> 1)) {
-            // As fp6: rows r + 32, r + 64, r + 96 are 32 kb bytes apart.
-            const int r = (wave & 1) * 128 + (lane & 31);
+            // As fp6: rows r + 32, r + 64, r + 96 are 32 kb bytes apart (16 kb
+            // in a gated weight, whose 16-row blocks alternate between halves).
+            int r = (wave & 1) * 128 + (lane & 31);
+            if constexpr (EXT::kGated)
+              if (!op) r = ((r >> 5) << 4) + (r & 15) + ((r >> 4) & 1) * ext_half();
             const uint32_t pos = (uint32_t)r * (uint32_t)a.kb;
             st_off = r < rows_valid ? pos + (uint32_t)(kChunkStride * (lane >> 5)) : kOOB;
+            if constexpr (kStRows) {
+              // Gathered rows lie anywhere: an offset for each.
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if (gather) {
+                  const int row = m0 + r + 32 * i;
+                  const int src = row < a.M ? ext_row(row) : -1;
+                  st_rows[i] = src >= 0 && src < rows_valid ? (uint32_t)src * (uint32_t)a.kb + (uint32_t)(kChunkStride * (lane >> 5))
+                                                            : kOOB;
+                } else {
+                  st_rows[i] = st_off == kOOB ? kOOB : st_off + (uint32_t)((EXT::kGated && !op ? 16 : 32) * i * a.kb);
+                }
+              }
+            }
           }
           // Lane 16 g + r reads rows 64 (g % 2) + 16 k + r of the wave's x
           // rows (g < 2) or y rows: 32-row block op 8 + 4 wave + 2 (g % 2)
@@ -2144,7 +2191,7 @@ struct Kernel {
     const f32x2 lo = {c[r0], c[r0 + 1]};
     const f32x2 up = {c[r0 + 2], c[r0 + 3]};
     u32x2 pk;
-    if constexpr (T::kDt == kF16) {
+    if constexpr (T::kOutF16) {
       pk[0] = __builtin_bit_cast(uint32_t, __builtin_convertvector(lo, f16x2));
       pk[1] = __builtin_bit_cast(uint32_t, __builtin_convertvector(up, f16x2));
     } else {
