@@ -22,7 +22,7 @@ typedef __attribute__((ext_vector_type(8))) int v8i;
 
 struct MxSlots {
   LDS_AS uint8_t *a[4], *b[4];  // kNS slots of TM, TN rows x 256 bytes
-  LDS_AS uint8_t *s[4];         // their scales: 256 bytes per 16 rows (B's blocks first), then the dwords behind them
+  LDS_AS uint8_t *s[4];         // their scales: 16 bytes of a row (B's rows first), then from 4 bytes on
 };
 
 // MxTile: TM x TN of C by 4 waves (2 x 2), K in slices of 512 elements (256
@@ -33,9 +33,11 @@ struct MxSlots {
 // elements.  Over the four products of a slice lane group g = l / 16 takes
 // blocks 4 g .. 4 g + 3, block 4 g + s in product s, of both operands alike:
 // its four scales of a slice are then one dword, byte s for product s, and no
-// scale moves between lanes.  A slot row keeps block 4 g + s at 16-byte chunk
-// (4 s + g) ^ (row % 16): 16 rows at one chunk, and 4 chunks of 4 rows, fall
-// on different LDS banks.
+// scale moves between lanes.  A slot row keeps block c at 16-byte chunk c ^
+// perm(row % 16): the rows of a fragment read fall on different LDS banks, and
+// four lanes side by side load 64 bytes side by side.  (With the chunks of one
+// product side by side instead, four lanes loaded from four places: 24 bytes a
+// clock and CU at most.)
 //
 // ALIGNED: every row's scales start on a dword.  If not, a lane loads the
 // dword that holds its first scale and the one behind, and shifts.
@@ -45,11 +47,12 @@ struct MxTile {
   static constexpr int kWM = TM / 2, kWN = TN / 2, kNBm = kWM / 16, kNBn = kWN / 16;
   static constexpr int kNS = TM * TN <= 64 * 64 ? 4 : 2;
   static constexpr int kLA = TM / 16, kLB = TN / 16;     // row load instructions of a wave and slice (4 rows each)
-  static constexpr int kScaleBlocks = (TM + TN) / 16;    // scale load instructions of a slice, 16 rows each
-  static constexpr int kLS = kScaleBlocks / 4, kPlanes = ALIGNED ? 1 : 2;
-  static constexpr int kLoads = kLA + kLB + kLS * kPlanes;
-  static constexpr int kScaleBytes = kScaleBlocks * 256 * kPlanes;
-  static_assert(kLA % 4 == 0 && kLB % 4 == 0 && kScaleBlocks % 4 == 0, "whole instructions");
+  // Scale loads: 64 rows an instruction, 16 bytes (those of a slice) each, one
+  // instruction a wave (the rows past TM + TN: nothing).
+  static constexpr int kPlanes = ALIGNED ? 1 : 2, kPlane = 4 * 1024;
+  static constexpr int kLoads = kLA + kLB + kPlanes;
+  static constexpr int kScaleBytes = kPlane * kPlanes;
+  static_assert(kLA % 4 == 0 && kLB % 4 == 0 && TN % 64 == 0 && TM + TN <= 256, "whole instructions");
   static_assert((kNS - 1) * kLoads < 64, "vmcnt is 6 bits");
 
   const Args &a;
@@ -59,12 +62,14 @@ struct MxTile {
   __amdgpu_buffer_rsrc_t ra, rb, rsa, rsb;
   uint32_t offa[kLA], offb[kLB];
   int kcol[4];             // this lane's byte in a slice row, by instruction % 4
-  uint32_t offs[kLS];      // aligned offset of this lane's scales in slice 0
+  uint32_t offs;           // aligned offset of this lane's row of scales in slice 0
   uint32_t sh_x[2], sh_y[EXT::kGather ? kNBm : 1];  // where this lane's scales start in their dword
   uint32_t frag;           // this lane's chunk of product 0
   f32x4 acc[kNBn][kNBm];
 
   __device__ __forceinline__ MxTile(const Args &args, const MxSlots &s, const EXT &ext) : a(args), slots(s), x(ext) {}
+
+  __device__ static __forceinline__ int perm(int r) { return r ^ ((r & 4) << 1); }
 
   // Row of B (from the tile's first on) that LDS row r holds, or -1.
   __device__ __forceinline__ int b_row(int r) const {
@@ -115,8 +120,7 @@ struct MxTile {
     // the wave's rows, whose number % 16 goes by i % 4.
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-      const int q = r ^ (4 * p + g);                  // chunk before the row's permutation: 4 s + g
-      kcol[p] = 16 * (4 * (q & 3) + (q >> 2));
+      kcol[p] = 16 * (r ^ perm(4 * p + g));
     }
 #pragma unroll
     for (int i = 0; i < kLA; ++i) {
@@ -128,14 +132,11 @@ struct MxTile {
       const int row = b_row(4 * (wave * kLB + i) + g);
       offb[i] = row >= 0 ? (uint32_t)row * (uint32_t)a.ldb + (uint32_t)kcol[i & 3] : kOOB;
     }
-    // Scales: instruction i of wave w takes 16-row block kLS w + i, lane l the
-    // dword of row l % 16 and lane group l / 16.
-#pragma unroll
-    for (int i = 0; i < kLS; ++i) {
-      const int b = wave * kLS + i;
-      const bool isb = b < kLB;
-      const int row = isb ? b_row(16 * b + r) : a_row(16 * (b - kLB) + r);
-      offs[i] = row >= 0 ? ((isb ? mis_b : mis_a) + (uint32_t)row * (uint32_t)a.kb + 4u * (uint32_t)g) & ~3u : kOOB;
+    // Scales: lane l of wave w takes row 64 w + l of B's and A's together.
+    {
+      const bool isb = wave < TN / 64;
+      const int row = isb ? b_row(64 * wave + lane) : a_row(64 * wave - TN + lane);
+      offs = row >= 0 ? ((isb ? mis_b : mis_a) + (uint32_t)row * (uint32_t)a.kb) & ~3u : kOOB;
     }
     if constexpr (!ALIGNED) {
       // (16 rows are 16 kb bytes: one shift for all blocks, of each half.)
@@ -149,7 +150,7 @@ struct MxTile {
         sh_y[0] = (mis_a + (uint32_t)r * (uint32_t)a.kb) & 3u;
       }
     }
-    frag = (uint32_t)(r * 256 + ((g ^ r) << 4));
+    frag = (uint32_t)(r * 256 + (((4 * g) ^ perm(r)) << 4));
 #pragma unroll
     for (int i = 0; i < kNBn; ++i)
 #pragma unroll
@@ -160,110 +161,183 @@ struct MxTile {
     return 0;
   }
 
-  // Every load of slice kt into slot S.  Slices past whole ones check columns:
-  // what lies past K arrives as zeros, and a slice past the last is all zeros.
-  template <int S>
-  __device__ __forceinline__ void load(int kt) const {
-    const uint32_t so = (uint32_t)kt * 256u;
+  // Load I of slice kt into slot S.  The last slices check columns: what lies
+  // past K arrives as zeros, and a slice past the last is all zeros.
+  template <int S, int I>
+  __device__ __forceinline__ void load_one(int kt) const {
     const int left = a.K - kt * 256;  // bytes of a row from this slice on
     const bool whole = left >= 256;
-#pragma unroll
-    for (int i = 0; i < kLA; ++i) {
-      const uint32_t v = whole || kcol[i & 3] < left ? offa[i] : kOOB;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (LDS_AS void *)(slots.a[S] + (wave * kLA + i) * 1024), 16, v, so, 0, 0);
+    if constexpr (I < kLA + kLB) {
+      constexpr bool isb = I >= kLA;
+      constexpr int i = isb ? I - kLA : I;
+      const uint32_t v = whole || kcol[i & 3] < left ? (isb ? offb[i % kLB] : offa[i % kLA]) : kOOB;
+      LDS_AS uint8_t *dst = (isb ? slots.b[S] : slots.a[S]) + (wave * (isb ? kLB : kLA) + i) * 1024;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(isb ? rb : ra, (LDS_AS void *)dst, 16, v, (uint32_t)kt * 256u, 0, 0);
+    } else {
+      constexpr int p = I - kLA - kLB;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wave < TN / 64 ? rsb : rsa,
+                                               (LDS_AS void *)(slots.s[S] + p * kPlane + wave * 1024), 16,
+                                               left > 0 ? offs : kOOB, (uint32_t)kt * 16u + 4u * (uint32_t)p, 0, 0);
     }
-#pragma unroll
-    for (int i = 0; i < kLB; ++i) {
-      const uint32_t v = whole || kcol[i & 3] < left ? offb[i] : kOOB;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (LDS_AS void *)(slots.b[S] + (wave * kLB + i) * 1024), 16, v, so, 0, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < kLS; ++i) {
-      const int b = wave * kLS + i;
-      const __amdgpu_buffer_rsrc_t rs = b < kLB ? rsb : rsa;
-      const uint32_t v = left > 0 ? offs[i] : kOOB;
-#pragma unroll
-      for (int p = 0; p < kPlanes; ++p)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LDS_AS void *)(slots.s[S] + (p * kScaleBlocks + b) * 256), 4, v,
-                                                 (uint32_t)kt * 16u + 4u * (uint32_t)p, 0, 0);
-    }
+  }
+  template <int S, int... I>
+  __device__ __forceinline__ void load_some(std::integer_sequence<int, I...>, int kt) const {
+    (load_one<S, I>(kt), ...);
   }
 
-  // This lane's scales of 16-row block b in slot S.
-  template <int S>
-  __device__ __forceinline__ uint32_t scale(int b, uint32_t sh, uint32_t keep) const {
-    const LDS_AS uint8_t *p = slots.s[S] + b * 256 + lane * 4;
-    uint32_t w = *(const LDS_AS uint32_t *)p;
-    if constexpr (!ALIGNED) w = __builtin_amdgcn_alignbyte(*(const LDS_AS uint32_t *)(p + kScaleBlocks * 256), w, sh);
-    return w & keep;
+  struct Frags {
+    u32x4 x[kNBn], y[kNBm];
+  };
+  struct Scales {
+    uint32_t x[kNBn], y[kNBm];
+  };
+  static constexpr int kPer = kNBn * kNBm, kNR = kNBn + kNBm;  // MFMAs and fragment reads of a product
+  // Fragment R (x blocks, then y blocks) of product P from slot S.
+  template <int S, int P, int R>
+  __device__ __forceinline__ void read_frag(Frags &f) const {
+    const uint32_t at = frag ^ (uint32_t)(P << 4);
+    if constexpr (R < kNBn)
+      f.x[R] = *(const LDS_AS u32x4 *)(slots.b[S] + (wave_n * kWN + 16 * R) * 256 + at);
+    else
+      f.y[R - kNBn] = *(const LDS_AS u32x4 *)(slots.a[S] + (wave_m * kWM + 16 * (R - kNBn)) * 256 + at);
   }
+  // This lane's scales of block R in slot S, of slice kt.  Bytes behind the
+  // row's last are the next row's: a NaN among them would meet the zeros past K.
+  template <int S, int R>
+  __device__ __forceinline__ void read_scale(Scales &c, int kt) const {
+    const int b = R < kNBn ? wave_n * kNBn + R : kLB + wave_m * kNBm + R - kNBn;
+    const LDS_AS uint8_t *p = slots.s[S] + b * 256 + 16 * (lane & 15) + 4 * (lane >> 4);
+    uint32_t w = *(const LDS_AS uint32_t *)p;
+    if constexpr (!ALIGNED) {
+      const uint32_t sh = R < kNBn ? sh_x[EXT::kGated ? R & 1 : 0] : sh_y[EXT::kGather ? (R < kNBn ? 0 : R - kNBn) : 0];
+      w = __builtin_amdgcn_alignbyte(*(const LDS_AS uint32_t *)(p + kPlane), w, sh);
+    }
+    const int left = a.kb - 16 * kt - 4 * (lane >> 4);
+    if (a.kb < 16 * kt + 16) w &= left >= 4 ? ~0u : left <= 0 ? 0u : ~0u >> (32 - 8 * left);
+    (R < kNBn ? c.x[R % kNBn] : c.y[(R - kNBn + kNBm) % kNBm]) = w;
+  }
+  template <int S, int... R>
+  __device__ __forceinline__ void read_first(std::integer_sequence<int, R...>, Frags &f, Scales &c, int kt) const {
+    (read_frag<S, 0, R>(f), ...);
+    (read_scale<S, R>(c, kt), ...);
+  }
+
   template <int SEL>
   __device__ static __forceinline__ f32x4 mma(const u32x4 &p, const u32x4 &q, const f32x4 &c, uint32_t sp, uint32_t sq) {
     const v8i p8 = {(int)p[0], (int)p[1], (int)p[2], (int)p[3], 0, 0, 0, 0};
     const v8i q8 = {(int)q[0], (int)q[1], (int)q[2], (int)q[3], 0, 0, 0, 0};
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p8, q8, c, 4, 4, SEL, (int)sp, SEL, (int)sq);
   }
-  template <int S, int P>
-  __device__ __forceinline__ void product(const uint32_t (&sx)[kNBn], const uint32_t (&sy)[kNBm]) {
-    u32x4 px[kNBn], py[kNBm];
-    const uint32_t at = frag ^ (uint32_t)(P << 6);
-#pragma unroll
-    for (int i = 0; i < kNBn; ++i) px[i] = *(const LDS_AS u32x4 *)(slots.b[S] + (wave_n * kWN + 16 * i) * 256 + at);
-#pragma unroll
-    for (int j = 0; j < kNBm; ++j) py[j] = *(const LDS_AS u32x4 *)(slots.a[S] + (wave_m * kWM + 16 * j) * 256 + at);
-#pragma unroll
-    for (int i = 0; i < kNBn; ++i)
-#pragma unroll
-      for (int j = 0; j < kNBm; ++j) acc[i][j] = mma<P>(px[i], py[j], acc[i][j], sx[i], sy[j]);
-  }
 
-  // Slice kt from slot S: its loads have landed in every wave behind the
-  // barrier, and every wave's reads of the slot before it lie in front.
+  // MFMA Q of product P of slice kt in slot S, its fragments in f.  Between
+  // the MFMAs the next product's fragments are read into fn, and the loads of
+  // the slice kNS behind the one that just left its slot go out:
+  //  * before product 3 a wait and a barrier: slice kt + 1 has landed in every
+  //    wave, and every wave holds the last fragments of slice kt, so that its
+  //    slot may take slice kt + kNS;
+  //  * product 3 reads the first fragments and the scales of slice kt + 1;
+  //  * the loads go out over the three products behind the barrier.
+  // (Left to the compiler, the loads sank to the end of the slice, in front of
+  // the wait for them, and the fragments' reads to their use: 128 x 128 tiles
+  // of 32768 x 4096 x 8192 1123 us.)
+  static constexpr int load_pos(int i) { return i * 3 * kPer / kLoads; }  // in MFMAs from the barrier on
+  template <int S, int P, int Q, int R>
+  __device__ __forceinline__ void read_at(int kt, Frags &fn, Scales &cn) const {
+    constexpr int N = P == 3 ? 2 * kNR : kNR;  // reads of this product
+    if constexpr (R < N)
+      if constexpr (R * kPer / N == Q) {
+        if constexpr (P < 3)
+          read_frag<S, P + 1, R>(fn);
+        else if constexpr (R < kNR)
+          read_frag<(S + 1) % kNS, 0, R>(fn);
+        else
+          read_scale<(S + 1) % kNS, R - kNR>(cn, kt + 1);
+      }
+  }
+  template <int S, int P, int Q, int I>
+  __device__ __forceinline__ void load_at(int kt) const {
+    if constexpr (load_pos(I) == ((P + 1) & 3) * kPer + Q) {
+      if constexpr (P == 3)
+        load_one<S, I>(kt + kNS);
+      else
+        load_one<(S + kNS - 1) % kNS, I>(kt + kNS - 1);
+    }
+  }
+  template <int S, int P, int Q, int... R>
+  __device__ __forceinline__ void reads_at(std::integer_sequence<int, R...>, int kt, Frags &fn, Scales &cn) const {
+    (read_at<S, P, Q, R>(kt, fn, cn), ...);
+  }
+  template <int S, int P, int Q, int... I>
+  __device__ __forceinline__ void loads_at(std::integer_sequence<int, I...>, int kt) const {
+    (load_at<S, P, Q, I>(kt), ...);
+  }
+  template <int S, int P, int Q>
+  __device__ __forceinline__ void mfma_one(int kt, const Frags &f, Frags &fn, const Scales &c, Scales &cn) {
+    if constexpr (P == 3 && Q == 0) {
+      wait_vm_lgkm0<(kNS - 2) * kLoads>();
+      barrier();
+    }
+    reads_at<S, P, Q>(std::make_integer_sequence<int, 2 * kNR>(), kt, fn, cn);
+    loads_at<S, P, Q>(std::make_integer_sequence<int, kLoads>(), kt);
+    // (The y blocks snake, so that MFMAs side by side share an operand.)
+    constexpr int I = Q / kNBm, J0 = Q % kNBm, J = (I & 1) ? kNBm - 1 - J0 : J0;
+    acc[I][J] = mma<P>(f.x[I], f.y[J], acc[I][J], c.x[I], c.y[J]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  template <int S, int P, int... Q>
+  __device__ __forceinline__ void product(std::integer_sequence<int, Q...>, int kt, const Frags &f, Frags &fn, const Scales &c,
+                                          Scales &cn) {
+    (mfma_one<S, P, Q>(kt, f, fn, c, cn), ...);
+  }
+  // Slice kt from slot S; its first fragments are in f0, its scales in c.
   template <int S>
-  __device__ __forceinline__ void step(int kt) {
-    wait_vm_lgkm0<(kNS - 2) * kLoads>();
-    barrier();
-    load<(S + kNS - 1) % kNS>(kt + kNS - 1);
-    // The scales of the row from this lane's first on (behind them lies the
-    // next row's: a NaN among them would meet the zeros past K).
-    const int left = a.kb - 16 * kt - 4 * (lane >> 4);
-    const uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : ~0u >> (32 - 8 * left);
-    uint32_t sx[kNBn], sy[kNBm];
-#pragma unroll
-    for (int i = 0; i < kNBn; ++i) sx[i] = scale<S>(wave_n * kNBn + i, sh_x[EXT::kGated ? i & 1 : 0], keep);
-#pragma unroll
-    for (int j = 0; j < kNBm; ++j) sy[j] = scale<S>(kLB + wave_m * kNBm + j, sh_y[EXT::kGather ? j : 0], keep);
-    product<S, 0>(sx, sy);
-    product<S, 1>(sx, sy);
-    product<S, 2>(sx, sy);
-    product<S, 3>(sx, sy);
+  __device__ __forceinline__ void step(int kt, Frags &f0, Frags &f1, Scales &c, Scales &cn) {
+    constexpr auto all = std::make_integer_sequence<int, kPer>();
+    product<S, 0>(all, kt, f0, f1, c, cn);
+    product<S, 1>(all, kt, f1, f0, c, cn);
+    product<S, 2>(all, kt, f0, f1, c, cn);
+    product<S, 3>(all, kt, f1, f0, c, cn);
+  }
+  static constexpr int early() {
+    int n = 0;
+    for (int i = 0; i < kLoads; ++i) n += load_pos(i) < kPer;
+    return n;
   }
 
   __device__ __forceinline__ void run() {
     init();
     const int nk = (a.K + 255) >> 8;
-    load<0>(0);
+    // Slices 0 .. kNS - 2, and of slice kNS - 1 what a slice before the first
+    // would have loaded behind its barrier.
+    constexpr auto all = std::make_integer_sequence<int, kLoads>();
+    load_some<0>(all, 0);
     if constexpr (kNS == 4) {
-      load<1>(1);
-      load<2>(2);
+      load_some<1>(all, 1);
+      load_some<2>(all, 2);
     }
+    load_some<kNS - 1>(std::make_integer_sequence<int, early()>(), kNS - 1);
+    wait_vm_lgkm0<(kNS - 2) * kLoads + early()>();
+    barrier();
+    Frags f0, f1;
+    Scales c0, c1;
+    read_first<0>(std::make_integer_sequence<int, kNR>(), f0, c0, 0);
     int kt = 0;
     if constexpr (kNS == 4) {
       for (; kt + 3 < nk; kt += 4) {
-        step<0>(kt);
-        step<1>(kt + 1);
-        step<2>(kt + 2);
-        step<3>(kt + 3);
+        step<0>(kt, f0, f1, c0, c1);
+        step<1>(kt + 1, f0, f1, c1, c0);
+        step<2>(kt + 2, f0, f1, c0, c1);
+        step<3>(kt + 3, f0, f1, c1, c0);
       }
-      if (kt < nk) step<0>(kt);
-      if (kt + 1 < nk) step<1>(kt + 1);
-      if (kt + 2 < nk) step<2>(kt + 2);
+      if (kt < nk) step<0>(kt, f0, f1, c0, c1);
+      if (kt + 1 < nk) step<1>(kt + 1, f0, f1, c1, c0);
+      if (kt + 2 < nk) step<2>(kt + 2, f0, f1, c0, c1);
     } else {
       for (; kt + 1 < nk; kt += 2) {
-        step<0>(kt);
-        step<1>(kt + 1);
+        step<0>(kt, f0, f1, c0, c1);
+        step<1>(kt + 1, f0, f1, c1, c0);
       }
-      if (kt < nk) step<0>(kt);
+      if (kt < nk) step<0>(kt, f0, f1, c0, c1);
     }
     // The loads still in flight into the slots.
     wait_vm_lgkm0<0>();
