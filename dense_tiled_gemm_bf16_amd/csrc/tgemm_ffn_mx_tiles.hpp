@@ -20,40 +20,57 @@ struct MxTraits : Traits<kFp4, true, true, true> {
 
 typedef __attribute__((ext_vector_type(8))) int v8i;
 
+// Bytes of a slice row, by tile; workgroups that share a CU.
+template <int TM>
+constexpr int kMxSlice = TM == 64 ? 256 : 128;
+template <int TM>
+constexpr int kMxShare = TM == 128 ? 2 : 1;
+
 struct MxSlots {
-  LDS_AS uint8_t *a[4], *b[4];  // kNS slots of TM, TN rows x 256 bytes
-  LDS_AS uint8_t *s[4];         // their scales: 16 bytes of a row (B's rows first), then from 4 bytes on
+  LDS_AS uint8_t *a[4], *b[4];  // kNS slots of TM, TN rows
+  LDS_AS uint8_t *s[4];         // scales, 16 bytes of a row: of B's rows, then A's; then the same from 4 bytes on
 };
 
-// MxTile: TM x TN of C by 4 waves (2 x 2), K in slices of 512 elements (256
-// bytes of a row) through a ring of kNS slots, rows and scales loaded into LDS
-// directly.
+// MxTile: TM x TN of C by 4 waves (2 x 2), K in slices of SL bytes (2 SL
+// elements) of a row through a ring of kNS slots, rows and scales loaded into
+// LDS directly.
 //
 // Lane l of the scaled v_mfma 16x16x128 takes row l % 16 and one block of 32
-// elements.  Over the four products of a slice lane group g = l / 16 takes
-// blocks 4 g .. 4 g + 3, block 4 g + s in product s, of both operands alike:
-// its four scales of a slice are then one dword, byte s for product s, and no
-// scale moves between lanes.  A slot row keeps block c at 16-byte chunk c ^
-// perm(row % 16): the rows of a fragment read fall on different LDS banks, and
-// four lanes side by side load 64 bytes side by side.  (With the chunks of one
-// product side by side instead, four lanes loaded from four places: 24 bytes a
-// clock and CU at most.)
+// elements.  Over the kP = SL / 64 products of a slice lane group g = l / 16
+// takes blocks kP g .. kP g + kP - 1 of the slice, one a product, of both
+// operands alike: its scales of a slice are then kP bytes side by side, byte s
+// for product s, and no scale moves between lanes.  A slot row keeps block c at
+// 16-byte chunk c ^ perm(row % 16): the rows of a fragment read fall on
+// different LDS banks (no conflict in 21 million reads), and four lanes side by
+// side load 64 bytes side by side.  (With the chunks of one product side by
+// side instead, four lanes loaded from four places: 24 bytes a clock and CU at
+// most.)  A row's scales come 16 bytes at a time, those of 512 elements: a load
+// of 4 bytes a lane and slice cost the texture path as much as the rows.
 //
-// ALIGNED: every row's scales start on a dword.  If not, a lane loads the
-// dword that holds its first scale and the one behind, and shifts.
+// 64 x 64 tiles: slices of 256 bytes and four slots (128 KiB), 96 KiB on their way,
+// for products of few tiles.  128 x 128: slices of 128 bytes and two slots, so that two
+// workgroups share a CU and the one multiplies while the other waits or stores.
+//
+// ALIGNED: every row's scales start on a dword.  If not, a lane loads from the
+// dword that holds the first, and shifts.
 template <int DT, int TM, int TN, bool ALIGNED, class EXT>
 struct MxTile {
   static constexpr int kBlk = 16;
   static constexpr int kWM = TM / 2, kWN = TN / 2, kNBm = kWM / 16, kNBn = kWN / 16;
-  static constexpr int kNS = TM * TN <= 64 * 64 ? 4 : 2;
-  static constexpr int kLA = TM / 16, kLB = TN / 16;     // row load instructions of a wave and slice (4 rows each)
+  static constexpr int SL = kMxSlice<TM>, kP = SL / 64;  // bytes of a slice row; products of a slice
+  static constexpr int kNS = SL == 256 ? 4 : 2;
+  static constexpr int kIR = 1024 / SL;                  // rows of a load instruction
+  static constexpr int kLA = TM / 4 / kIR, kLB = TN / 4 / kIR;  // row load instructions of a wave and slice
+  static constexpr int kPer16 = 16 / kIR;                // instructions after which the rows' permutation repeats
+  static constexpr int kPairs = 256 / SL;                // slices that share a load of scales
   // Scale loads: 64 rows an instruction, 16 bytes (those of a slice) each, one
   // instruction a wave (the rows past TM + TN: nothing).
   static constexpr int kPlanes = ALIGNED ? 1 : 2, kPlane = 4 * 1024;
   static constexpr int kLoads = kLA + kLB + kPlanes;
   static constexpr int kScaleBytes = kPlane * kPlanes;
-  static_assert(kLA % 4 == 0 && kLB % 4 == 0 && TN % 64 == 0 && TM + TN <= 256, "whole instructions");
+  static_assert(kLA % kPer16 == 0 && kLB % kPer16 == 0 && TN % 64 == 0 && TM + TN <= 256, "whole instructions");
   static_assert((kNS - 1) * kLoads < 64, "vmcnt is 6 bits");
+  static_assert(kNS == 2 || kPairs == 1, "the waits count the same loads for every slice");
 
   const Args &a;
   MxSlots slots;
@@ -61,7 +78,7 @@ struct MxTile {
   int lane, wave, wave_m, wave_n, m0, n0;
   __amdgpu_buffer_rsrc_t ra, rb, rsa, rsb;
   uint32_t offa[kLA], offb[kLB];
-  int kcol[4];             // this lane's byte in a slice row, by instruction % 4
+  int kcol[kPer16];        // this lane's byte in a slice row, by instruction % kPer16
   uint32_t offs;           // aligned offset of this lane's row of scales in slice 0
   uint32_t sh_x[2], sh_y[EXT::kGather ? kNBm : 1];  // where this lane's scales start in their dword
   uint32_t frag;           // this lane's chunk of product 0
@@ -69,7 +86,13 @@ struct MxTile {
 
   __device__ __forceinline__ MxTile(const Args &args, const MxSlots &s, const EXT &ext) : a(args), slots(s), x(ext) {}
 
-  __device__ static __forceinline__ int perm(int r) { return r ^ ((r & 4) << 1); }
+  // Banks repeat every 256 bytes, one row or two.  LDS serves a read of 16
+  // bytes a lane in groups of 16 lanes; whether those are 16 rows of one lane
+  // group, or rows 0-3 and 12-15 of one and 4-11 of the next, their chunks differ.
+  __device__ static __forceinline__ int perm(int r) {
+    if constexpr (SL == 256) return r ^ ((r & 4) << 1);
+    return ((r >> 1) & 3) | ((((r >> 2) ^ (r >> 3)) & 1) << 2);
+  }
 
   // Row of B (from the tile's first on) that LDS row r holds, or -1.
   __device__ __forceinline__ int b_row(int r) const {
@@ -116,21 +139,21 @@ struct MxTile {
     rsb = make_rsrc((const void *)(pb - mis_b), (mis_b + (uint32_t)brows * (uint32_t)a.kb + 3u) & ~3u);
 
     const int r = lane & 15, g = lane >> 4;
-    // Rows: lane l of instruction i writes chunk l % 16 of row 4 i + l / 16 of
-    // the wave's rows, whose number % 16 goes by i % 4.
+    // Rows: lane l of instruction i writes chunk l % kCh of row kIR i + l / kCh
+    // of the wave's rows, whose number % 16 goes by i % kPer16.
+    constexpr int kCh = SL / 16;
+    const int lr = lane / kCh;
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      kcol[p] = 16 * (r ^ perm(4 * p + g));
-    }
+    for (int p = 0; p < kPer16; ++p) kcol[p] = 16 * ((lane % kCh) ^ perm(kIR * p + lr));
 #pragma unroll
     for (int i = 0; i < kLA; ++i) {
-      const int row = a_row(4 * (wave * kLA + i) + g);
-      offa[i] = row >= 0 ? (uint32_t)row * (uint32_t)a.lda + (uint32_t)kcol[i & 3] : kOOB;
+      const int row = a_row(kIR * (wave * kLA + i) + lr);
+      offa[i] = row >= 0 ? (uint32_t)row * (uint32_t)a.lda + (uint32_t)kcol[i % kPer16] : kOOB;
     }
 #pragma unroll
     for (int i = 0; i < kLB; ++i) {
-      const int row = b_row(4 * (wave * kLB + i) + g);
-      offb[i] = row >= 0 ? (uint32_t)row * (uint32_t)a.ldb + (uint32_t)kcol[i & 3] : kOOB;
+      const int row = b_row(kIR * (wave * kLB + i) + lr);
+      offb[i] = row >= 0 ? (uint32_t)row * (uint32_t)a.ldb + (uint32_t)kcol[i % kPer16] : kOOB;
     }
     // Scales: lane l of wave w takes row 64 w + l of B's and A's together.
     {
@@ -150,7 +173,7 @@ struct MxTile {
         sh_y[0] = (mis_a + (uint32_t)r * (uint32_t)a.kb) & 3u;
       }
     }
-    frag = (uint32_t)(r * 256 + (((4 * g) ^ perm(r)) << 4));
+    frag = (uint32_t)(r * SL + (((kP * g) ^ perm(r)) << 4));
 #pragma unroll
     for (int i = 0; i < kNBn; ++i)
 #pragma unroll
@@ -161,23 +184,25 @@ struct MxTile {
     return 0;
   }
 
-  // Load I of slice kt into slot S.  The last slices check columns: what lies
+  // S below is kt % 4: slot kt % kNS, scales of slices kt .. of a pair in kt /
+  // kPairs % 2 or % 4.
+  // Load I of slice kt into its slot.  The last slices check columns: what lies
   // past K arrives as zeros, and a slice past the last is all zeros.
   template <int S, int I>
   __device__ __forceinline__ void load_one(int kt) const {
-    const int left = a.K - kt * 256;  // bytes of a row from this slice on
-    const bool whole = left >= 256;
+    const int left = a.K - kt * SL;  // bytes of a row from this slice on
+    const bool whole = left >= SL;
     if constexpr (I < kLA + kLB) {
       constexpr bool isb = I >= kLA;
       constexpr int i = isb ? I - kLA : I;
-      const uint32_t v = whole || kcol[i & 3] < left ? (isb ? offb[i % kLB] : offa[i % kLA]) : kOOB;
-      LDS_AS uint8_t *dst = (isb ? slots.b[S] : slots.a[S]) + (wave * (isb ? kLB : kLA) + i) * 1024;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(isb ? rb : ra, (LDS_AS void *)dst, 16, v, (uint32_t)kt * 256u, 0, 0);
-    } else {
+      const uint32_t v = whole || kcol[i % kPer16] < left ? (isb ? offb[i % kLB] : offa[i % kLA]) : kOOB;
+      LDS_AS uint8_t *dst = (isb ? slots.b[S % kNS] : slots.a[S % kNS]) + (wave * (isb ? kLB : kLA) + i) * 1024;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(isb ? rb : ra, (LDS_AS void *)dst, 16, v, (uint32_t)(kt * SL), 0, 0);
+    } else if constexpr (S % kPairs == 0) {
       constexpr int p = I - kLA - kLB;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(wave < TN / 64 ? rsb : rsa,
-                                               (LDS_AS void *)(slots.s[S] + p * kPlane + wave * 1024), 16,
-                                               left > 0 ? offs : kOOB, (uint32_t)kt * 16u + 4u * (uint32_t)p, 0, 0);
+                                               (LDS_AS void *)(slots.s[S / kPairs] + p * kPlane + wave * 1024), 16,
+                                               left > 0 ? offs : kOOB, (uint32_t)(kt / kPairs) * 16u + 4u * (uint32_t)p, 0, 0);
     }
   }
   template <int S, int... I>
@@ -192,28 +217,40 @@ struct MxTile {
     uint32_t x[kNBn], y[kNBm];
   };
   static constexpr int kPer = kNBn * kNBm, kNR = kNBn + kNBm;  // MFMAs and fragment reads of a product
-  // Fragment R (x blocks, then y blocks) of product P from slot S.
+  // Fragment R (x blocks, then y blocks) of product P.
   template <int S, int P, int R>
   __device__ __forceinline__ void read_frag(Frags &f) const {
     const uint32_t at = frag ^ (uint32_t)(P << 4);
     if constexpr (R < kNBn)
-      f.x[R] = *(const LDS_AS u32x4 *)(slots.b[S] + (wave_n * kWN + 16 * R) * 256 + at);
+      f.x[R] = *(const LDS_AS u32x4 *)(slots.b[S % kNS] + (wave_n * kWN + 16 * R) * SL + at);
     else
-      f.y[R - kNBn] = *(const LDS_AS u32x4 *)(slots.a[S] + (wave_m * kWM + 16 * (R - kNBn)) * 256 + at);
+      f.y[R - kNBn] = *(const LDS_AS u32x4 *)(slots.a[S % kNS] + (wave_m * kWM + 16 * (R - kNBn)) * SL + at);
   }
-  // This lane's scales of block R in slot S, of slice kt.  Bytes behind the
-  // row's last are the next row's: a NaN among them would meet the zeros past K.
+  // This lane's scales of block R, slice kt: kP bytes.  Bytes behind the row's
+  // last are the next row's: a NaN among them would meet the zeros past K.
   template <int S, int R>
   __device__ __forceinline__ void read_scale(Scales &c, int kt) const {
-    const int b = R < kNBn ? wave_n * kNBn + R : kLB + wave_m * kNBm + R - kNBn;
-    const LDS_AS uint8_t *p = slots.s[S] + b * 256 + 16 * (lane & 15) + 4 * (lane >> 4);
-    uint32_t w = *(const LDS_AS uint32_t *)p;
-    if constexpr (!ALIGNED) {
+    const int b = R < kNBn ? wave_n * kNBn + R : TN / 16 + wave_m * kNBm + R - kNBn;
+    const int g = lane >> 4;
+    // Byte of the row's 16 where this lane's start.
+    const int at = kP == 4 ? 4 * g : 8 * (S % kPairs) + 2 * g;
+    const LDS_AS uint8_t *p = slots.s[S / kPairs] + b * 256 + 16 * (lane & 15);
+    uint32_t w;
+    if constexpr (ALIGNED) {
+      if constexpr (kP == 4)
+        w = *(const LDS_AS uint32_t *)(p + at);
+      else
+        w = *(const LDS_AS uint16_t *)(p + at);
+    } else {
       const uint32_t sh = R < kNBn ? sh_x[EXT::kGated ? R & 1 : 0] : sh_y[EXT::kGather ? (R < kNBn ? 0 : R - kNBn) : 0];
-      w = __builtin_amdgcn_alignbyte(*(const LDS_AS uint32_t *)(p + kPlane), w, sh);
+      const uint32_t lo = *(const LDS_AS uint32_t *)(p + (at & ~3)), hi = *(const LDS_AS uint32_t *)(p + kPlane + (at & ~3));
+      if constexpr (kP == 4)
+        w = __builtin_amdgcn_alignbyte(hi, lo, sh);
+      else
+        w = (uint32_t)(((uint64_t)hi << 32 | lo) >> (8 * (sh + (uint32_t)(at & 3))));  // (up to 5 bytes, for two)
     }
-    const int left = a.kb - 16 * kt - 4 * (lane >> 4);
-    if (a.kb < 16 * kt + 16) w &= left >= 4 ? ~0u : left <= 0 ? 0u : ~0u >> (32 - 8 * left);
+    const int left = a.kb - (kP * 4 * kt + kP * g);
+    if (a.kb < kP * 4 * (kt + 1)) w &= left >= kP ? ~0u : left <= 0 ? 0u : ~0u >> (32 - 8 * left);
     (R < kNBn ? c.x[R % kNBn] : c.y[(R - kNBn + kNBm) % kNBm]) = w;
   }
   template <int S, int... R>
@@ -232,35 +269,36 @@ struct MxTile {
   // MFMA Q of product P of slice kt in slot S, its fragments in f.  Between
   // the MFMAs the next product's fragments are read into fn, and the loads of
   // the slice kNS behind the one that just left its slot go out:
-  //  * before product 3 a wait and a barrier: slice kt + 1 has landed in every
-  //    wave, and every wave holds the last fragments of slice kt, so that its
-  //    slot may take slice kt + kNS;
-  //  * product 3 reads the first fragments and the scales of slice kt + 1;
-  //  * the loads go out over the three products behind the barrier.
+  //  * before the last product a wait and a barrier: slice kt + 1 has landed in
+  //    every wave, and every wave holds the last fragments of slice kt, so that
+  //    its slot may take slice kt + kNS;
+  //  * the last product reads the first fragments and the scales of slice kt + 1;
+  //  * the loads go out over kWindow MFMAs behind the barrier.
   // (Left to the compiler, the loads sank to the end of the slice, in front of
   // the wait for them, and the fragments' reads to their use: 128 x 128 tiles
   // of 32768 x 4096 x 8192 1123 us.)
-  static constexpr int load_pos(int i) { return i * 3 * kPer / kLoads; }  // in MFMAs from the barrier on
+  static constexpr int kWindow = (kP - 1) * kPer;
+  static constexpr int load_pos(int i) { return i * kWindow / kLoads; }  // in MFMAs from the barrier on
   template <int S, int P, int Q, int R>
   __device__ __forceinline__ void read_at(int kt, Frags &fn, Scales &cn) const {
-    constexpr int N = P == 3 ? 2 * kNR : kNR;  // reads of this product
+    constexpr int N = P == kP - 1 ? 2 * kNR : kNR;  // reads of this product
     if constexpr (R < N)
       if constexpr (R * kPer / N == Q) {
-        if constexpr (P < 3)
+        if constexpr (P < kP - 1)
           read_frag<S, P + 1, R>(fn);
         else if constexpr (R < kNR)
-          read_frag<(S + 1) % kNS, 0, R>(fn);
+          read_frag<(S + 1) % 4, 0, R>(fn);
         else
-          read_scale<(S + 1) % kNS, R - kNR>(cn, kt + 1);
+          read_scale<(S + 1) % 4, R - kNR>(cn, kt + 1);
       }
   }
   template <int S, int P, int Q, int I>
   __device__ __forceinline__ void load_at(int kt) const {
-    if constexpr (load_pos(I) == ((P + 1) & 3) * kPer + Q) {
-      if constexpr (P == 3)
-        load_one<S, I>(kt + kNS);
+    if constexpr (load_pos(I) == (P + 1) % kP * kPer + Q) {
+      if constexpr (P == kP - 1)
+        load_one<(S + kNS) % 4, I>(kt + kNS);
       else
-        load_one<(S + kNS - 1) % kNS, I>(kt + kNS - 1);
+        load_one<(S + kNS - 1) % 4, I>(kt + kNS - 1);
     }
   }
   template <int S, int P, int Q, int... R>
@@ -273,7 +311,7 @@ struct MxTile {
   }
   template <int S, int P, int Q>
   __device__ __forceinline__ void mfma_one(int kt, const Frags &f, Frags &fn, const Scales &c, Scales &cn) {
-    if constexpr (P == 3 && Q == 0) {
+    if constexpr (P == kP - 1 && Q == 0) {
       wait_vm_lgkm0<(kNS - 2) * kLoads>();
       barrier();
     }
@@ -289,24 +327,28 @@ struct MxTile {
                                           Scales &cn) {
     (mfma_one<S, P, Q>(kt, f, fn, c, cn), ...);
   }
-  // Slice kt from slot S; its first fragments are in f0, its scales in c.
+  // Slice kt (S = kt % 4); its first fragments are in f0, its scales in c.
   template <int S>
   __device__ __forceinline__ void step(int kt, Frags &f0, Frags &f1, Scales &c, Scales &cn) {
     constexpr auto all = std::make_integer_sequence<int, kPer>();
     product<S, 0>(all, kt, f0, f1, c, cn);
     product<S, 1>(all, kt, f1, f0, c, cn);
-    product<S, 2>(all, kt, f0, f1, c, cn);
-    product<S, 3>(all, kt, f1, f0, c, cn);
+    if constexpr (kP == 4) {
+      product<S, 2>(all, kt, f0, f1, c, cn);
+      product<S, 3>(all, kt, f1, f0, c, cn);
+    }
   }
+  // Loads of slice kNS - 1 that go out in front of the first barrier (scales
+  // come with every kPairs-th slice).
   static constexpr int early() {
     int n = 0;
-    for (int i = 0; i < kLoads; ++i) n += load_pos(i) < kPer;
+    for (int i = 0; i < kLoads; ++i) n += load_pos(i) < kPer && (i < kLA + kLB || (kNS - 1) % kPairs == 0);
     return n;
   }
 
   __device__ __forceinline__ void run() {
     init();
-    const int nk = (a.K + 255) >> 8;
+    const int nk = (a.K + SL - 1) / SL;
     // Slices 0 .. kNS - 2, and of slice kNS - 1 what a slice before the first
     // would have loaded behind its barrier.
     constexpr auto all = std::make_integer_sequence<int, kLoads>();
@@ -315,30 +357,22 @@ struct MxTile {
       load_some<1>(all, 1);
       load_some<2>(all, 2);
     }
-    load_some<kNS - 1>(std::make_integer_sequence<int, early()>(), kNS - 1);
+    load_some<kNS - 1>(std::make_integer_sequence<int, early()>(), kNS - 1);  // (row loads come first)
     wait_vm_lgkm0<(kNS - 2) * kLoads + early()>();
     barrier();
     Frags f0, f1;
     Scales c0, c1;
     read_first<0>(std::make_integer_sequence<int, kNR>(), f0, c0, 0);
     int kt = 0;
-    if constexpr (kNS == 4) {
-      for (; kt + 3 < nk; kt += 4) {
-        step<0>(kt, f0, f1, c0, c1);
-        step<1>(kt + 1, f0, f1, c1, c0);
-        step<2>(kt + 2, f0, f1, c0, c1);
-        step<3>(kt + 3, f0, f1, c1, c0);
-      }
-      if (kt < nk) step<0>(kt, f0, f1, c0, c1);
-      if (kt + 1 < nk) step<1>(kt + 1, f0, f1, c1, c0);
-      if (kt + 2 < nk) step<2>(kt + 2, f0, f1, c0, c1);
-    } else {
-      for (; kt + 1 < nk; kt += 2) {
-        step<0>(kt, f0, f1, c0, c1);
-        step<1>(kt + 1, f0, f1, c1, c0);
-      }
-      if (kt < nk) step<0>(kt, f0, f1, c0, c1);
+    for (; kt + 3 < nk; kt += 4) {
+      step<0>(kt, f0, f1, c0, c1);
+      step<1>(kt + 1, f0, f1, c1, c0);
+      step<2>(kt + 2, f0, f1, c0, c1);
+      step<3>(kt + 3, f0, f1, c1, c0);
     }
+    if (kt < nk) step<0>(kt, f0, f1, c0, c1);
+    if (kt + 1 < nk) step<1>(kt + 1, f0, f1, c1, c0);
+    if (kt + 2 < nk) step<2>(kt + 2, f0, f1, c0, c1);
     // The loads still in flight into the slots.
     wait_vm_lgkm0<0>();
     x.store(*this);
@@ -373,11 +407,11 @@ struct MxTile {
   }
 };
 
-#define TGEMM_MX_SLOTS(TM, TN, NS, SCALES)                                  \
-  __shared__ __attribute__((aligned(1024))) uint8_t sA0[TM * 256];          \
-  __shared__ __attribute__((aligned(1024))) uint8_t sA1[TM * 256];          \
-  __shared__ __attribute__((aligned(1024))) uint8_t sB0[TN * 256];          \
-  __shared__ __attribute__((aligned(1024))) uint8_t sB1[TN * 256];          \
+#define TGEMM_MX_SLOTS(TM, TN, SL, SCALES)                                  \
+  __shared__ __attribute__((aligned(1024))) uint8_t sA0[TM * SL];           \
+  __shared__ __attribute__((aligned(1024))) uint8_t sA1[TM * SL];           \
+  __shared__ __attribute__((aligned(1024))) uint8_t sB0[TN * SL];           \
+  __shared__ __attribute__((aligned(1024))) uint8_t sB1[TN * SL];           \
   __shared__ __attribute__((aligned(1024))) uint8_t sS0[SCALES];            \
   __shared__ __attribute__((aligned(1024))) uint8_t sS1[SCALES];            \
   MxSlots slots;                                                            \
@@ -387,11 +421,11 @@ struct MxTile {
   slots.b[1] = (LDS_AS uint8_t *)sB1;                                       \
   slots.s[0] = (LDS_AS uint8_t *)sS0;                                       \
   slots.s[1] = (LDS_AS uint8_t *)sS1;                                       \
-  if constexpr (NS == 4) {                                                  \
-    __shared__ __attribute__((aligned(1024))) uint8_t sA2[TM * 256];        \
-    __shared__ __attribute__((aligned(1024))) uint8_t sA3[TM * 256];        \
-    __shared__ __attribute__((aligned(1024))) uint8_t sB2[TN * 256];        \
-    __shared__ __attribute__((aligned(1024))) uint8_t sB3[TN * 256];        \
+  if constexpr (SL == 256) {                                                \
+    __shared__ __attribute__((aligned(1024))) uint8_t sA2[TM * SL];         \
+    __shared__ __attribute__((aligned(1024))) uint8_t sA3[TM * SL];         \
+    __shared__ __attribute__((aligned(1024))) uint8_t sB2[TN * SL];         \
+    __shared__ __attribute__((aligned(1024))) uint8_t sB3[TN * SL];         \
     __shared__ __attribute__((aligned(1024))) uint8_t sS2[SCALES];          \
     __shared__ __attribute__((aligned(1024))) uint8_t sS3[SCALES];          \
     slots.a[2] = (LDS_AS uint8_t *)sA2;                                     \
@@ -430,19 +464,19 @@ __device__ __forceinline__ void mx_tile(const Args &a, const X &x) {
     k.run();
   } else {
     using K = MxTile<DT, TM, TN, ALIGNED, X>;
-    TGEMM_MX_SLOTS(TM, TN, K::kNS, K::kScaleBytes)
+    TGEMM_MX_SLOTS(TM, TN, K::SL, K::kScaleBytes)
     K k(a, slots, x);
     k.run();
   }
 }
 
 template <int DT, int TM, int TN, bool ALIGNED, bool GATED, bool FUSED>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(kMxShare<TM>, kMxShare<TM>)))
 void mx_epilogue_kernel(const Args a, const Tail t) {
 #if defined(__HIP_DEVICE_COMPILE__)
   int tm, tn;
   tile_of((int)blockIdx.x, a.tiles_m * a.tiles_n, a.tiles_m, a.tiles_n, tm, tn);
-  constexpr int kArea = (TM < TN ? TM : TN) * (TM == 256 ? 128 : 256);
+  constexpr int kArea = (TM < TN ? TM : TN) * kMxSlice<TM>;
   const MxExt<DT, GATED, false, FUSED, kArea> x{tm * TM, tn * (GATED ? TN / 2 : TN), t.half, nullptr, 0, t};
   mx_tile<DT, TM, TN, ALIGNED>(a, x);
 #endif
@@ -456,7 +490,7 @@ struct MxGroups {
 };
 
 template <int DT, int TM, int TN, bool ALIGNED, bool GATED, bool FUSED>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(kMxShare<TM>, kMxShare<TM>)))
 void mx_grouped_kernel(const Args a0, const Tail t0, const MxGroups g) {
 #if defined(__HIP_DEVICE_COMPILE__)
   const int lane = threadIdx.x & 63;
@@ -479,7 +513,7 @@ void mx_grouped_kernel(const Args a0, const Tail t0, const MxGroups g) {
   }
   if (t.bias) t.bias += (size_t)f.e * (size_t)g.stride_bias * 2;
   if (t.pre) t.pre += (size_t)f.lo * t.ldp * 2;
-  constexpr int kArea = (TM < TN ? TM : TN) * (TM == 256 ? 128 : 256);
+  constexpr int kArea = (TM < TN ? TM : TN) * kMxSlice<TM>;
   const MxExt<DT, GATED, true, FUSED, kArea> x{__builtin_amdgcn_readfirstlane(tm * TM),
                                                __builtin_amdgcn_readfirstlane(tn * (GATED ? TN / 2 : TN)), t.half,
                                                g.rows ? g.rows + f.lo : nullptr, g.src_rows, t};
