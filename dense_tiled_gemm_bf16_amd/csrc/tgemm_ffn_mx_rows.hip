@@ -100,9 +100,6 @@ template <int DT, int W, int NB, bool GATED, bool GROUPED>
 __global__ __launch_bounds__(64 * W) void mx_rows_kernel(const MxRowsArgs a) {
   constexpr int kOutB = GATED ? NB / 2 : NB, kCols = 16 * kOutB;
   static_assert(kOutB <= W, "an output piece a thread");
-  // Units of a batch; two batches are in registers, one on its way while the
-  // other is multiplied.
-  constexpr int kU = NB == 1 ? 2 : 1;
   __shared__ v4f part[W][NB][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -176,64 +173,40 @@ __global__ __launch_bounds__(64 * W) void mx_rows_kernel(const MxRowsArgs a) {
 #pragma unroll
   for (int i = 0; i < NB; ++i) acc[i] = v4f{};
   const int units = (a.K + 511) >> 9;
-  struct Batch {
-    v4u x[kU][4][NB], y[kU][4];
-    v2u sx[kU][NB], sy[kU];
-  };
-  // (K % 32 == 0: a block is all inside K or all outside, where both operands
-  // read zeros; a unit past the last is all outside.  The weights' loads
-  // first: A's wait for its row's index.)
-  auto load = [&](Batch &f, int u0) {
+  // One unit at a time: the next one's loads wait for it, but the registers
+  // that holding both would take are worth more as further waves.
+  for (int u = wave; u < units; u += W) {
+    v4u x[4][NB], y[4];
+    v2u wx[NB], wy;
+    // (K % 32 == 0: a block is all inside K or all outside, where both operands
+    // read zeros.  The weights' loads first: A's wait for its row's index.)
 #pragma unroll
-    for (int i = 0; i < kU; ++i) {
-      const int u = u0 + W * i;
+    for (int s = 0; s < 4; ++s) {
+      const bool in = 512 * u + 128 * g + 32 * s < a.K;
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const bool in = 512 * u + 128 * g + 32 * s < a.K;
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-          f.x[i][s][b] = __builtin_amdgcn_raw_buffer_load_b128(rb, in ? boff[b] + 16u * (uint32_t)s : kOOB, (uint32_t)u * 256u, 0);
-      }
-#pragma unroll
-      for (int b = 0; b < NB; ++b) f.sx[i][b] = sb[b].load(srb, (uint32_t)u);
+      for (int b = 0; b < NB; ++b)
+        x[s][b] = __builtin_amdgcn_raw_buffer_load_b128(rb, in ? boff[b] + 16u * (uint32_t)s : kOOB, (uint32_t)u * 256u, 0);
     }
 #pragma unroll
-    for (int i = 0; i < kU; ++i) {
-      const int u = u0 + W * i;
+    for (int b = 0; b < NB; ++b) wx[b] = sb[b].load(srb, (uint32_t)u);
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const bool in = 512 * u + 128 * g + 32 * s < a.K;
-        f.y[i][s] = __builtin_amdgcn_raw_buffer_load_b128(ra, in ? aoff + 16u * (uint32_t)s : kOOB, (uint32_t)u * 256u, 0);
-      }
-      f.sy[i] = sa.load(sra, (uint32_t)u);
+    for (int s = 0; s < 4; ++s) {
+      const bool in = 512 * u + 128 * g + 32 * s < a.K;
+      y[s] = __builtin_amdgcn_raw_buffer_load_b128(ra, in ? aoff + 16u * (uint32_t)s : kOOB, (uint32_t)u * 256u, 0);
     }
-    __builtin_amdgcn_sched_barrier(0);  // (all on their way before the next products)
-  };
-  auto multiply = [&](const Batch &f, int u0) {
+    wy = sa.load(sra, (uint32_t)u);
+    __builtin_amdgcn_sched_barrier(0);  // (all on their way before the products)
+    const int left = a.kb - (16 * u + 4 * g);
+    const uint32_t sy = sa.get(wy, left);
 #pragma unroll
-    for (int i = 0; i < kU; ++i) {
-      const int left = a.kb - (16 * (u0 + W * i) + 4 * g);
-      const uint32_t sy = sa.get(f.sy[i], left);
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const uint32_t sx = sb[b].get(f.sx[i][b], left);
-        acc[b] = mfma<0>(f.x[i][0][b], f.y[i][0], acc[b], sx, sy);
-        acc[b] = mfma<1>(f.x[i][1][b], f.y[i][1], acc[b], sx, sy);
-        acc[b] = mfma<2>(f.x[i][2][b], f.y[i][2], acc[b], sx, sy);
-        acc[b] = mfma<3>(f.x[i][3][b], f.y[i][3], acc[b], sx, sy);
-      }
+    for (int b = 0; b < NB; ++b) {
+      const uint32_t sx = sb[b].get(wx[b], left);
+      acc[b] = mfma<0>(x[0][b], y[0], acc[b], sx, sy);
+      acc[b] = mfma<1>(x[1][b], y[1], acc[b], sx, sy);
+      acc[b] = mfma<2>(x[2][b], y[2], acc[b], sx, sy);
+      acc[b] = mfma<3>(x[3][b], y[3], acc[b], sx, sy);
     }
     __builtin_amdgcn_sched_barrier(0);
-  };
-  Batch f0, f1;
-  constexpr int kStep = W * kU;
-  load(f0, wave);
-  for (int u0 = wave; u0 < units; u0 += 2 * kStep) {
-    load(f1, u0 + kStep);
-    multiply(f0, u0);
-    if (u0 + kStep >= units) break;
-    load(f0, u0 + 2 * kStep);
-    multiply(f1, u0 + kStep);
   }
 #pragma unroll
   for (int b = 0; b < NB; ++b) part[wave][b][lane] = acc[b];
@@ -317,9 +290,15 @@ hipError_t launch_one(const MxGemm &g) {
   return hipLaunchKernel(fn, dim3((unsigned)wgs), dim3(64 * W), args, 0, g.stream);
 }
 
+template <int DT, int W>
+hipError_t launch_waves(const MxGemm &g) {
+  if (is_gated(g.act)) return launch_one<DT, W, 2, true>(g);
+  return g.N * (g.groups ? std::min(g.groups, g.M) : 1) <= 32 * g.cus ? launch_one<DT, W, 1, false>(g) : launch_one<DT, W, 2, false>(g);
+}
+
 template <int DT>
 hipError_t launch_dt(const MxGemm &g) {
-  return is_gated(g.act) ? launch_one<DT, 4, 2, true>(g) : launch_one<DT, 4, 1, false>(g);
+  return g.K > 2048 ? launch_waves<DT, 8>(g) : launch_waves<DT, 4>(g);
 }
 
 }  // namespace
