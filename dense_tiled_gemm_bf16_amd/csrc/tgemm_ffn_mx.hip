@@ -74,7 +74,12 @@ hipError_t launch_mx(const MxGemm &g) {
   int tm = g.tile_m;
   if (tm == 0) tm = g.M <= (g.groups ? 10 * g.groups : 16) ? 16 : pick(g);
   if (tm == 16) return launch_mx_rows(g);
-  return g.dtype == 1 ? launch_mx_f16(g, tm) : launch_mx_bf16(g, tm);
+  bool two = false;
+  if (tm == 64) {
+    const int64_t tiles = g.groups ? g.M / 64 + std::min(g.groups, g.M) : (g.M + 63) / 64;
+    two = tiles * ((g.N + 63) / 64) > 256;
+  }
+  return g.dtype == 1 ? launch_mx_f16(g, tm, two) : launch_mx_bf16(g, tm, two);
 }
 
 }  // namespace ffn

@@ -4,7 +4,7 @@
 namespace tgemm {
 namespace ffn {
 
-hipError_t launch_mx_bf16(const MxGemm &g, int tm) { return launch_mx_tiles_dt<0>(g, tm); }
+hipError_t launch_mx_bf16(const MxGemm &g, int tm, bool two) { return launch_mx_tiles_dt<0>(g, tm, two); }
 
 }  // namespace ffn
 }  // namespace tgemm

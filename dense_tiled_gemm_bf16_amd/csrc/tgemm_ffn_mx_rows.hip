@@ -5,14 +5,13 @@
 // elements.  A workgroup takes 16 NB rows of the weight (columns of C) and up
 // to 16 rows of A, and its W waves divide K: wave w takes units of 512 K
 // elements (256 bytes of each row) w, w + W, ...  Rows and scales go from
-// memory straight into the registers of the scaled v_mfma 16x16x128: lane l
-// holds row l % 16 and, of a unit, the four blocks of 32 elements from
-// 4 (l / 16) on.  Which block goes into which of the unit's four products is
-// free as long as both operands agree, so product s takes each lane's block s:
-// the lane's 64 bytes lie together, and its four scales are one dword whose
-// byte s the instruction selects.  The waves' sums meet in LDS, are added in
-// wave order (the result does not depend on timing) and pass through the
-// epilogue.
+// memory straight into the registers of the scaled v_mfma 16x16x128: in
+// product s of a unit lane l holds row l % 16 and block 4 s + l / 16 of 32
+// elements.  A lane loads its row's 16 scale bytes of the unit and picks every
+// fourth, one for each product.  (Blocks 4 (l / 16) + s instead, whose scales are a
+// dword as it lies, made a lane's loads 64 bytes of one row: 10% slower.)  The
+// waves' sums meet in LDS, are added in wave order (the result does not depend
+// on timing) and pass through the epilogue.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -63,11 +62,11 @@ __device__ __forceinline__ void store4(uint8_t *p, const float (&v)[4]) {
 
 constexpr int kTM = 16;
 
-// The scale rows of one operand.  A lane's four scales of a unit need not
-// start on a dword (rows of K / 32 bytes, from any address): it loads the
-// dword that holds the first and the one behind, and shifts them together.
-// The resource is based at the dword that holds the first row's first byte
-// and ends with the one that holds the last row's last.
+// The scale rows of one operand.  A row's 16 scales of a unit need not start
+// on a dword (rows of K / 32 bytes, from any address): a lane loads from the
+// dword that holds the first on, one more, and shifts.  The resource is based
+// at the dword that holds the first row's first byte and ends with the one that
+// holds the last row's last.
 struct ScaleRows {
   __amdgpu_buffer_rsrc_t r;
   uint32_t mis;
@@ -78,21 +77,27 @@ struct ScaleRows {
     r = rsrc_of((const void *)(at - mis), rows ? (mis + rows * (uint32_t)kb + 3u) & ~3u : 0u);
   }
 };
+struct ScaleWords {
+  v4u w;
+  uint32_t next;
+};
 struct ScaleLane {
-  uint32_t off, sh;  // this lane's aligned offset in unit 0 (or kOOB), the byte it starts at
-  __device__ __forceinline__ void init(const ScaleRows &s, bool in, uint32_t row, int kb, int g) {
-    const uint32_t pos = s.mis + row * (uint32_t)kb + 4u * (uint32_t)g;
+  uint32_t off, sh;  // the row's aligned offset in unit 0 (or kOOB), the byte it starts at
+  __device__ __forceinline__ void init(const ScaleRows &s, bool in, uint32_t row, int kb) {
+    const uint32_t pos = s.mis + row * (uint32_t)kb;
     off = in ? pos & ~3u : kOOB;
     sh = pos & 3u;
   }
-  __device__ __forceinline__ v2u load(const ScaleRows &s, uint32_t u) const {
-    return __builtin_amdgcn_raw_buffer_load_b64(s.r, off, 16u * u, 0);
+  __device__ __forceinline__ ScaleWords load(const ScaleRows &s, uint32_t u) const {
+    return {__builtin_amdgcn_raw_buffer_load_b128(s.r, off, 16u * u, 0),
+            __builtin_amdgcn_raw_buffer_load_b32(s.r, off, 16u * u + 16u, 0)};
   }
-  // left: the scales of the row from this lane's first on (the bytes behind
-  // them are the next row's: a NaN among them would meet the zeros past K).
-  __device__ __forceinline__ uint32_t get(const v2u &w, int left) const {
-    const uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : ~0u >> (32 - 8 * left);
-    return __builtin_amdgcn_alignbyte(w[1], w[0], sh) & keep;
+  // pick: bytes g and 4 + g of two dwords.
+  __device__ __forceinline__ uint32_t get(const ScaleWords &c, uint32_t pick, uint32_t keep) const {
+    const uint32_t w0 = __builtin_amdgcn_alignbyte(c.w[1], c.w[0], sh), w1 = __builtin_amdgcn_alignbyte(c.w[2], c.w[1], sh);
+    const uint32_t w2 = __builtin_amdgcn_alignbyte(c.w[3], c.w[2], sh), w3 = __builtin_amdgcn_alignbyte(c.next, c.w[3], sh);
+    const uint32_t lo = __builtin_amdgcn_perm(w1, w0, pick), hi = __builtin_amdgcn_perm(w3, w2, pick);
+    return (lo | hi << 16) & keep;
   }
 };
 
@@ -136,8 +141,8 @@ __global__ __launch_bounds__(64 * W) void mx_rows_kernel(const MxRowsArgs a) {
   for (int b = 0; b < NB; ++b) {
     const int c = (GATED ? b >> 1 : b) * 16 + r;
     const uint32_t row = (uint32_t)(c + (GATED && (b & 1) ? a.half : 0));
-    boff[b] = c < cols ? row * (uint32_t)a.ldb + 64u * (uint32_t)g : kOOB;
-    sb[b].init(srb, c < cols, row, a.kb, g);
+    boff[b] = c < cols ? row * (uint32_t)a.ldb + 16u * (uint32_t)g : kOOB;
+    sb[b].init(srb, c < cols, row, a.kb);
   }
   __amdgpu_buffer_rsrc_t ra;
   if (GROUPED && a.rows) {
@@ -145,14 +150,14 @@ __global__ __launch_bounds__(64 * W) void mx_rows_kernel(const MxRowsArgs a) {
     sra.init(SA, (uint32_t)a.src_rows, a.kb);
     const int src = m0 + r < M ? a.rows[lo + m0 + r] : -1;
     const bool in = src >= 0 && src < a.src_rows;
-    aoff = in ? (uint32_t)src * (uint32_t)a.lda + 64u * (uint32_t)g : kOOB;
-    sa.init(sra, in, in ? (uint32_t)src : 0u, a.kb, g);
+    aoff = in ? (uint32_t)src * (uint32_t)a.lda + 16u * (uint32_t)g : kOOB;
+    sa.init(sra, in, in ? (uint32_t)src : 0u, a.kb);
   } else {
     const int rows = min(M - m0, kTM);
     ra = rsrc_of(A + (size_t)(lo + m0) * a.lda, (uint32_t)(rows - 1) * (uint32_t)a.lda + row_bytes);
     sra.init(SA + (size_t)(lo + m0) * a.kb, (uint32_t)rows, a.kb);
-    aoff = r < rows ? (uint32_t)r * (uint32_t)a.lda + 64u * (uint32_t)g : kOOB;
-    sa.init(sra, r < rows, (uint32_t)r, a.kb, g);
+    aoff = r < rows ? (uint32_t)r * (uint32_t)a.lda + 16u * (uint32_t)g : kOOB;
+    sa.init(sra, r < rows, (uint32_t)r, a.kb);
   }
 
   // This thread's piece of the output: lane l of wave ob holds row l % 16,
@@ -173,34 +178,39 @@ __global__ __launch_bounds__(64 * W) void mx_rows_kernel(const MxRowsArgs a) {
 #pragma unroll
   for (int i = 0; i < NB; ++i) acc[i] = v4f{};
   const int units = (a.K + 511) >> 9;
+  const uint32_t pick = 0x0c0c0400u + 0x0101u * (uint32_t)g;
   // One unit at a time: the next one's loads wait for it, but the registers
   // that holding both would take are worth more as further waves.
   for (int u = wave; u < units; u += W) {
     v4u x[4][NB], y[4];
-    v2u wx[NB], wy;
+    ScaleWords wx[NB], wy;
     // (K % 32 == 0: a block is all inside K or all outside, where both operands
     // read zeros.  The weights' loads first: A's wait for its row's index.)
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      const bool in = 512 * u + 128 * g + 32 * s < a.K;
+      const bool in = 512 * u + 128 * s + 32 * g < a.K;
 #pragma unroll
       for (int b = 0; b < NB; ++b)
-        x[s][b] = __builtin_amdgcn_raw_buffer_load_b128(rb, in ? boff[b] + 16u * (uint32_t)s : kOOB, (uint32_t)u * 256u, 0);
+        x[s][b] = __builtin_amdgcn_raw_buffer_load_b128(rb, in ? boff[b] : kOOB, (uint32_t)u * 256u + 64u * (uint32_t)s, 0);
     }
 #pragma unroll
     for (int b = 0; b < NB; ++b) wx[b] = sb[b].load(srb, (uint32_t)u);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      const bool in = 512 * u + 128 * g + 32 * s < a.K;
-      y[s] = __builtin_amdgcn_raw_buffer_load_b128(ra, in ? aoff + 16u * (uint32_t)s : kOOB, (uint32_t)u * 256u, 0);
+      const bool in = 512 * u + 128 * s + 32 * g < a.K;
+      y[s] = __builtin_amdgcn_raw_buffer_load_b128(ra, in ? aoff : kOOB, (uint32_t)u * 256u + 64u * (uint32_t)s, 0);
     }
     wy = sa.load(sra, (uint32_t)u);
     __builtin_amdgcn_sched_barrier(0);  // (all on their way before the products)
-    const int left = a.kb - (16 * u + 4 * g);
-    const uint32_t sy = sa.get(wy, left);
+    // Blocks of the row from this lane's first of the unit on, four apart (bytes
+    // behind the row's last are the next row's: a NaN among them would meet the
+    // zeros past K).
+    const int left = (a.kb - 16 * u - g + 3) >> 2;
+    const uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : ~0u >> (32 - 8 * left);
+    const uint32_t sy = sa.get(wy, pick, keep);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const uint32_t sx = sb[b].get(wx[b], left);
+      const uint32_t sx = sb[b].get(wx[b], pick, keep);
       acc[b] = mfma<0>(x[0][b], y[0], acc[b], sx, sy);
       acc[b] = mfma<1>(x[1][b], y[1], acc[b], sx, sy);
       acc[b] = mfma<2>(x[2][b], y[2], acc[b], sx, sy);

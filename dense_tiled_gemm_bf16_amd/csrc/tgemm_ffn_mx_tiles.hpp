@@ -20,11 +20,9 @@ struct MxTraits : Traits<kFp4, true, true, true> {
 
 typedef __attribute__((ext_vector_type(8))) int v8i;
 
-// Bytes of a slice row, by tile; workgroups that share a CU.
-template <int TM>
-constexpr int kMxSlice = TM == 64 ? 256 : 128;
-template <int TM>
-constexpr int kMxShare = TM == 128 ? 2 : 1;
+// Bytes of a slice row.  TWO: two workgroups share a CU.
+template <int TM, bool TWO>
+constexpr int kMxSlice = TM == 64 && !TWO ? 256 : 128;
 
 struct MxSlots {
   LDS_AS uint8_t *a[4], *b[4];  // kNS slots of TM, TN rows
@@ -47,18 +45,19 @@ struct MxSlots {
 // most.)  A row's scales come 16 bytes at a time, those of 512 elements: a load
 // of 4 bytes a lane and slice cost the texture path as much as the rows.
 //
-// 64 x 64 tiles: slices of 256 bytes and four slots (128 KiB), 96 KiB on their way,
-// for products of few tiles.  128 x 128: slices of 128 bytes and two slots, so that two
-// workgroups share a CU and the one multiplies while the other waits or stores.
+// Few 64 x 64 tiles, one a CU: slices of 256 bytes and four slots (128 KiB), 96 KiB
+// on their way.  TWO, for more tiles than CUs: slices of 128 bytes, four slots
+// of 64 x 64 or two of 128 x 128 (64 KiB), so that two workgroups share a CU and
+// the one multiplies while the other waits or stores.
 //
 // ALIGNED: every row's scales start on a dword.  If not, a lane loads from the
 // dword that holds the first, and shifts.
-template <int DT, int TM, int TN, bool ALIGNED, class EXT>
+template <int DT, int TM, int TN, bool TWO, bool ALIGNED, class EXT>
 struct MxTile {
   static constexpr int kBlk = 16;
   static constexpr int kWM = TM / 2, kWN = TN / 2, kNBm = kWM / 16, kNBn = kWN / 16;
-  static constexpr int SL = kMxSlice<TM>, kP = SL / 64;  // bytes of a slice row; products of a slice
-  static constexpr int kNS = SL == 256 ? 4 : 2;
+  static constexpr int SL = kMxSlice<TM, TWO>, kP = SL / 64;  // bytes of a slice row; products of a slice
+  static constexpr int kNS = TM == 64 ? 4 : 2;
   static constexpr int kIR = 1024 / SL;                  // rows of a load instruction
   static constexpr int kLA = TM / 4 / kIR, kLB = TN / 4 / kIR;  // row load instructions of a wave and slice
   static constexpr int kPer16 = 16 / kIR;                // instructions after which the rows' permutation repeats
@@ -70,7 +69,9 @@ struct MxTile {
   static constexpr int kScaleBytes = kPlane * kPlanes;
   static_assert(kLA % kPer16 == 0 && kLB % kPer16 == 0 && TN % 64 == 0 && TM + TN <= 256, "whole instructions");
   static_assert((kNS - 1) * kLoads < 64, "vmcnt is 6 bits");
-  static_assert(kNS == 2 || kPairs == 1, "the waits count the same loads for every slice");
+  // Loads of the slices behind the next one that may be on their way when it is
+  // waited for: of two slices (an even and an odd one, if they share scales), or none.
+  static constexpr int kAhead = kNS == 2 ? 0 : 2 * (kLA + kLB) + 2 / kPairs * kPlanes;
 
   const Args &a;
   MxSlots slots;
@@ -184,8 +185,7 @@ struct MxTile {
     return 0;
   }
 
-  // S below is kt % 4: slot kt % kNS, scales of slices kt .. of a pair in kt /
-  // kPairs % 2 or % 4.
+  // S below is kt % 4: rows in slot kt % kNS, scales in slot S / kPairs.
   // Load I of slice kt into its slot.  The last slices check columns: what lies
   // past K arrives as zeros, and a slice past the last is all zeros.
   template <int S, int I>
@@ -213,9 +213,11 @@ struct MxTile {
   struct Frags {
     u32x4 x[kNBn], y[kNBm];
   };
-  struct Scales {
-    uint32_t x[kNBn], y[kNBm];
+  // Scales as read (block R: x blocks, then y blocks), and as the MFMAs take them.
+  struct Raw {
+    uint32_t w[kNBn + kNBm][(ALIGNED ? 1 : 2) * kPairs];
   };
+  uint32_t sc[kNBn + kNBm];
   static constexpr int kPer = kNBn * kNBm, kNR = kNBn + kNBm;  // MFMAs and fragment reads of a product
   // Fragment R (x blocks, then y blocks) of product P.
   template <int S, int P, int R>
@@ -226,37 +228,51 @@ struct MxTile {
     else
       f.y[R - kNBn] = *(const LDS_AS u32x4 *)(slots.a[S % kNS] + (wave_m * kWM + 16 * (R - kNBn)) * SL + at);
   }
-  // This lane's scales of block R, slice kt: kP bytes.  Bytes behind the row's
-  // last are the next row's: a NaN among them would meet the zeros past K.
+  // This lane's scales of block R: of slice kt, or of slices kt and kt + 1 (kt
+  // even, kPairs == 2; both at once, so that the slot is free for the pair after
+  // the next when slice kt begins).  Read in front of slice kt, made up in it
+  // (finish_scale): on the spot, each would wait for its read.
   template <int S, int R>
-  __device__ __forceinline__ void read_scale(Scales &c, int kt) const {
+  __device__ __forceinline__ void read_scale(Raw &c) const {
     const int b = R < kNBn ? wave_n * kNBn + R : TN / 16 + wave_m * kNBm + R - kNBn;
     const int g = lane >> 4;
-    // Byte of the row's 16 where this lane's start.
-    const int at = kP == 4 ? 4 * g : 8 * (S % kPairs) + 2 * g;
-    const LDS_AS uint8_t *p = slots.s[S / kPairs] + b * 256 + 16 * (lane & 15);
-    uint32_t w;
+    const LDS_AS uint8_t *p = slots.s[S / kPairs] + b * 256 + 16 * (lane & 15) + ((kP * g) & ~3);
+#pragma unroll
+    for (int h = 0; h < kPairs; ++h) {
+      c.w[R][h] = *(const LDS_AS uint32_t *)(p + 8 * h);
+      if constexpr (!ALIGNED) c.w[R][kPairs + h] = *(const LDS_AS uint32_t *)(p + 8 * h + kPlane);
+    }
+  }
+  template <int R>
+  __device__ __forceinline__ void finish_scale(const Raw &c, uint32_t keep) {
+    // (kP == 2: the lane's two bytes of each dword, two further on in odd lane groups.)
+    const int odd = (lane >> 4) & 1;
     if constexpr (ALIGNED) {
-      if constexpr (kP == 4)
-        w = *(const LDS_AS uint32_t *)(p + at);
-      else
-        w = *(const LDS_AS uint16_t *)(p + at);
+      sc[R] = (kPairs == 1 ? c.w[R][0] : __builtin_amdgcn_perm(c.w[R][kPairs - 1], c.w[R][0], odd ? 0x07060302u : 0x05040100u)) & keep;
     } else {
       const uint32_t sh = R < kNBn ? sh_x[EXT::kGated ? R & 1 : 0] : sh_y[EXT::kGather ? (R < kNBn ? 0 : R - kNBn) : 0];
-      const uint32_t lo = *(const LDS_AS uint32_t *)(p + (at & ~3)), hi = *(const LDS_AS uint32_t *)(p + kPlane + (at & ~3));
-      if constexpr (kP == 4)
-        w = __builtin_amdgcn_alignbyte(hi, lo, sh);
-      else
-        w = (uint32_t)(((uint64_t)hi << 32 | lo) >> (8 * (sh + (uint32_t)(at & 3))));  // (up to 5 bytes, for two)
+      if constexpr (kPairs == 1) {
+        sc[R] = __builtin_amdgcn_alignbyte(c.w[R][1], c.w[R][0], sh) & keep;
+      } else {
+        const uint32_t by = 8 * sh + 16 * odd;  // (up to 5 bytes on)
+        const uint32_t lo = (uint32_t)(((uint64_t)c.w[R][2] << 32 | c.w[R][0]) >> by);
+        const uint32_t hi = (uint32_t)(((uint64_t)c.w[R][3] << 32 | c.w[R][1]) >> by);
+        sc[R] = __builtin_amdgcn_perm(hi, lo, 0x05040100u) & keep;
+      }
     }
-    const int left = a.kb - (kP * 4 * kt + kP * g);
-    if (a.kb < kP * 4 * (kt + 1)) w &= left >= kP ? ~0u : left <= 0 ? 0u : ~0u >> (32 - 8 * left);
-    (R < kNBn ? c.x[R % kNBn] : c.y[(R - kNBn + kNBm) % kNBm]) = w;
+  }
+  // The bytes of a lane's scales that are the row's: those behind its last are
+  // the next row's, and a NaN among them would meet the zeros past K.
+  __device__ __forceinline__ uint32_t keep_of(int kt) const {
+    const int left = a.kb - kP * (4 * kt + (lane >> 4));
+    auto low = [](int n, int most) { return n >= most ? ~0u >> (32 - 8 * most) : n <= 0 ? 0u : ~0u >> (32 - 8 * n); };
+    if constexpr (kPairs == 1) return low(left, 4);
+    return low(left, 2) | low(left - 8, 2) << 16;
   }
   template <int S, int... R>
-  __device__ __forceinline__ void read_first(std::integer_sequence<int, R...>, Frags &f, Scales &c, int kt) const {
+  __device__ __forceinline__ void read_first(std::integer_sequence<int, R...>, Frags &f, Raw &c) const {
     (read_frag<S, 0, R>(f), ...);
-    (read_scale<S, R>(c, kt), ...);
+    (read_scale<S, R>(c), ...);
   }
 
   template <int SEL>
@@ -272,7 +288,8 @@ struct MxTile {
   //  * before the last product a wait and a barrier: slice kt + 1 has landed in
   //    every wave, and every wave holds the last fragments of slice kt, so that
   //    its slot may take slice kt + kNS;
-  //  * the last product reads the first fragments and the scales of slice kt + 1;
+  //  * the last product reads the first fragments and the scales of slice kt + 1
+  //    (of the pair that it begins);
   //  * the loads go out over kWindow MFMAs behind the barrier.
   // (Left to the compiler, the loads sank to the end of the slice, in front of
   // the wait for them, and the fragments' reads to their use: 128 x 128 tiles
@@ -280,17 +297,17 @@ struct MxTile {
   static constexpr int kWindow = (kP - 1) * kPer;
   static constexpr int load_pos(int i) { return i * kWindow / kLoads; }  // in MFMAs from the barrier on
   template <int S, int P, int Q, int R>
-  __device__ __forceinline__ void read_at(int kt, Frags &fn, Scales &cn) const {
-    constexpr int N = P == kP - 1 ? 2 * kNR : kNR;  // reads of this product
-    if constexpr (R < N)
-      if constexpr (R * kPer / N == Q) {
-        if constexpr (P < kP - 1)
-          read_frag<S, P + 1, R>(fn);
-        else if constexpr (R < kNR)
-          read_frag<(S + 1) % 4, 0, R>(fn);
-        else
-          read_scale<(S + 1) % 4, R - kNR>(cn, kt + 1);
-      }
+  __device__ __forceinline__ void read_at(int kt, Frags &fn, Raw &cn) const {
+    // (The compiler waits for loads into the scales' slots in front of these
+    // reads, whichever slot they read: right behind the barrier, in front of the next loads,
+    // it has none or few to wait for.)
+    if constexpr (P == kP - 1 && Q == 0 && (S + 1) % kPairs == 0) read_scale<(S + 1) % 4, R>(cn);
+    if constexpr (R * kPer / kNR == Q) {
+      if constexpr (P < kP - 1)
+        read_frag<S, P + 1, R>(fn);
+      else
+        read_frag<(S + 1) % 4, 0, R>(fn);
+    }
   }
   template <int S, int P, int Q, int I>
   __device__ __forceinline__ void load_at(int kt) const {
@@ -302,7 +319,7 @@ struct MxTile {
     }
   }
   template <int S, int P, int Q, int... R>
-  __device__ __forceinline__ void reads_at(std::integer_sequence<int, R...>, int kt, Frags &fn, Scales &cn) const {
+  __device__ __forceinline__ void reads_at(std::integer_sequence<int, R...>, int kt, Frags &fn, Raw &cn) const {
     (read_at<S, P, Q, R>(kt, fn, cn), ...);
   }
   template <int S, int P, int Q, int... I>
@@ -310,32 +327,39 @@ struct MxTile {
     (load_at<S, P, Q, I>(kt), ...);
   }
   template <int S, int P, int Q>
-  __device__ __forceinline__ void mfma_one(int kt, const Frags &f, Frags &fn, const Scales &c, Scales &cn) {
+  __device__ __forceinline__ void mfma_one(int kt, const Frags &f, Frags &fn, Raw &c) {
     if constexpr (P == kP - 1 && Q == 0) {
-      wait_vm_lgkm0<(kNS - 2) * kLoads>();
+      wait_vm_lgkm0<kAhead>();
       barrier();
     }
-    reads_at<S, P, Q>(std::make_integer_sequence<int, 2 * kNR>(), kt, fn, cn);
+    constexpr bool kNewScales = P == 0 && S % kPairs == 0;
+    if constexpr (kNewScales) {
+      // Blocks that this MFMA is the first to take.
+      const uint32_t keep = keep_of(kt);
+      if constexpr (Q < kNBm) finish_scale<kNBn + Q>(c, keep);
+      if constexpr (Q % kNBm == 0) finish_scale<Q / kNBm>(c, keep);
+    }
+    reads_at<S, P, Q>(std::make_integer_sequence<int, kNR>(), kt, fn, c);
     loads_at<S, P, Q>(std::make_integer_sequence<int, kLoads>(), kt);
     // (The y blocks snake, so that MFMAs side by side share an operand.)
     constexpr int I = Q / kNBm, J0 = Q % kNBm, J = (I & 1) ? kNBm - 1 - J0 : J0;
-    acc[I][J] = mma<P>(f.x[I], f.y[J], acc[I][J], c.x[I], c.y[J]);
+    acc[I][J] = mma<P + kP * (S % kPairs)>(f.x[I], f.y[J], acc[I][J], sc[I], sc[kNBn + J]);
     __builtin_amdgcn_sched_barrier(0);
   }
   template <int S, int P, int... Q>
-  __device__ __forceinline__ void product(std::integer_sequence<int, Q...>, int kt, const Frags &f, Frags &fn, const Scales &c,
-                                          Scales &cn) {
-    (mfma_one<S, P, Q>(kt, f, fn, c, cn), ...);
+  __device__ __forceinline__ void product(std::integer_sequence<int, Q...>, int kt, const Frags &f, Frags &fn, Raw &c) {
+    (mfma_one<S, P, Q>(kt, f, fn, c), ...);
   }
-  // Slice kt (S = kt % 4); its first fragments are in f0, its scales in c.
+  // Slice kt (S = kt % 4); its first fragments are in f0, its scales, if they
+  // are new, in c.
   template <int S>
-  __device__ __forceinline__ void step(int kt, Frags &f0, Frags &f1, Scales &c, Scales &cn) {
+  __device__ __forceinline__ void step(int kt, Frags &f0, Frags &f1, Raw &c) {
     constexpr auto all = std::make_integer_sequence<int, kPer>();
-    product<S, 0>(all, kt, f0, f1, c, cn);
-    product<S, 1>(all, kt, f1, f0, c, cn);
+    product<S, 0>(all, kt, f0, f1, c);
+    product<S, 1>(all, kt, f1, f0, c);
     if constexpr (kP == 4) {
-      product<S, 2>(all, kt, f0, f1, c, cn);
-      product<S, 3>(all, kt, f1, f0, c, cn);
+      product<S, 2>(all, kt, f0, f1, c);
+      product<S, 3>(all, kt, f1, f0, c);
     }
   }
   // Loads of slice kNS - 1 that go out in front of the first barrier (scales
@@ -358,21 +382,21 @@ struct MxTile {
       load_some<2>(all, 2);
     }
     load_some<kNS - 1>(std::make_integer_sequence<int, early()>(), kNS - 1);  // (row loads come first)
-    wait_vm_lgkm0<(kNS - 2) * kLoads + early()>();
+    wait_vm_lgkm0<kAhead + early()>();
     barrier();
     Frags f0, f1;
-    Scales c0, c1;
-    read_first<0>(std::make_integer_sequence<int, kNR>(), f0, c0, 0);
+    Raw c;
+    read_first<0>(std::make_integer_sequence<int, kNR>(), f0, c);
     int kt = 0;
     for (; kt + 3 < nk; kt += 4) {
-      step<0>(kt, f0, f1, c0, c1);
-      step<1>(kt + 1, f0, f1, c1, c0);
-      step<2>(kt + 2, f0, f1, c0, c1);
-      step<3>(kt + 3, f0, f1, c1, c0);
+      step<0>(kt, f0, f1, c);
+      step<1>(kt + 1, f0, f1, c);
+      step<2>(kt + 2, f0, f1, c);
+      step<3>(kt + 3, f0, f1, c);
     }
-    if (kt < nk) step<0>(kt, f0, f1, c0, c1);
-    if (kt + 1 < nk) step<1>(kt + 1, f0, f1, c1, c0);
-    if (kt + 2 < nk) step<2>(kt + 2, f0, f1, c0, c1);
+    if (kt < nk) step<0>(kt, f0, f1, c);
+    if (kt + 1 < nk) step<1>(kt + 1, f0, f1, c);
+    if (kt + 2 < nk) step<2>(kt + 2, f0, f1, c);
     // The loads still in flight into the slots.
     wait_vm_lgkm0<0>();
     x.store(*this);
@@ -407,31 +431,31 @@ struct MxTile {
   }
 };
 
-#define TGEMM_MX_SLOTS(TM, TN, SL, SCALES)                                  \
-  __shared__ __attribute__((aligned(1024))) uint8_t sA0[TM * SL];           \
-  __shared__ __attribute__((aligned(1024))) uint8_t sA1[TM * SL];           \
-  __shared__ __attribute__((aligned(1024))) uint8_t sB0[TN * SL];           \
-  __shared__ __attribute__((aligned(1024))) uint8_t sB1[TN * SL];           \
+// (Arrays, not one: the compiler then sees that a read of one slot needs no
+// wait for loads into another. It tells at most eight apart.)
+#define TGEMM_MX_SLOTS(TM, TN, SL, NS, SCALES)                              \
+  __shared__ __attribute__((aligned(1024))) uint8_t sR0[(TM + TN) * SL];    \
+  __shared__ __attribute__((aligned(1024))) uint8_t sR1[(TM + TN) * SL];    \
   __shared__ __attribute__((aligned(1024))) uint8_t sS0[SCALES];            \
   __shared__ __attribute__((aligned(1024))) uint8_t sS1[SCALES];            \
   MxSlots slots;                                                            \
-  slots.a[0] = (LDS_AS uint8_t *)sA0;                                       \
-  slots.a[1] = (LDS_AS uint8_t *)sA1;                                       \
-  slots.b[0] = (LDS_AS uint8_t *)sB0;                                       \
-  slots.b[1] = (LDS_AS uint8_t *)sB1;                                       \
+  slots.a[0] = (LDS_AS uint8_t *)sR0;                                       \
+  slots.a[1] = (LDS_AS uint8_t *)sR1;                                       \
+  slots.b[0] = (LDS_AS uint8_t *)sR0 + TM * SL;                             \
+  slots.b[1] = (LDS_AS uint8_t *)sR1 + TM * SL;                             \
   slots.s[0] = (LDS_AS uint8_t *)sS0;                                       \
   slots.s[1] = (LDS_AS uint8_t *)sS1;                                       \
+  if constexpr (NS == 4) {                                                  \
+    __shared__ __attribute__((aligned(1024))) uint8_t sR2[(TM + TN) * SL];  \
+    __shared__ __attribute__((aligned(1024))) uint8_t sR3[(TM + TN) * SL];  \
+    slots.a[2] = (LDS_AS uint8_t *)sR2;                                     \
+    slots.a[3] = (LDS_AS uint8_t *)sR3;                                     \
+    slots.b[2] = (LDS_AS uint8_t *)sR2 + TM * SL;                           \
+    slots.b[3] = (LDS_AS uint8_t *)sR3 + TM * SL;                           \
+  }                                                                         \
   if constexpr (SL == 256) {                                                \
-    __shared__ __attribute__((aligned(1024))) uint8_t sA2[TM * SL];         \
-    __shared__ __attribute__((aligned(1024))) uint8_t sA3[TM * SL];         \
-    __shared__ __attribute__((aligned(1024))) uint8_t sB2[TN * SL];         \
-    __shared__ __attribute__((aligned(1024))) uint8_t sB3[TN * SL];         \
     __shared__ __attribute__((aligned(1024))) uint8_t sS2[SCALES];          \
     __shared__ __attribute__((aligned(1024))) uint8_t sS3[SCALES];          \
-    slots.a[2] = (LDS_AS uint8_t *)sA2;                                     \
-    slots.a[3] = (LDS_AS uint8_t *)sA3;                                     \
-    slots.b[2] = (LDS_AS uint8_t *)sB2;                                     \
-    slots.b[3] = (LDS_AS uint8_t *)sB3;                                     \
     slots.s[2] = (LDS_AS uint8_t *)sS2;                                     \
     slots.s[3] = (LDS_AS uint8_t *)sS3;                                     \
   }
@@ -444,7 +468,7 @@ using MxExt = typename std::conditional<
     typename std::conditional<GATED, GatedExt<DT, GROUPED>, PlainExt>::type>::type;
 
 // One tile with its first row m0 and first column n0, by the kernel of its size.
-template <int DT, int TM, int TN, bool ALIGNED, class X>
+template <int DT, int TM, int TN, bool TWO, bool ALIGNED, class X>
 __device__ __forceinline__ void mx_tile(const Args &a, const X &x) {
   if constexpr (TM == 256) {
     using T = MxTraits<DT == 1>;
@@ -463,22 +487,22 @@ __device__ __forceinline__ void mx_tile(const Args &a, const X &x) {
     Kernel<T, 256, 256, false, X> k(a, slots, x);
     k.run();
   } else {
-    using K = MxTile<DT, TM, TN, ALIGNED, X>;
-    TGEMM_MX_SLOTS(TM, TN, K::SL, K::kScaleBytes)
+    using K = MxTile<DT, TM, TN, TWO, ALIGNED, X>;
+    TGEMM_MX_SLOTS(TM, TN, K::SL, K::kNS, K::kScaleBytes)
     K k(a, slots, x);
     k.run();
   }
 }
 
-template <int DT, int TM, int TN, bool ALIGNED, bool GATED, bool FUSED>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(kMxShare<TM>, kMxShare<TM>)))
+template <int DT, int TM, int TN, bool TWO, bool ALIGNED, bool GATED, bool FUSED>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(TWO ? 2 : 1, TWO ? 2 : 1)))
 void mx_epilogue_kernel(const Args a, const Tail t) {
 #if defined(__HIP_DEVICE_COMPILE__)
   int tm, tn;
   tile_of((int)blockIdx.x, a.tiles_m * a.tiles_n, a.tiles_m, a.tiles_n, tm, tn);
-  constexpr int kArea = (TM < TN ? TM : TN) * kMxSlice<TM>;
+  constexpr int kArea = (TM < TN ? TM : TN) * kMxSlice<TM, TWO>;
   const MxExt<DT, GATED, false, FUSED, kArea> x{tm * TM, tn * (GATED ? TN / 2 : TN), t.half, nullptr, 0, t};
-  mx_tile<DT, TM, TN, ALIGNED>(a, x);
+  mx_tile<DT, TM, TN, TWO, ALIGNED>(a, x);
 #endif
 }
 
@@ -489,8 +513,8 @@ struct MxGroups {
   int64_t stride_b, stride_sb, stride_bias;  // bytes, bytes, elements
 };
 
-template <int DT, int TM, int TN, bool ALIGNED, bool GATED, bool FUSED>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(kMxShare<TM>, kMxShare<TM>)))
+template <int DT, int TM, int TN, bool TWO, bool ALIGNED, bool GATED, bool FUSED>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(TWO ? 2 : 1, TWO ? 2 : 1)))
 void mx_grouped_kernel(const Args a0, const Tail t0, const MxGroups g) {
 #if defined(__HIP_DEVICE_COMPILE__)
   const int lane = threadIdx.x & 63;
@@ -513,15 +537,15 @@ void mx_grouped_kernel(const Args a0, const Tail t0, const MxGroups g) {
   }
   if (t.bias) t.bias += (size_t)f.e * (size_t)g.stride_bias * 2;
   if (t.pre) t.pre += (size_t)f.lo * t.ldp * 2;
-  constexpr int kArea = (TM < TN ? TM : TN) * kMxSlice<TM>;
+  constexpr int kArea = (TM < TN ? TM : TN) * kMxSlice<TM, TWO>;
   const MxExt<DT, GATED, true, FUSED, kArea> x{__builtin_amdgcn_readfirstlane(tm * TM),
                                                __builtin_amdgcn_readfirstlane(tn * (GATED ? TN / 2 : TN)), t.half,
                                                g.rows ? g.rows + f.lo : nullptr, g.src_rows, t};
-  mx_tile<DT, TM, TN, ALIGNED>(a, x);
+  mx_tile<DT, TM, TN, TWO, ALIGNED>(a, x);
 #endif
 }
 
-template <int DT, int TM, int TN, bool ALIGNED, bool GATED>
+template <int DT, int TM, int TN, bool TWO, bool ALIGNED, bool GATED>
 hipError_t launch_mx_tile(const MxGemm &g) {
   Args a{};
   a.A = static_cast<const uint8_t *>(g.A);
@@ -550,9 +574,9 @@ hipError_t launch_mx_tile(const MxGemm &g) {
     const int64_t wgs = (int64_t)a.tiles_m * a.tiles_n;
     if (!grid_ok(wgs)) return hipErrorInvalidConfiguration;
     void *args[] = {&a, &t};
-    const void *fn = reinterpret_cast<const void *>(&mx_epilogue_kernel<DT, TM, TN, ALIGNED, GATED, true>);
+    const void *fn = reinterpret_cast<const void *>(&mx_epilogue_kernel<DT, TM, TN, TWO, ALIGNED, GATED, true>);
     if constexpr (kBare)
-      if (!fused) fn = reinterpret_cast<const void *>(&mx_epilogue_kernel<DT, TM, TN, ALIGNED, GATED, false>);
+      if (!fused) fn = reinterpret_cast<const void *>(&mx_epilogue_kernel<DT, TM, TN, TWO, ALIGNED, GATED, false>);
     return hipLaunchKernel(fn, dim3((unsigned)wgs), dim3(kThreads), args, 0, g.stream);
   }
   // The most tiles the groups can have: each one's last may be partial.
@@ -560,23 +584,27 @@ hipError_t launch_mx_tile(const MxGemm &g) {
   if (!grid_ok(wgs)) return hipErrorInvalidConfiguration;
   MxGroups gr{g.offsets, g.rows, (int)g.groups, (int)g.M, (int)g.src_rows, g.stride_b, g.stride_sb, g.N};
   void *args[] = {&a, &t, &gr};
-  const void *fn = reinterpret_cast<const void *>(&mx_grouped_kernel<DT, TM, TN, ALIGNED, GATED, true>);
+  const void *fn = reinterpret_cast<const void *>(&mx_grouped_kernel<DT, TM, TN, TWO, ALIGNED, GATED, true>);
   if constexpr (kBare)
-    if (!fused) fn = reinterpret_cast<const void *>(&mx_grouped_kernel<DT, TM, TN, ALIGNED, GATED, false>);
+    if (!fused) fn = reinterpret_cast<const void *>(&mx_grouped_kernel<DT, TM, TN, TWO, ALIGNED, GATED, false>);
   return hipLaunchKernel(fn, dim3((unsigned)wgs), dim3(kThreads), args, 0, g.stream);
 }
 
-template <int DT, int TM, int TN, bool ALIGNED>
+template <int DT, int TM, int TN, bool TWO, bool ALIGNED>
 hipError_t launch_mx_gated(const MxGemm &g) {
-  return is_gated(g.act) ? launch_mx_tile<DT, TM, TN, ALIGNED, true>(g) : launch_mx_tile<DT, TM, TN, ALIGNED, false>(g);
+  return is_gated(g.act) ? launch_mx_tile<DT, TM, TN, TWO, ALIGNED, true>(g)
+                         : launch_mx_tile<DT, TM, TN, TWO, ALIGNED, false>(g);
+}
+template <int DT, int TM, int TN, bool TWO>
+hipError_t launch_mx_aligned(const MxGemm &g) {
+  return mx_scales_aligned(g) ? launch_mx_gated<DT, TM, TN, TWO, true>(g) : launch_mx_gated<DT, TM, TN, TWO, false>(g);
 }
 
 template <int DT>
-hipError_t launch_mx_tiles_dt(const MxGemm &g, int tm) {
-  if (tm == 256) return launch_mx_gated<DT, 256, 256, true>(g);
-  const bool aligned = mx_scales_aligned(g);
-  if (tm == 128) return aligned ? launch_mx_gated<DT, 128, 128, true>(g) : launch_mx_gated<DT, 128, 128, false>(g);
-  return aligned ? launch_mx_gated<DT, 64, 64, true>(g) : launch_mx_gated<DT, 64, 64, false>(g);
+hipError_t launch_mx_tiles_dt(const MxGemm &g, int tm, bool two) {
+  if (tm == 256) return launch_mx_gated<DT, 256, 256, false, true>(g);
+  if (tm == 128) return launch_mx_aligned<DT, 128, 128, true>(g);
+  return two ? launch_mx_aligned<DT, 64, 64, true>(g) : launch_mx_aligned<DT, 64, 64, false>(g);
 }
 
 }  // namespace
