@@ -3,6 +3,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "tgemm_ffn_internal.hpp"
 
@@ -21,44 +22,44 @@ int mx_splits(int64_t, int64_t, int64_t) { return 1; }
 
 namespace {
 
-// A round is one tile a CU, or two of 128 x 128; it takes about base + slice *
-// (K / 256) us, and more with an epilogue that is not the rounding alone
-// (tile 128: half a round of tiles takes 0.72 of one).  Measured, us, the rounding
-// alone | bias, gelu and residual | swiglu alone:
+// A round is one 256 x 256 tile a CU or two of the smaller ones; it takes about base +
+// slice * (K / 256) us, and more with an epilogue that is not the rounding
+// alone; up to one smaller tile a CU take 0.6 of a round.  Measured, us, with the
+// rounding alone | bias, gelu and residual | swiglu alone:
 //   M     N     K      64                   128                 256
-//   256   4096  4096   9.4   11.5  9.6      14.7  18.4  14.1    25.5  39.5  30.2
-//   512   4096  4096   16.9  19.4  17.6     14.9  18.6  15.0    25.8  39.3  30.5
-//   2048  4096  4096   60    69    60       23.0  29.2  22.1    27.0  43.1  33.2
-//   4096  4096  1024   57    76    58       17.3  28.3  14.5    14.1  29.4  19.6
-//   4096  4096  2048   80    96    79       25.0  34.9  22.7    20.3  35.3  25.6
-//   4096  4096  8192   184   202   182      79.2  88.5  78.5    60.1  74.9  65.8
-//   8192  8192  4096   457   544   454      177   223   170     134   187   147
+//   256   4096  4096   8.1   9.2   7.6      14.2  17.5  13.6    25.6  39.1  30.0
+//   512   4096  4096   11.7  13.6  11.4     14.3  18.0  13.9    25.6  39.3  30.1
+//   1024  4096  4096   20.4  24.1  20.2     16.8  20.2  15.5    26.8  40.2  31.7
+//   2048  4096  4096   37.6  40.9  36.0     23.2  30.0  22.3    29.0  44.0  35.7
+//   4096  4096  1024   29.7  39.2  29.0     18.1  27.5  14.7    14.4  28.5  19.2
+//   4096  4096  2048   42.8  49.8  41.0     25.8  33.5  22.7    20.6  34.7  25.5
+//   4096  4096  8192   135   137   130      78.6  87.1  79.2    59.5  73.2  64.6
+//   8192  8192  4096   284   328   282      165   211   159     131   188   146
 struct MxShape {
   int tm, per_round;
   double base, slice, fused, gated;
 };
 constexpr MxShape kMxShapes[] = {
-    {256, 256, 7.5, 1.64, 15.4, 6.0}, {128, 512, 4.6, 1.10, 5.0, -0.8}, {64, 256, 3.0, 0.27, 1.0, 0.0}};
+    {256, 256, 5.0, 1.63, 14.5, 6.0}, {128, 512, 3.3, 1.085, 4.5, -1.0}, {64, 512, 1.5, 0.48, 0.8, -0.3}};
+
+// Tiles of tm x tm, of groups of any sizes: a group's last one is half full on
+// average, and every group that has rows has one.
+double tiles_of(const MxGemm &g, int tm) {
+  const double across = (double)((g.N + tm - 1) / tm);
+  if (!g.groups) return (double)((g.M + tm - 1) / tm) * across;
+  const double hit = (double)std::min(g.groups, g.M);
+  return std::max(hit, (double)g.M / tm + 0.5 * hit) * across;
+}
 
 int pick(const MxGemm &g) {
   int best = 0;
   double best_t = 0;
   const bool gated = is_gated(g.act), fused = g.bias || g.residual || g.preact || (!gated && g.act != kNone);
-  const int64_t hit = std::min(g.groups, g.M);
   for (const MxShape &s : kMxShapes) {
     if (s.tm == 256 && !big_tile(g)) continue;
-    double rounds;
-    if (g.groups) {
-      // A group's last tile is half full on average, and the groups' tiles do not
-      // fill their last round.
-      const double tiles = ((double)g.M / s.tm + 0.5 * (double)hit) * (double)((g.N + s.tm - 1) / s.tm);
-      rounds = tiles / s.per_round;
-      rounds = rounds < 0.5 ? (s.per_round > 256 ? 0.72 : 1.0) : rounds < 1.0 ? 1.0 : rounds + 0.5;
-    } else {
-      const int64_t tiles = ((g.M + s.tm - 1) / s.tm) * ((g.N + s.tm - 1) / s.tm);
-      const int64_t rest = tiles % s.per_round;
-      rounds = (double)(tiles / s.per_round) + (rest == 0 ? 0.0 : rest <= 256 && s.per_round > 256 ? 0.72 : 1.0);
-    }
+    const double tiles = tiles_of(g, s.tm), whole = std::floor(tiles / s.per_round), rest = tiles - whole * s.per_round;
+    double rounds = whole + (rest <= 0 ? 0.0 : rest <= 256 && s.per_round > 256 ? 0.6 : 1.0);
+    if (g.groups && whole > 0) rounds = tiles / s.per_round + 0.5;  // (the groups end at different times)
     const double t = rounds * (s.base + s.slice * (double)g.K / 256.0 + (gated ? s.gated : 0.0) + (fused ? s.fused * (gated ? 0.5 : 1.0) : 0.0));
     if (best == 0 || t < best_t) {
       best = s.tm;
@@ -68,17 +69,27 @@ int pick(const MxGemm &g) {
   return best;
 }
 
+// Whether a product takes the kernel for few rows: up to 16 rows of one
+// weight, up to 10 a group on average, where 64 x 64 tiles are fewer than half
+// the CUs or K is short; with more of them those read the weights faster.  us, this
+// kernel and 64 x 64 tiles:
+//   one row: 4096 x 4096 5.2 and 7.4, 1024 x 8192 5.7 and 8.9, 4096 x 1024 5.3 and
+//   5.7, 8192 x 8192 11.3 and 11.0, 32768 x 4096 15.9 and 13.5; 16 rows of 8192 x
+//   4096 8.3 and 7.7; 64 gated experts of 2048 x 2048, 6 hit 6.7 and 6.5, 55 hit
+//   by 4 rows each 32.5 and 31.9; 55 of 2048 x 1024 16.8 and 18.4.
+bool few_rows(const MxGemm &g) {
+  if (g.M > (g.groups ? 10 * g.groups : 16)) return false;
+  return g.K <= 1024 || tiles_of(g, 64) < 0.5 * g.cus;
+}
+
 }  // namespace
 
 hipError_t launch_mx(const MxGemm &g) {
   int tm = g.tile_m;
-  if (tm == 0) tm = g.M <= (g.groups ? 10 * g.groups : 16) ? 16 : pick(g);
+  if (tm == 0) tm = few_rows(g) ? 16 : pick(g);
   if (tm == 16) return launch_mx_rows(g);
-  bool two = false;
-  if (tm == 64) {
-    const int64_t tiles = g.groups ? g.M / 64 + std::min(g.groups, g.M) : (g.M + 63) / 64;
-    two = tiles * ((g.N + 63) / 64) > 256;
-  }
+  // 64 x 64 tiles: one a CU with a deep ring while they are that few, else two.
+  const bool two = tm == 64 && tiles_of(g, 64) > (double)g.cus;
   return g.dtype == 1 ? launch_mx_f16(g, tm, two) : launch_mx_bf16(g, tm, two);
 }
 

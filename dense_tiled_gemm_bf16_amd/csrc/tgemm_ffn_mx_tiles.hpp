@@ -215,7 +215,7 @@ struct MxTile {
   };
   // Scales as read (block R: x blocks, then y blocks), and as the MFMAs take them.
   struct Raw {
-    uint32_t w[kNBn + kNBm][(ALIGNED ? 1 : 2) * kPairs];
+    uint32_t w[kNBn + kNBm][kPairs == 2 ? 4 : ALIGNED ? 1 : 2];
   };
   uint32_t sc[kNBn + kNBm];
   static constexpr int kPer = kNBn * kNBm, kNR = kNBn + kNBm;  // MFMAs and fragment reads of a product
@@ -236,7 +236,14 @@ struct MxTile {
   __device__ __forceinline__ void read_scale(Raw &c) const {
     const int b = R < kNBn ? wave_n * kNBn + R : TN / 16 + wave_m * kNBm + R - kNBn;
     const int g = lane >> 4;
-    const LDS_AS uint8_t *p = slots.s[S / kPairs] + b * 256 + 16 * (lane & 15) + ((kP * g) & ~3);
+    const LDS_AS uint8_t *p = slots.s[S / kPairs] + b * 256 + 16 * (lane & 15);
+    if constexpr (ALIGNED && kPairs == 2) {
+      const u32x4 v = *(const LDS_AS u32x4 *)p;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c.w[R][i] = v[i];
+      return;
+    }
+    p += (kP * g) & ~3;
 #pragma unroll
     for (int h = 0; h < kPairs; ++h) {
       c.w[R][h] = *(const LDS_AS uint32_t *)(p + 8 * h);
@@ -245,16 +252,20 @@ struct MxTile {
   }
   template <int R>
   __device__ __forceinline__ void finish_scale(const Raw &c, uint32_t keep) {
-    // (kP == 2: the lane's two bytes of each dword, two further on in odd lane groups.)
-    const int odd = (lane >> 4) & 1;
     if constexpr (ALIGNED) {
-      sc[R] = (kPairs == 1 ? c.w[R][0] : __builtin_amdgcn_perm(c.w[R][kPairs - 1], c.w[R][0], odd ? 0x07060302u : 0x05040100u)) & keep;
+      if constexpr (kPairs == 1) {
+        sc[R] = c.w[R][0] & keep;
+      } else {
+        const uint32_t pick = 0x0100u + 0x0202u * (uint32_t)(lane >> 4);  // bytes 2 g and 2 g + 1 of eight
+        sc[R] = (__builtin_amdgcn_perm(c.w[R][1], c.w[R][0], 0x0c0c0000u | pick) |
+                 __builtin_amdgcn_perm(c.w[R][3], c.w[R][2], pick << 16 | 0x0c0cu)) & keep;
+      }
     } else {
       const uint32_t sh = R < kNBn ? sh_x[EXT::kGated ? R & 1 : 0] : sh_y[EXT::kGather ? (R < kNBn ? 0 : R - kNBn) : 0];
       if constexpr (kPairs == 1) {
         sc[R] = __builtin_amdgcn_alignbyte(c.w[R][1], c.w[R][0], sh) & keep;
       } else {
-        const uint32_t by = 8 * sh + 16 * odd;  // (up to 5 bytes on)
+        const uint32_t by = 8 * sh + 16 * ((lane >> 4) & 1);  // (up to 5 bytes on)
         const uint32_t lo = (uint32_t)(((uint64_t)c.w[R][2] << 32 | c.w[R][0]) >> by);
         const uint32_t hi = (uint32_t)(((uint64_t)c.w[R][3] << 32 | c.w[R][1]) >> by);
         sc[R] = __builtin_amdgcn_perm(hi, lo, 0x05040100u) & keep;
