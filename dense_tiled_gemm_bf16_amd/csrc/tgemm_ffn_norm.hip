@@ -55,11 +55,20 @@ struct Eight {
 };
 constexpr int bytes_of(int dt) { return dt == 2 ? 4 : 2; }
 
-// Sum over the wave, in every lane.
+// Sum over the wave, in every lane: rows of 16 lanes by shifts, then the rows'
+// totals handed on, the wave's in lane 63.  (By lane exchanges through LDS, six
+// one after the other, a row's two sums took 0.4 us.)
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d, 64);
-  return v;
+  auto add = [&](auto ctrl) {
+    v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), decltype(ctrl)::value, 0xf, 0xf, true));
+  };
+  add(Int<0x111>());
+  add(Int<0x112>());
+  add(Int<0x114>());
+  add(Int<0x118>());
+  v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x142, 0xa, 0xf, false));
+  v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x143, 0xc, 0xf, false));
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
 
 struct NormArgs {
@@ -190,6 +199,8 @@ hipError_t launch_norm_types(const Norm &g) {
     fn = reinterpret_cast<const void *>(&norm_kernel<DT, WDT, 256, 1>);
   } else if (g.N <= 4096) {
     fn = reinterpret_cast<const void *>(&norm_kernel<DT, WDT, 256, 2>);
+  } else if (g.N <= 6144) {
+    fn = reinterpret_cast<const void *>(&norm_kernel<DT, WDT, 256, 3>);
   } else if (g.N <= 8192) {
     fn = reinterpret_cast<const void *>(&norm_kernel<DT, WDT, 256, 4>);
   } else if (g.N <= 16384) {
@@ -207,11 +218,21 @@ hipError_t launch_norm_types(const Norm &g) {
 // ---------------------------------------------------------------------------
 // Gradients.
 //
-// Rows of any length in two steps: norm_rows_kernel, a row a workgroup, leaves
+// Rows of up to 8192 values in one pass (norm_grad_kernel): T threads hold a row
+// of x, dy and the residual in registers between its two sums and dx, and add
+// up dy h and dy of their own columns over all the rows that their workgroup
+// takes.  The workgroups, one a CU (two of 1032 to 2048 values), take sets of rows in turn; the sums of the row groups of a workgroup meet in LDS, those of the
+// workgroups in the workspace, where norm_sum_kernel adds them in order (atomics
+// would add them in another each time).  The next rows are loaded before the
+// sums of the present ones are waited for.
+//
+// Longer rows in two steps: norm_rows_kernel, a row a workgroup, leaves
 // mean(g) and mean(g h) in the workspace; norm_columns_kernel takes kRowsWg
 // rows and 256 columns (as the epilogue's gradient), writes dx and adds up its
-// columns of dy h and dy.  norm_sum_kernel adds those of all row blocks.
+// columns.  (8192 x 4096 bf16 with the residual this way 23 + 57 us, in one pass
+// 53, 5.1 TB/s; but 2048 x 12288 48 and 69, whose one pass would spill.)
 // ---------------------------------------------------------------------------
+constexpr int kGradWgs = 256;
 constexpr int kRowsWg = 64;
 
 struct NormGradArgs {
@@ -224,6 +245,142 @@ struct NormGradArgs {
   float inv_n;
   int tiles_n, blocks;
 };
+
+template <int DT, int WDT, int T, int P>
+__global__ __launch_bounds__(512) void norm_grad_kernel(const NormGradArgs a) {
+  constexpr int kB = bytes_of(DT), kW = bytes_of(WDT), kGroups = 512 / T, kWaves = T / 64;
+  constexpr bool kAhead = DT != 2;  // (registers for two sets of rows)
+  __shared__ float part[2][kGroups][2][kWaves];
+  __shared__ float sums[2 * P * 8 * T];
+  const int t = (int)threadIdx.x % T, group = (int)threadIdx.x / T;
+  struct Row {
+    Eight<DT> x[P], d[P], r[P];
+    float mu, rs;
+  };
+  auto load = [&](Row &v, int row) {
+    const bool in = row < a.M;
+    v.mu = in ? a.mean[row] : 0.0f;
+    v.rs = in ? a.rstd[row] : 0.0f;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int n = (p * T + t) * 8;
+      v.x[p] = v.d[p] = v.r[p] = Eight<DT>{};
+      if (in && n < a.N) {
+        v.x[p].load(a.x + (size_t)row * a.ldx + (size_t)n * kB);
+        v.d[p].load(a.dy + (size_t)row * a.ldd + (size_t)n * kB);
+        if (a.res) v.r[p].load(a.res + (size_t)row * a.ldr + (size_t)n * kB);
+      }
+    }
+  };
+  Eight<WDT> w[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int n = (p * T + t) * 8;
+    w[p] = Eight<WDT>{};
+    if (a.w && n < a.N) w[p].load(a.w + (size_t)n * kW);
+  }
+  float sw[P][8] = {}, sb[P][8] = {};
+  const int step = a.blocks * kGroups, first = (int)blockIdx.x * kGroups;
+  Row cur;
+  load(cur, first + group);
+  int which = 0;
+  // (row0 is the workgroup's: every thread takes as many turns.)
+  for (int row0 = first; row0 < a.M; row0 += step, which ^= 1) {
+    const int row = row0 + group;
+    float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      float d[8], x[8], wv[8];
+      cur.x[p].get(x);
+      cur.d[p].get(d);
+      w[p].get(wv);
+      const bool in = (p * T + t) * 8 < a.N;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float h = in ? (x[q] - cur.mu) * cur.rs : 0.0f, g = a.w ? d[q] * wv[q] : d[q];
+        s0 += g;
+        s1 += g * h;
+        sw[p][q] += d[q] * h;
+        sb[p][q] += d[q];
+      }
+    }
+    Row next;
+    if constexpr (kAhead) load(next, row + step);
+    s0 = wave_sum(s0);
+    s1 = wave_sum(s1);
+    if constexpr (kWaves > 1) {
+      if ((threadIdx.x & 63) == 0) {
+        part[which][group][0][t >> 6] = s0;
+        part[which][group][1][t >> 6] = s1;
+      }
+      __syncthreads();  // (the buffers alternate: the next turn's writes need no barrier of their own)
+      s0 = s1 = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kWaves; ++i) {
+        s0 += part[which][group][0][i];
+        s1 += part[which][group][1][i];
+      }
+    }
+    const float c0 = s0 * a.inv_n, c1 = s1 * a.inv_n;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int n = (p * T + t) * 8;
+      float d[8], x[8], wv[8], r[8], o[8];
+      cur.d[p].get(d);
+      cur.x[p].get(x);
+      w[p].get(wv);
+      cur.r[p].get(r);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) o[q] = cur.rs * ((a.w ? d[q] * wv[q] : d[q]) - c0 - (x[q] - cur.mu) * cur.rs * c1) + r[q];
+      if (row < a.M && n < a.N) {
+        Eight<DT> e;
+        e.set(o);
+        e.store(a.dx + (size_t)row * a.ldo + (size_t)n * kB);
+      }
+    }
+    if constexpr (kAhead)
+      cur = next;
+    else
+      load(cur, row + step);
+  }
+  if (!a.dw && !a.db) return;
+  // The row groups' sums one after the other, into the first's registers.
+#pragma unroll 1
+  for (int g = 1; g < kGroups; ++g) {
+    __syncthreads();
+    if (group == g) {
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          sums[(p * 8 + q) * T + t] = sw[p][q];
+          sums[((P + p) * 8 + q) * T + t] = sb[p][q];
+        }
+    }
+    __syncthreads();
+    if (group == 0) {
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          sw[p][q] += sums[(p * 8 + q) * T + t];
+          sb[p][q] += sums[((P + p) * 8 + q) * T + t];
+        }
+    }
+  }
+  if (group > 0) return;
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int n = (p * T + t) * 8;
+    if (n >= a.N) continue;
+    float *c = a.colsums + (size_t)blockIdx.x * 2 * a.N + n;
+    *(v4f *)c = v4f{sw[p][0], sw[p][1], sw[p][2], sw[p][3]};
+    *(v4f *)(c + 4) = v4f{sw[p][4], sw[p][5], sw[p][6], sw[p][7]};
+    c += a.N;
+    *(v4f *)c = v4f{sb[p][0], sb[p][1], sb[p][2], sb[p][3]};
+    *(v4f *)(c + 4) = v4f{sb[p][4], sb[p][5], sb[p][6], sb[p][7]};
+  }
+}
 
 template <int DT, int WDT>
 __global__ __launch_bounds__(256) void norm_rows_kernel(const NormGradArgs a) {
@@ -349,6 +506,14 @@ __global__ __launch_bounds__(1024) void norm_sum_kernel(const NormGradArgs a) {
   }
 }
 
+constexpr int64_t kFusedMost = 8192;  // values of a row
+// Blocks of column sums in the workspace.
+int grad_blocks(int64_t M, int64_t N) {
+  if (N > kFusedMost) return (int)((M + kRowsWg - 1) / kRowsWg);
+  const int groups = N <= 1024 ? 8 : N <= 4096 ? 2 : 1;  // rows of a workgroup at a time
+  return (int)std::min<int64_t>((M + groups - 1) / groups, N > 1024 && N <= 2048 ? 2 * kGradWgs : kGradWgs);
+}
+
 template <int DT, int WDT>
 hipError_t launch_norm_grad_types(const NormGrad &g) {
   const int b = bytes_of(DT);
@@ -370,12 +535,19 @@ hipError_t launch_norm_grad_types(const NormGrad &g) {
   a.ldo = g.ldo * b;
   a.inv_n = (float)(1.0 / (double)g.N);
   a.tiles_n = (a.N + 255) / 256;
-  a.blocks = (int)((g.M + kRowsWg - 1) / kRowsWg);
+  a.blocks = grad_blocks(g.M, g.N);
   a.rowsums = g.ws;
-  a.colsums = g.ws + (g.M + 1) / 2 * 4;
+  a.colsums = g.ws + (g.N > kFusedMost ? (g.M + 1) / 2 * 4 : 0);
   void *args[] = {&a};
   hipError_t e = hipSuccess;
-  if (g.M > 0) {
+  if (g.M > 0 && g.N <= kFusedMost) {
+    const void *fn = g.N <= 512    ? reinterpret_cast<const void *>(&norm_grad_kernel<DT, WDT, 64, 1>)
+                     : g.N <= 1024 ? reinterpret_cast<const void *>(&norm_grad_kernel<DT, WDT, 64, 2>)
+                     : g.N <= 2048 ? reinterpret_cast<const void *>(&norm_grad_kernel<DT, WDT, 256, 1>)
+                     : g.N <= 4096 ? reinterpret_cast<const void *>(&norm_grad_kernel<DT, WDT, 256, 2>)
+                                   : reinterpret_cast<const void *>(&norm_grad_kernel<DT, WDT, 512, 2>);
+    e = hipLaunchKernel(fn, dim3((unsigned)a.blocks), dim3(512), args, 0, g.stream);
+  } else if (g.M > 0) {
     const int64_t wgs = (int64_t)a.blocks * a.tiles_n;
     if (g.M > (int64_t)(UINT32_MAX / 256) || wgs > (int64_t)(UINT32_MAX / 256)) return hipErrorInvalidConfiguration;
     e = hipLaunchKernel(reinterpret_cast<const void *>(&norm_rows_kernel<DT, WDT>), dim3((unsigned)g.M), dim3(256), args, 0,
@@ -393,7 +565,7 @@ hipError_t launch_norm_grad_types(const NormGrad &g) {
 }  // namespace
 
 uint64_t norm_grad_ws_floats(int64_t M, int64_t N) {
-  return (uint64_t)((M + 1) / 2 * 4) + (uint64_t)((M + kRowsWg - 1) / kRowsWg) * 2u * (uint64_t)N;
+  return (N > kFusedMost ? (uint64_t)((M + 1) / 2 * 4) : 0u) + (uint64_t)grad_blocks(M, N) * 2u * (uint64_t)N;
 }
 
 hipError_t launch_norm(const Norm &g) {

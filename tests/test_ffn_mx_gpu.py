@@ -121,6 +121,19 @@ def test_quantize_every_scale():
     check_quant(x)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_quantize_every_16_bit_value(dtype):
+    """Each as the largest of its block, with parts of it beside; in rows and columns."""
+    x = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(dtype)
+    v = torch.zeros(65536, 32, dtype=dtype)
+    v[:, 0] = x
+    for i, part in enumerate((0.04, 0.05, 0.1, 0.13, 0.2, 0.21, 0.3, 0.42, 0.5, 0.6, 0.84, 0.99)):
+        v[:, 2 + i] = (x.float() * (part if i % 2 else -part)).to(dtype)
+    same_bits(tg.quantize_mxfp4(v.cuda()), more.quantize(v), "rows")
+    u = v[::7].t().contiguous()
+    same_bits(tg.quantize_mxfp4(u[:, :9344].contiguous().cuda(), rows=False, columns=True), more.quantize(u[:, :9344].t()), "columns")
+
+
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])
 def test_quantize_not_finite(dtype):
     x = rand(3, 70, 96, dtype=dtype)
