@@ -674,7 +674,9 @@ PyObject *quantize(Args o) {
   }
   if (columns) {
     const int64_t blocks = (p.M + 31) / 32;
-    t[n] = on.out(o[5], "qt", b, {p.N, 16 * blocks});
+    // (Rows of a new qt start on a cache line, whatever M is: a product's loads would
+    // take every line of rows that do not twice.)
+    t[n] = o[5] == Py_None ? on.empty({p.N, (16 * blocks + 127) / 128 * 128}, b).narrow(1, 0, 16 * blocks) : tensor(o[5], "qt");
     p.ldqt = on.mat(t[n], "qt", b, p.N, 16 * blocks);
     p.qt = ptr(t[n]);
     t[n + 1] = on.out(o[6], "scalest", b, {p.N, blocks});

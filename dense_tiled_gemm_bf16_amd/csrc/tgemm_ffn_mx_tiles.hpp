@@ -471,12 +471,61 @@ struct MxTile {
     slots.s[3] = (LDS_AS uint8_t *)sS3;                                     \
   }
 
-// FUSED: with the operands of the epilogue or an activation that is not gated;
-// else a gated activation alone, or none.
-template <int DT, bool GATED, bool GROUPED, bool FUSED, int AREA>
+// A bias alone, straight from the accumulators (as the rounding alone): lane l
+// holds row l % 16 and columns 4 (l / 16) .. + 3 of each block.  (4096 x 4096 x 2048
+// through LDS 29 us.)
+template <int DT, bool GROUPED>
+struct BiasExt {
+  static constexpr bool kOn = true, kGated = false, kGather = GROUPED, kPrefetch = true;
+  int m0, n0;
+  int half;
+  const int32_t *rows;
+  int src_rows;
+  Tail t;
+  template <class K>
+  __device__ __forceinline__ void store(K &k) const {
+    const int q = k.lane >> 4;
+    float b[K::kNBn][4];
+#pragma unroll
+    for (int i = 0; i < K::kNBn; ++i) {
+      const int n = min(n0 + k.wave_n * K::kWN + 16 * i + 4 * q, k.a.N - 4);
+      const v2u w = *(const v2u *)(t.bias + (size_t)n * 2);
+      unpack2<DT>(w[0], b[i]);
+      unpack2<DT>(w[1], b[i] + 2);
+    }
+#pragma unroll
+    for (int j = 0; j < K::kNBm; ++j) {
+      const int m = m0 + k.wave_m * K::kWM + j * 16 + (k.lane & 15);
+      uint8_t *crow = k.a.C + (size_t)m * k.a.ldc * 2;
+#pragma unroll
+      for (int i = 0; i < K::kNBn; i += 2) {
+        const f32x4 &u = k.acc[i][j], &v = k.acc[i + 1][j];
+        const uint32_t us[2] = {pack2<DT>(u[0] + b[i][0], u[1] + b[i][1]), pack2<DT>(u[2] + b[i][2], u[3] + b[i][3])};
+        const uint32_t vs[2] = {pack2<DT>(v[0] + b[i + 1][0], v[1] + b[i + 1][1]),
+                                pack2<DT>(v[2] + b[i + 1][2], v[3] + b[i + 1][3])};
+        uint32_t xo[2], yo[2];
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+          const auto h = __builtin_amdgcn_permlane32_swap(us[d], vs[d], false, false);
+          const auto r = __builtin_amdgcn_permlane16_swap(h[0], h[1], false, false);
+          xo[d] = r[0];
+          yo[d] = r[1];
+        }
+        const int n = n0 + k.wave_n * K::kWN + i * 16 + 8 * q;
+        if (m < k.a.M && n < k.a.N) store_c(crow + (size_t)n * 2, u32x4{xo[0], xo[1], yo[0], yo[1]});
+      }
+    }
+  }
+};
+
+// What the epilogue has to do: the rounding alone or a gated activation alone, a
+// bias alone, or anything.
+enum : int { kBare = 0, kBias = 1, kFull = 2 };
+template <int DT, bool GATED, bool GROUPED, int EPI, int AREA>
 using MxExt = typename std::conditional<
-    FUSED, FfnExt<DT, GATED, GROUPED, AREA>,
-    typename std::conditional<GATED, GatedExt<DT, GROUPED>, PlainExt>::type>::type;
+    EPI == kFull, FfnExt<DT, GATED, GROUPED, AREA>,
+    typename std::conditional<EPI == kBias, BiasExt<DT, GROUPED>,
+                              typename std::conditional<GATED, GatedExt<DT, GROUPED>, PlainExt>::type>::type>::type;
 
 // One tile with its first row m0 and first column n0, by the kernel of its size.
 template <int DT, int TM, int TN, bool TWO, bool ALIGNED, class X>
@@ -505,14 +554,14 @@ __device__ __forceinline__ void mx_tile(const Args &a, const X &x) {
   }
 }
 
-template <int DT, int TM, int TN, bool TWO, bool ALIGNED, bool GATED, bool FUSED>
+template <int DT, int TM, int TN, bool TWO, bool ALIGNED, bool GATED, int EPI>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(TWO ? 2 : 1, TWO ? 2 : 1)))
 void mx_epilogue_kernel(const Args a, const Tail t) {
 #if defined(__HIP_DEVICE_COMPILE__)
   int tm, tn;
   tile_of((int)blockIdx.x, a.tiles_m * a.tiles_n, a.tiles_m, a.tiles_n, tm, tn);
   constexpr int kArea = (TM < TN ? TM : TN) * kMxSlice<TM, TWO>;
-  const MxExt<DT, GATED, false, FUSED, kArea> x{tm * TM, tn * (GATED ? TN / 2 : TN), t.half, nullptr, 0, t};
+  const MxExt<DT, GATED, false, EPI, kArea> x{tm * TM, tn * (GATED ? TN / 2 : TN), t.half, nullptr, 0, t};
   mx_tile<DT, TM, TN, TWO, ALIGNED>(a, x);
 #endif
 }
@@ -524,7 +573,7 @@ struct MxGroups {
   int64_t stride_b, stride_sb, stride_bias;  // bytes, bytes, elements
 };
 
-template <int DT, int TM, int TN, bool TWO, bool ALIGNED, bool GATED, bool FUSED>
+template <int DT, int TM, int TN, bool TWO, bool ALIGNED, bool GATED, int EPI>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(TWO ? 2 : 1, TWO ? 2 : 1)))
 void mx_grouped_kernel(const Args a0, const Tail t0, const MxGroups g) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -549,7 +598,7 @@ void mx_grouped_kernel(const Args a0, const Tail t0, const MxGroups g) {
   if (t.bias) t.bias += (size_t)f.e * (size_t)g.stride_bias * 2;
   if (t.pre) t.pre += (size_t)f.lo * t.ldp * 2;
   constexpr int kArea = (TM < TN ? TM : TN) * kMxSlice<TM, TWO>;
-  const MxExt<DT, GATED, true, FUSED, kArea> x{__builtin_amdgcn_readfirstlane(tm * TM),
+  const MxExt<DT, GATED, true, EPI, kArea> x{__builtin_amdgcn_readfirstlane(tm * TM),
                                                __builtin_amdgcn_readfirstlane(tn * (GATED ? TN / 2 : TN)), t.half,
                                                g.rows ? g.rows + f.lo : nullptr, g.src_rows, t};
   mx_tile<DT, TM, TN, TWO, ALIGNED>(a, x);
@@ -579,15 +628,16 @@ hipError_t launch_mx_tile(const MxGemm &g) {
   Tail t{static_cast<const uint8_t *>(g.bias), static_cast<const uint8_t *>(g.residual), static_cast<uint8_t *>(g.preact),
          (int)g.ldr, (int)g.ldp, g.act, GATED ? a.N : 0};
   // (A gated 256 x 256 tile straight from the accumulators would spill.)
-  const bool fused = g.bias || g.residual || g.preact || (GATED ? TM == 256 : g.act != kNone);
-  constexpr bool kBare = !(GATED && TM == 256);
+  const int epi = g.residual || g.preact || (GATED ? g.bias || TM == 256 : g.act != kNone) ? kFull : g.bias ? kBias : kBare;
   if (g.groups == 0) {
     const int64_t wgs = (int64_t)a.tiles_m * a.tiles_n;
     if (!grid_ok(wgs)) return hipErrorInvalidConfiguration;
     void *args[] = {&a, &t};
-    const void *fn = reinterpret_cast<const void *>(&mx_epilogue_kernel<DT, TM, TN, TWO, ALIGNED, GATED, true>);
-    if constexpr (kBare)
-      if (!fused) fn = reinterpret_cast<const void *>(&mx_epilogue_kernel<DT, TM, TN, TWO, ALIGNED, GATED, false>);
+    const void *fn = reinterpret_cast<const void *>(&mx_epilogue_kernel<DT, TM, TN, TWO, ALIGNED, GATED, kFull>);
+    if constexpr (!(GATED && TM == 256))
+      if (epi == kBare) fn = reinterpret_cast<const void *>(&mx_epilogue_kernel<DT, TM, TN, TWO, ALIGNED, GATED, kBare>);
+    if constexpr (!GATED)
+      if (epi == kBias) fn = reinterpret_cast<const void *>(&mx_epilogue_kernel<DT, TM, TN, TWO, ALIGNED, GATED, kBias>);
     return hipLaunchKernel(fn, dim3((unsigned)wgs), dim3(kThreads), args, 0, g.stream);
   }
   // The most tiles the groups can have: each one's last may be partial.
@@ -595,9 +645,11 @@ hipError_t launch_mx_tile(const MxGemm &g) {
   if (!grid_ok(wgs)) return hipErrorInvalidConfiguration;
   MxGroups gr{g.offsets, g.rows, (int)g.groups, (int)g.M, (int)g.src_rows, g.stride_b, g.stride_sb, g.N};
   void *args[] = {&a, &t, &gr};
-  const void *fn = reinterpret_cast<const void *>(&mx_grouped_kernel<DT, TM, TN, TWO, ALIGNED, GATED, true>);
-  if constexpr (kBare)
-    if (!fused) fn = reinterpret_cast<const void *>(&mx_grouped_kernel<DT, TM, TN, TWO, ALIGNED, GATED, false>);
+  const void *fn = reinterpret_cast<const void *>(&mx_grouped_kernel<DT, TM, TN, TWO, ALIGNED, GATED, kFull>);
+  if constexpr (!(GATED && TM == 256))
+    if (epi == kBare) fn = reinterpret_cast<const void *>(&mx_grouped_kernel<DT, TM, TN, TWO, ALIGNED, GATED, kBare>);
+  if constexpr (!GATED)
+    if (epi == kBias) fn = reinterpret_cast<const void *>(&mx_grouped_kernel<DT, TM, TN, TWO, ALIGNED, GATED, kBias>);
   return hipLaunchKernel(fn, dim3((unsigned)wgs), dim3(kThreads), args, 0, g.stream);
 }
 

@@ -290,8 +290,9 @@ def quantize_mxfp4(x, rows=True, columns=False, q=None, scales=None, qt=None, sc
     gemm_mxfp4_epilogue take them, one scale per 32 values of a row.  columns:
     (qt (N,P/2), scalest (N,P/32)), the same of x.t(), zeros behind its M
     values up to P, M rounded up to 32: what the products of a backward pass
-    take.  Both, in one read of x: (q, scales, qt, scalest).  A block with an
-    infinity or a NaN becomes NaN.
+    take; the rows of a qt made here are a multiple of 128 bytes apart.  Both, in
+    one read of x: (q, scales, qt, scalest).  A block with an infinity or a NaN
+    becomes NaN.
     """
     return _call("quantize_mxfp4", x, stream, x, rows, columns, q, scales, qt, scalest)
 
