@@ -286,6 +286,8 @@ hipError_t launch_mx_f16(const MxGemm &g, int tm, bool two);
 inline bool mx_scales_aligned(const MxGemm &g) {
   return g.K % 128 == 0 && ((uintptr_t)g.SA | (uintptr_t)g.SB | (uintptr_t)(g.groups ? g.stride_sb : 0)) % 4 == 0;
 }
+hipError_t launch_mx_split(const MxGemm &g);  // the K split's partial sums, before launch_join
+// Splits of K for a dense product (1: none).
 int mx_splits(int64_t M, int64_t N, int64_t K);
 bool mx_tile_supported(const MxGemm &g, int tm, int tn);
 

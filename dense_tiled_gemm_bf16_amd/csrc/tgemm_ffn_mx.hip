@@ -18,7 +18,24 @@ bool mx_tile_supported(const MxGemm &g, int tm, int tn) {
   return tm == tn && (tm == 16 || tm == 64 || tm == 128 || (tm == 256 && big_tile(g)));
 }
 
-int mx_splits(int64_t, int64_t, int64_t) { return 1; }
+// K is split where 64 x 64 tiles leave at least half the compute units idle and
+// K is so deep that each is spared nine slices of 512 or more (0.45 us each): as
+// many splits as fill the units once.  The second launch and the sums on their
+// way cost about 4 us.  us, unsplit -> split, rows read from memory:
+//   M    N     K                          M    N     K
+//   48   8192  28672  29.3 -> 23.9 (2)    48   8192  8192   11.2 -> 11.3 (2)
+//   48   4096  14336  15.9 -> 11.6 (4)    512  1024  8192   11.2 -> 11.8 (2)
+//   64   1024  8192   10.9 -> 8.7 (4)     64   1024  4096    7.3 -> 7.9 (2)
+//   100  256   8192   11.0 -> 8.7 (4)     200  2048  4096    7.6 -> 9.7 (2)
+// (256 compute units: the workspace's size is asked for where there may be no
+// device.  Up to 16 rows the kernel for few rows splits K among its waves.)
+int mx_splits(int64_t M, int64_t N, int64_t K) {
+  const int64_t tiles = ((M + 63) / 64) * ((N + 63) / 64), slices = (K + 511) / 512;
+  if (M <= 16 || tiles == 0 || tiles * 2 > 256 || slices < 8) return 1;
+  const int64_t n = std::min<int64_t>({256 / tiles, slices / 4, 16});
+  const int64_t each = (slices + n - 1) / n;
+  return slices - each >= 9 ? (int)((slices + each - 1) / each) : 1;
+}
 
 namespace {
 
@@ -85,6 +102,26 @@ bool few_rows(const MxGemm &g) {
 }  // namespace
 
 hipError_t launch_mx(const MxGemm &g) {
+  if (g.splits > 1) {
+    const hipError_t e = launch_mx_split(g);
+    if (e != hipSuccess) return e;
+    Gemm j{};
+    j.dtype = g.dtype;
+    j.M = g.M;
+    j.N = g.N;
+    j.bias = g.bias;
+    j.residual = g.residual;
+    j.ldr = g.ldr;
+    j.preact = g.preact;
+    j.ldp = g.ldp;
+    j.C = g.C;
+    j.ldc = g.ldc;
+    j.act = g.act;
+    j.ws = g.ws;
+    j.splits = g.splits;
+    j.stream = g.stream;
+    return launch_join(j);
+  }
   int tm = g.tile_m;
   if (tm == 0) tm = few_rows(g) ? 16 : pick(g);
   if (tm == 16) return launch_mx_rows(g);

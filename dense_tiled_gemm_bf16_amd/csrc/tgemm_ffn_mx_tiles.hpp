@@ -76,6 +76,7 @@ struct MxTile {
   const Args &a;
   MxSlots slots;
   EXT x;
+  int kbv;  // scales of a row from the first slice on (rows are a.kb apart)
   int lane, wave, wave_m, wave_n, m0, n0;
   __amdgpu_buffer_rsrc_t ra, rb, rsa, rsb;
   uint32_t offa[kLA], offb[kLB];
@@ -85,7 +86,7 @@ struct MxTile {
   uint32_t frag;           // this lane's chunk of product 0
   f32x4 acc[kNBn][kNBm];
 
-  __device__ __forceinline__ MxTile(const Args &args, const MxSlots &s, const EXT &ext) : a(args), slots(s), x(ext) {}
+  __device__ __forceinline__ MxTile(const Args &args, const MxSlots &s, const EXT &ext) : a(args), slots(s), x(ext), kbv(args.kb) {}
 
   // Banks repeat every 256 bytes, one row or two.  LDS serves a read of 16
   // bytes a lane in groups of 16 lanes; whether those are 16 rows of one lane
@@ -136,8 +137,8 @@ struct MxTile {
     const uintptr_t pa = (uintptr_t)(a.SA + (gather ? (size_t)0 : (size_t)m0 * a.kb));
     const uintptr_t pb = (uintptr_t)(a.SB + (size_t)n0 * a.kb);
     const uint32_t mis_a = (uint32_t)(pa & 3), mis_b = (uint32_t)(pb & 3);
-    rsa = make_rsrc((const void *)(pa - mis_a), src > 0 ? (mis_a + (uint32_t)src * (uint32_t)a.kb + 3u) & ~3u : 0u);
-    rsb = make_rsrc((const void *)(pb - mis_b), (mis_b + (uint32_t)brows * (uint32_t)a.kb + 3u) & ~3u);
+    rsa = make_rsrc((const void *)(pa - mis_a), src > 0 ? (mis_a + (uint32_t)(src - 1) * (uint32_t)a.kb + (uint32_t)kbv + 3u) & ~3u : 0u);
+    rsb = make_rsrc((const void *)(pb - mis_b), (mis_b + (uint32_t)(brows - 1) * (uint32_t)a.kb + (uint32_t)kbv + 3u) & ~3u);
 
     const int r = lane & 15, g = lane >> 4;
     // Rows: lane l of instruction i writes chunk l % kCh of row kIR i + l / kCh
@@ -275,7 +276,7 @@ struct MxTile {
   // The bytes of a lane's scales that are the row's: those behind its last are
   // the next row's, and a NaN among them would meet the zeros past K.
   __device__ __forceinline__ uint32_t keep_of(int kt) const {
-    const int left = a.kb - kP * (4 * kt + (lane >> 4));
+    const int left = kbv - kP * (4 * kt + (lane >> 4));
     auto low = [](int n, int most) { return n >= most ? ~0u >> (32 - 8 * most) : n <= 0 ? 0u : ~0u >> (32 - 8 * n); };
     if constexpr (kPairs == 1) return low(left, 4);
     return low(left, 2) | low(left - 8, 2) << 16;
@@ -566,6 +567,46 @@ void mx_epilogue_kernel(const Args a, const Tail t) {
 #endif
 }
 
+// The K split: workgroup w computes tile w % tiles over its range of slices and
+// leaves its sums in plane w / tiles of the workspace.
+struct MxSplitExt {
+  static constexpr bool kOn = true, kGated = false, kGather = false, kPrefetch = false;
+  int m0, n0, split;
+  template <class K>
+  __device__ __forceinline__ void store(K &k) const {
+    float *plane = k.a.ws + (size_t)split * (size_t)k.a.M * (size_t)k.a.N;
+#pragma unroll
+    for (int j = 0; j < K::kNBm; ++j) {
+      const int m = m0 + k.wave_m * K::kWM + j * 16 + (k.lane & 15);
+#pragma unroll
+      for (int i = 0; i < K::kNBn; ++i) {
+        const int n = n0 + k.wave_n * K::kWN + 16 * i + 4 * (k.lane >> 4);
+        if (m < k.a.M && n < k.a.N) store_c((uint8_t *)(plane + (size_t)m * k.a.N + n), __builtin_bit_cast(u32x4, k.acc[i][j]));
+      }
+    }
+  }
+};
+
+template <bool ALIGNED>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void mx_split_kernel(const Args a0) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const int tiles = a0.tiles_m * a0.tiles_n, split = (int)blockIdx.x / tiles, t = (int)blockIdx.x - split * tiles;
+  const int s0 = split * a0.kq;
+  Args a = a0;
+  a.A += (size_t)s0 * 256;
+  a.B += (size_t)s0 * 256;
+  a.SA += (size_t)s0 * 16;
+  a.SB += (size_t)s0 * 16;
+  a.K = min(a0.K - s0 * 256, a0.kq * 256);
+  using K = MxTile<0, 64, 64, false, ALIGNED, MxSplitExt>;
+  TGEMM_MX_SLOTS(64, 64, K::SL, K::kNS, K::kScaleBytes)
+  K k(a, slots, MxSplitExt{t % a0.tiles_m * 64, t / a0.tiles_m * 64, split});
+  k.kbv = a0.kb - s0 * 16;
+  k.run();
+#endif
+}
+
 struct MxGroups {
   const int32_t *offsets;
   const int32_t *rows;  // or nullptr
@@ -605,8 +646,7 @@ void mx_grouped_kernel(const Args a0, const Tail t0, const MxGroups g) {
 #endif
 }
 
-template <int DT, int TM, int TN, bool TWO, bool ALIGNED, bool GATED>
-hipError_t launch_mx_tile(const MxGemm &g) {
+inline Args mx_args(const MxGemm &g) {
   Args a{};
   a.A = static_cast<const uint8_t *>(g.A);
   a.B = static_cast<const uint8_t *>(g.B);
@@ -614,14 +654,37 @@ hipError_t launch_mx_tile(const MxGemm &g) {
   a.SB = static_cast<const uint8_t *>(g.SB);
   a.C = static_cast<uint8_t *>(g.C);
   a.M = (int)g.M;
-  a.N = (int)(GATED ? g.N / 2 : g.N);
-  a.K = (int)(g.K / 2);  // bytes
+  a.N = (int)(is_gated(g.act) ? g.N / 2 : g.N);  // output columns
+  a.K = (int)(g.K / 2);                          // bytes
   a.lda = (int)g.lda;
   a.ldb = (int)g.ldb;
   a.ldc = (int)g.ldc;
   a.kb = (int)(g.K / 32);
   a.ksteps = (int)(g.K / 256);  // (256-row tiles)
   a.splits = 1;
+  return a;
+}
+
+inline hipError_t launch_mx_split_tiles(const MxGemm &g) {
+  Args a = mx_args(g);
+  a.N = (int)g.N;  // the product's columns, gated or not
+  a.tiles_m = (int)((g.M + 63) / 64);
+  a.tiles_n = (int)((g.N + 63) / 64);
+  a.ws = g.ws;
+  const int slices = (a.K + 255) / 256;
+  a.kq = (slices + g.splits - 1) / g.splits;  // (mx_splits leaves no split empty)
+  a.splits = g.splits;
+  const int64_t wgs = (int64_t)a.tiles_m * a.tiles_n * a.splits;
+  if (!grid_ok(wgs)) return hipErrorInvalidConfiguration;
+  void *args[] = {&a};
+  const void *fn = mx_scales_aligned(g) ? reinterpret_cast<const void *>(&mx_split_kernel<true>)
+                                        : reinterpret_cast<const void *>(&mx_split_kernel<false>);
+  return hipLaunchKernel(fn, dim3((unsigned)wgs), dim3(kThreads), args, 0, g.stream);
+}
+
+template <int DT, int TM, int TN, bool TWO, bool ALIGNED, bool GATED>
+hipError_t launch_mx_tile(const MxGemm &g) {
+  Args a = mx_args(g);
   constexpr int kCols = GATED ? TN / 2 : TN;
   a.tiles_m = (int)((g.M + TM - 1) / TM);
   a.tiles_n = (a.N + kCols - 1) / kCols;

@@ -2,6 +2,9 @@
 refused with the documented status before any device is touched.  No test here
 launches a kernel."""
 import math
+import os
+import re
+import subprocess
 
 import pytest
 import torch
@@ -133,6 +136,53 @@ def grp(**kw):
 ])
 def test_mx_grouped_refuses(fields, code, word):
     refused("gemm_mxfp4_grouped", code, word, **fields)
+
+
+def deep(**kw):
+    """A call whose K is split."""
+    return mx(M=64, K=8192, lda=4096, ldb=4096, workspace_bytes=1 << 22, **kw)
+
+
+@pytest.mark.parametrize("fields,code,word", [
+    (deep(workspace=P[8] + 4), tg.EALIGN, "workspace"), (deep(workspace=P[0] + 4096), tg.EINVAL, "workspace overlaps A"),
+    (deep(workspace=P[3]), tg.EINVAL, "workspace overlaps scale_B"), (deep(workspace=P[4]), tg.EINVAL, "C overlaps workspace"),
+])
+def test_mx_split_refuses(fields, code, word):
+    refused("gemm_mxfp4_epilogue", code, word, **fields)
+
+
+def test_workspace_sizes():
+    mxw, norm_w = ffn.lib().tgemm_mxfp4_workspace_bytes, ffn.lib().tgemm_layer_norm_backward_workspace_bytes
+    assert mxw(64, 32, 8192) == 4 * 64 * 32 * 4
+    assert mxw(48, 8192, 28672) == 2 * 48 * 8192 * 4
+    assert mxw(16, 32, 8192) == 0                    # few rows split K by themselves
+    assert mxw(64, 32, 4096) == 0                    # not deep enough
+    assert mxw(1024, 1024, 1 << 20) == 0             # enough tiles without
+    assert mxw(0, 32, 8192) == mxw(64, -8, 8192) == mxw(64, 1 << 31, 8192) == mxw(64, 32, 1 << 31) == 0
+    assert norm_w(1, 4096) == 2 * 4096 * 4
+    assert norm_w(8192, 4096) == 256 * 2 * 4096 * 4
+    assert norm_w(128, 16384) == (256 + 2 * 2 * 16384) * 4      # two steps: a pair a row, a pair of sums a 64 rows
+    assert norm_w(0, 64) == norm_w(-1, 64) == norm_w(64, 0) == norm_w(1 << 31, 64) == 0
+
+
+def test_the_kernels_keep_their_accumulators_in_registers(tmp_path):
+    """No kernel of these operators uses scratch memory."""
+    tools = "/opt/rocm/lib/llvm/bin"
+    if not os.path.exists(os.path.join(tools, "llvm-readelf")):
+        pytest.skip("no LLVM tools")
+    so = tmp_path / "lib.so"
+    so.write_bytes(open(ffn.LIB_PATH, "rb").read())
+    subprocess.run([os.path.join(tools, "llvm-objdump"), "--offloading", str(so)], capture_output=True, check=True,
+                   cwd=tmp_path)
+    seen = 0
+    for f in tmp_path.glob("lib.so.*gfx950*"):
+        notes = subprocess.run([os.path.join(tools, "llvm-readelf"), "--notes", str(f)], capture_output=True, text=True,
+                               check=True).stdout
+        for name, size in re.findall(r"\.name:\s+(\S+).*?\.private_segment_fixed_size:\s+(\d+)", notes, re.S):
+            if re.search(r"(mx_\w+|norm\w*|quant\w*)_kernel", name):
+                seen += 1
+                assert int(size) == 0, name
+    assert seen > 100
 
 
 def test_nothing_to_do_needs_no_device():

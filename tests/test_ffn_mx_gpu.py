@@ -201,6 +201,10 @@ def run_epilogue(M, N, K, dtype=BF16, act="none", bias=True, residual=True, prea
     torch.cuda.synchronize()
     yr, ty, zr, tz = more.product(a, sa, b, sb, bs, act, rs, dtype)
     assert y.dtype == dtype
+    if dtype == F16:
+        # Half a step past the largest binary16 (65520 and on) rounds to infinity.
+        over = torch.isinf(y.cpu()) & (yr.abs() + ty >= 65520) & (y.cpu().sign() == yr.sign())
+        y = torch.where(over, yr, y.cpu().double())
     ref.assert_near(y, yr, ty, "out")
     if preact:
         ref.assert_near(z, zr, tz, "preact")
@@ -243,6 +247,57 @@ def test_activations(act, size, tile):
 def test_every_tail_of_k(K, size, tile):
     tile(size, K)
     run_epilogue(70, 72, K, BF16, "none", residual=False, preact=False, seed=K)
+
+
+@pytest.mark.parametrize("M,N,K,act", [(17, 72, 8192, "gelu"), (100, 256, 8224, "silu"), (300, 136, 9312, "relu"),
+                                       (64, 1024, 16384, "none"), (130, 272, 8288, "swiglu"), (40, 1040, 7200, "geglu")])
+def test_split_k(M, N, K, act):
+    assert ffn.lib().tgemm_mxfp4_workspace_bytes(M, N, K) > 0
+    run_epilogue(M, N, K, BF16, act, seed=M)
+    run_epilogue(M, N, K, F16, act, bias=False, residual=False, preact=False, seed=M + 9)
+
+
+def test_split_k_workspaces():
+    """The sums stay within the bytes asked for; with a byte less K is not
+    split; a replayed graph has the same bits."""
+    M, N, K = 100, 256, 8224
+    a, sa = (t.cuda() for t in rand_mx(0, M, K))
+    b, sb = (t.cuda() for t in rand_mx(1, N, K))
+    need = ffn.lib().tgemm_mxfp4_workspace_bytes(M, N, K)
+    guard = torch.full((need + 256,), 165, dtype=torch.uint8, device="cuda")
+    want = tg.gemm_mxfp4_epilogue(a, b, sa, sb, act="silu", workspace=guard[:need])
+    assert (guard[need:] == 165).all() and (guard[:need] != 165).any()
+    guard.fill_(165)
+    less = tg.gemm_mxfp4_epilogue(a, b, sa, sb, act="silu", workspace=guard[:need - 16])
+    assert (guard == 165).all()
+    _, tol, _, _ = more.product(a.cpu(), sa.cpu(), b.cpu(), sb.cpu(), None, "silu", None, BF16)
+    ref.assert_near(less, want.cpu().double(), 2 * tol)
+    assert torch.equal(tg.gemm_mxfp4_epilogue(a, b, sa, sb, act="silu"), want)
+    out = torch.empty_like(want)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        tg.gemm_mxfp4_epilogue(a, b, sa, sb, act="silu", out=out, workspace=guard[:need])
+    for _ in range(3):
+        out.zero_()
+        guard.fill_(7)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
+def test_split_k_nan_scales():
+    M, N, K = 70, 72, 8288
+    a, sa = rand_mx(1, M, K)
+    b, sb = rand_mx(2, N, K)
+    clean = tg.gemm_mxfp4_epilogue(a.cuda(), b.cuda(), sa.cuda(), sb.cuda())
+    sa[1, 0], sa[33, -1], sb[5, 0], sb[64, -1] = 255, 255, 255, 255
+    got = tg.gemm_mxfp4_epilogue(a.cuda(), b.cuda(), sa.cuda(), sb.cuda())
+    hit = torch.zeros(M, N, dtype=torch.bool)
+    hit[[1, 33]] = True
+    hit[:, [5, 64]] = True
+    assert torch.isnan(got.cpu()[hit]).all() and torch.equal(got.cpu()[~hit], clean.cpu()[~hit])
 
 
 @pytest.mark.parametrize("size", TILES)
@@ -514,6 +569,61 @@ def test_same_bits_in_graphs_and_on_streams():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, step())
+
+
+def test_chosen_kernels():
+    """Sizes that take each kernel by the library's own choice: few rows, one and
+    two 64 x 64 tiles a CU, 128 x 128, 256 x 256."""
+    for M, N, K, act in [(16, 4096, 512, "silu"), (64, 4096, 1088, "gelu"), (600, 3000, 320, "none"), (1030, 2056, 288, "relu"),
+                         (4100, 4104, 256, "none"), (1500, 4112, 96, "swiglu")]:
+        run_epilogue(M, N, K, BF16, act, seed=M)
+        run_epilogue(M, N, K, F16, act, bias=True, residual=False, preact=False, seed=M)
+
+
+def test_calls_from_threads_at_once():
+    import threading
+
+    M, N, K = 200, 264, 1056
+    a, sa = (t.cuda() for t in rand_mx(0, M, K))
+    b, sb = (t.cuda() for t in rand_mx(1, N, K))
+    x = rand(2, M, 512).cuda()
+    want, q = tg.gemm_mxfp4_epilogue(a, b, sa, sb, act="silu"), tg.quantize_mxfp4(x, columns=True)
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                y, p = tg.gemm_mxfp4_epilogue(a, b, sa, sb, act="silu"), tg.quantize_mxfp4(x, columns=True)
+                s.synchronize()
+                if not torch.equal(y, want) or not all(torch.equal(i, j) for i, j in zip(p, q)):
+                    bad.append(1)
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
+def test_a_padded_batch():
+    """Rows behind the last group (ids -1 in the routing) have no part in anything."""
+    T, E, k, D, H = 40, 5, 2, 64, 96
+    x = rand(0, T, D)
+    ids = torch.randint(0, E, (T, k), generator=torch.Generator().manual_seed(1), dtype=torch.int32)
+    ids[30:] = -1
+    w = rand(2, E, H, D, scale=0.1)
+    b, sb = (t.view(E, H, -1) for t in tg.quantize_mxfp4(w.cuda().view(-1, D)))
+    off, rows, slots = tg.route_plan(ids.cuda(), E)
+    a, sa = tg.quantize_mxfp4(x.cuda())
+    out = torch.full((T * k, H), 9.0, dtype=BF16, device="cuda")
+    tg.gemm_mxfp4_grouped(a, b, sa, sb, off, rows=rows, out=out)
+    n = int(off[-1])
+    assert n == 60 and (out[n:] == 9).all() and (out[:n] != 9).any()
+    y = tg.expert_combine(out, slots)
+    assert (y[30:] == 0).all()
 
 
 def test_types_follow_what_is_given():
