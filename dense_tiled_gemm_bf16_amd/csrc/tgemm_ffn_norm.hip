@@ -154,21 +154,21 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_kernel(const NormArgs 
   } else {
     float v[8], s = 0.0f, d = 0.0f;
     Eight<DT> e;
-    for (int n = t * 8; n < a.N; n += T * 8) {
+    for (uint32_t n = t * 8; n < (uint32_t)a.N; n += T * 8) {  // (the step past the end may pass 2^31)
       e.load(x + (size_t)n * kB);
       e.get(v);
 #pragma unroll
       for (int q = 0; q < 8; ++q) s += v[q];
     }
     mu = total(s, 0) * a.inv_n;
-    for (int n = t * 8; n < a.N; n += T * 8) {
+    for (uint32_t n = t * 8; n < (uint32_t)a.N; n += T * 8) {
       e.load(x + (size_t)n * kB);
       e.get(v);
 #pragma unroll
       for (int q = 0; q < 8; ++q) d += (v[q] - mu) * (v[q] - mu);
     }
     rs = 1.0f / sqrtf(total(d, 1) * a.inv_n + a.eps);
-    for (int n = t * 8; n < a.N; n += T * 8) {
+    for (uint32_t n = t * 8; n < (uint32_t)a.N; n += T * 8) {
       e.load(x + (size_t)n * kB);
       e.get(v);
       put(n, v, mu, rs);
