@@ -69,7 +69,7 @@ def build_binding(verbose: bool = False) -> str:
     for path in includes:
         cmd += ["-isystem", path]
     cmd += [BINDING_SOURCE, "-o", BINDING + ".tmp", "-L" + PKG, "-l:libtgemm_ffn.so", "-L" + torch_lib, "-lc10",
-            "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+            "-lc10_hip", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
     _run(cmd, verbose)
     os.replace(BINDING + ".tmp", BINDING)
     return BINDING

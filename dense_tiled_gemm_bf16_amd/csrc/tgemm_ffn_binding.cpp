@@ -11,6 +11,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -112,8 +113,10 @@ struct On {
   On(const On &) = delete;
 
   hipStream_t stream() const { return c10::hip::getCurrentHIPStream(device.index()).stream(); }
+  // (at::empty, past its dispatch; that fills new memory if torch is asked to be deterministic.)
   Tensor empty(at::IntArrayRef shape, ScalarType t) const {
-    return at::empty(shape, at::TensorOptions().dtype(t).device(device));
+    if (at::globalContext().deterministicAlgorithms()) return at::empty(shape, at::TensorOptions().dtype(t).device(device));
+    return Tensor(at::detail::empty_cuda(shape, t, device, std::nullopt));
   }
   const Tensor &same(const Tensor &t, const char *name) const {
     if (t.device() != device)

@@ -297,9 +297,14 @@ def quantize_mxfp4(x, rows=True, columns=False, q=None, scales=None, qt=None, sc
     return _call("quantize_mxfp4", x, stream, x, rows, columns, q, scales, qt, scalest)
 
 
+_dtypes = {}  # (made once: in every call it took as long as an allocation, 0.6 us)
+
+
 def _dtype(dtype):
-    torch = _torch()
-    code = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(dtype)
+    if not _dtypes:
+        torch = _torch()
+        _dtypes.update({None: -1, torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+    code = _dtypes.get(dtype)
     if code is None:
         raise TypeError(f"dtype must be torch.bfloat16, torch.float16 or torch.float32, got {dtype!r}")
     return code
@@ -309,7 +314,7 @@ def dequantize_mxfp4(q, scales, dtype=None, out=None, stream=None):
     """The values of MXFP4 rows q (M,N/2), scales (M,N/32): (M,N) in dtype
     (torch.bfloat16 when None; out's if one is given), which holds each exactly
     unless it is float16."""
-    return _call("dequantize_mxfp4", q, stream, q, scales, -1 if dtype is None else _dtype(dtype), out)
+    return _call("dequantize_mxfp4", q, stream, q, scales, _dtype(dtype), out)
 
 
 def gemm_mxfp4_epilogue(a, b, scale_a, scale_b, bias=None, act="none", residual=None, preact=None, out=None, dtype=None,
@@ -325,7 +330,7 @@ def gemm_mxfp4_epilogue(a, b, scale_a, scale_b, bias=None, act="none", residual=
     there is none); allocated when None.
     """
     return _call("gemm_mxfp4_epilogue", a, stream, a, b, scale_a, scale_b, bias, _act(act), residual, preact, out,
-                 -1 if dtype is None else _dtype(dtype), workspace)
+                 _dtype(dtype), workspace)
 
 
 def gemm_mxfp4_grouped(a, b, scale_a, scale_b, offsets, rows=None, bias=None, act="none", preact=None, out=None, dtype=None,
@@ -339,4 +344,4 @@ def gemm_mxfp4_grouped(a, b, scale_a, scale_b, offsets, rows=None, bias=None, ac
     written.
     """
     return _call("gemm_mxfp4_grouped", a, stream, a, b, scale_a, scale_b, offsets, rows, bias, _act(act), preact, out,
-                 -1 if dtype is None else _dtype(dtype))
+                 _dtype(dtype))
