@@ -44,14 +44,14 @@ namespace {
 // alone; up to one smaller tile a CU take 0.6 of a round.  Measured, us, with the
 // rounding alone | bias, gelu and residual | swiglu alone:
 //   M     N     K      64                   128                 256
-//   256   4096  4096   8.1   9.2   7.6      14.2  17.5  13.6    25.6  39.1  30.0
-//   512   4096  4096   11.7  13.6  11.4     14.3  18.0  13.9    25.6  39.3  30.1
-//   1024  4096  4096   20.4  24.1  20.2     16.8  20.2  15.5    26.8  40.2  31.7
-//   2048  4096  4096   37.6  40.9  36.0     23.2  30.0  22.3    29.0  44.0  35.7
-//   4096  4096  1024   29.7  39.2  29.0     18.1  27.5  14.7    14.4  28.5  19.2
-//   4096  4096  2048   42.8  49.8  41.0     25.8  33.5  22.7    20.6  34.7  25.5
-//   4096  4096  8192   135   137   130      78.6  87.1  79.2    59.5  73.2  64.6
-//   8192  8192  4096   284   328   282      165   211   159     131   188   146
+//   256   4096  4096   7.7   9.0   7.8      12.1  15.7  11.7    25.4  39.0  30.3
+//   512   4096  4096   11.8  13.5  11.7     12.5  16.2  12.1    25.4  39.3  30.4
+//   1024  4096  4096   20.9  24.1  20.7     14.7  18.8  13.8    25.7  39.8  30.6
+//   2048  4096  4096   38.8  42.7  36.8     22.8  28.4  21.8    26.6  41.5  31.5
+//   4096  4096  1024   27.5  39.0  28.0     16.4  26.7  14.2    13.8  28.5  18.8
+//   4096  4096  2048   40.5  49.6  39.4     23.9  33.2  21.9    19.6  33.6  24.7
+//   4096  4096  8192   136   137   129      78.5  86.6  78.4    58.7  72.8  63.8
+//   8192  8192  4096   285   335   275      168   221   160     129   201   142
 struct MxShape {
   int tm, per_round;
   double base, slice, fused, gated;

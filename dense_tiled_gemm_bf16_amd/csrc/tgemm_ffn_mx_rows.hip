@@ -2,7 +2,8 @@
 // for gfx950: single tokens and small batches against 4-bit weights (N x K).
 //
 // What bounds such a product is reading the weight once, 17 bytes per 32
-// elements.  A workgroup takes 16 NB rows of the weight (columns of C) and up
+// elements (16384 x 4096 9.7 us, 3.7 TB/s), and below some megabytes the latency
+// of a launch and one load (4096 x 1024 2.9).  A workgroup takes 16 NB rows of the weight (columns of C) and up
 // to 16 rows of A, and its W waves divide K: wave w takes units of 512 K
 // elements (256 bytes of each row) w, w + W, ...  Rows and scales go from
 // memory straight into the registers of the scaled v_mfma 16x16x128: in
@@ -300,6 +301,15 @@ hipError_t launch_one(const MxGemm &g) {
   return hipLaunchKernel(fn, dim3((unsigned)wgs), dim3(64 * W), args, 0, g.stream);
 }
 
+// NB blocks of weight rows a wave and W waves; one row by N x K from memory, us
+// between launches of a graph:
+//   N      K     NB 1, W 4   W 8    NB 2, W 4   W 8
+//   4096   1024  2.86        2.95   3.33        3.45
+//   4096   2048  3.46        3.55   4.08        4.18
+//   4096   4096  4.72        4.63   6.13        5.83
+//   4096   8192  7.66        6.86   10.8        10.0
+//   8192   4096  6.48        6.54   7.26        6.72
+//   16384  4096  9.80        9.84   10.3        9.67
 template <int DT, int W>
 hipError_t launch_waves(const MxGemm &g) {
   if (is_gated(g.act)) return launch_one<DT, W, 2, true>(g);

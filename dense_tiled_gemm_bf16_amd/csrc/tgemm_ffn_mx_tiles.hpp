@@ -69,9 +69,13 @@ struct MxTile {
   static constexpr int kScaleBytes = kPlane * kPlanes;
   static_assert(kLA % kPer16 == 0 && kLB % kPer16 == 0 && TN % 64 == 0 && TM + TN <= 256, "whole instructions");
   static_assert((kNS - 1) * kLoads < 64, "vmcnt is 6 bits");
-  // Loads of the slices behind the next one that may be on their way when it is
-  // waited for: of two slices (an even and an odd one, if they share scales), or none.
-  static constexpr int kAhead = kNS == 2 ? 0 : 2 * (kLA + kLB) + 2 / kPairs * kPlanes;
+  static_assert(kNS == 4 || (kP == 2 && kPairs == 2), "two slots: two products, scales of two slices");
+  // Loads behind slice kt + 1 that may be on their way when it is waited for in
+  // slice kt, S = kt % 4: of the two slices after it, or with two slots of the one.
+  // (Of two slices one is even; if they share scales, those come with it.)
+  static constexpr int ahead(int S) {
+    return kNS == 2 ? kLA + kLB + (S % 2 == 0 ? kPlanes : 0) : 2 * (kLA + kLB) + 2 / kPairs * kPlanes;
+  }
 
   const Args &a;
   MxSlots slots;
@@ -296,25 +300,37 @@ struct MxTile {
 
   // MFMA Q of product P of slice kt in slot S, its fragments in f.  Between
   // the MFMAs the next product's fragments are read into fn, and the loads of
-  // the slice kNS behind the one that just left its slot go out:
+  // the slice kNS behind the one that just left its slot go out.  Four slots:
   //  * before the last product a wait and a barrier: slice kt + 1 has landed in
   //    every wave, and every wave holds the last fragments of slice kt, so that
-  //    its slot may take slice kt + kNS;
+  //    its slot may take slice kt + 4;
   //  * the last product reads the first fragments and the scales of slice kt + 1
   //    (of the pair that it begins);
   //  * the loads go out over kWindow MFMAs behind the barrier.
+  // Two slots (and two products): a slot is read in as short a time as goes, so
+  // that its next slice is loaded for one and a half slices, not one.
+  //  * The first half of the first product reads the second's fragments; then a
+  //    barrier, and the loads of slice kt + 2 go out over kWindow MFMAs.
+  //  * In the middle of the second product slice kt + 1 is waited for (slice
+  //    kt + 2 is on its way), a barrier, and its first fragments and scales are read.
+  // (Freed and waited for at one place, as with four slots: 1024 x 4096 x 4096 16.4
+  // -> 14.9 us, 32768 gathered rows of 32 experts, 4096 x 2048, 235 -> 227; 32768 x 4096 x
+  // 8192 swiglu 634 -> 640.)  What is left is the loads themselves: without them 392
+  // of 622 us there, without the reads of fragments 576.  Loads over half as many MFMAs: 626.
   // (Left to the compiler, the loads sank to the end of the slice, in front of
-  // the wait for them, and the fragments' reads to their use: 128 x 128 tiles
-  // of 32768 x 4096 x 8192 1123 us.)
-  static constexpr int kWindow = (kP - 1) * kPer;
-  static constexpr int load_pos(int i) { return i * kWindow / kLoads; }  // in MFMAs from the barrier on
+  // the wait for them, and the fragments' reads to their use: 1123 us.)
+  static constexpr int kWindow = kNS == 2 ? kPer : (kP - 1) * kPer;
+  static constexpr int kHalf = kPer / 2;
+  // The MFMA of load i, from the barrier on.
+  static constexpr int load_pos(int i) { return i * kWindow / kLoads; }
   template <int S, int P, int Q, int R>
   __device__ __forceinline__ void read_at(int kt, Frags &fn, Raw &cn) const {
     // (The compiler waits for loads into the scales' slots in front of these
     // reads, whichever slot they read: right behind the barrier, in front of the next loads,
     // it has none or few to wait for.)
-    if constexpr (P == kP - 1 && Q == 0 && (S + 1) % kPairs == 0) read_scale<(S + 1) % 4, R>(cn);
-    if constexpr (R * kPer / kNR == Q) {
+    constexpr int kAt = kNS == 2 && P == kP - 1 ? kHalf : 0;  // the first MFMA with reads
+    if constexpr (P == kP - 1 && Q == kAt && (S + 1) % kPairs == 0) read_scale<(S + 1) % 4, R>(cn);
+    if constexpr (kAt + R * (kNS == 2 ? kHalf : kPer) / kNR == Q) {
       if constexpr (P < kP - 1)
         read_frag<S, P + 1, R>(fn);
       else
@@ -323,7 +339,9 @@ struct MxTile {
   }
   template <int S, int P, int Q, int I>
   __device__ __forceinline__ void load_at(int kt) const {
-    if constexpr (load_pos(I) == (P + 1) % kP * kPer + Q) {
+    if constexpr (kNS == 2) {
+      if constexpr (load_pos(I) + kHalf == P * kPer + Q) load_one<(S + 2) % 4, I>(kt + 2);
+    } else if constexpr (load_pos(I) == (P + 1) % kP * kPer + Q) {
       if constexpr (P == kP - 1)
         load_one<(S + kNS) % 4, I>(kt + kNS);
       else
@@ -340,8 +358,12 @@ struct MxTile {
   }
   template <int S, int P, int Q>
   __device__ __forceinline__ void mfma_one(int kt, const Frags &f, Frags &fn, Raw &c) {
-    if constexpr (P == kP - 1 && Q == 0) {
-      wait_vm_lgkm0<kAhead>();
+    if constexpr (kNS == 2 && P == 0 && Q == kHalf) {
+      wait_vm_lgkm0<63>();  // (the reads alone)
+      barrier();
+    }
+    if constexpr (P == kP - 1 && Q == (kNS == 2 ? kHalf : 0)) {
+      wait_vm_lgkm0<ahead(S)>();
       barrier();
     }
     constexpr bool kNewScales = P == 0 && S % kPairs == 0;
@@ -375,8 +397,9 @@ struct MxTile {
     }
   }
   // Loads of slice kNS - 1 that go out in front of the first barrier (scales
-  // come with every kPairs-th slice).
+  // come with every kPairs-th slice).  Two slots: all of them.
   static constexpr int early() {
+    if (kNS == 2) return kLA + kLB;
     int n = 0;
     for (int i = 0; i < kLoads; ++i) n += load_pos(i) < kPer && (i < kLA + kLB || (kNS - 1) % kPairs == 0);
     return n;
@@ -386,7 +409,7 @@ struct MxTile {
     init();
     const int nk = (a.K + SL - 1) / SL;
     // Slices 0 .. kNS - 2, and of slice kNS - 1 what a slice before the first
-    // would have loaded behind its barrier.
+    // would have loaded behind its barrier (two slots: all; an odd slice brings no scales).
     constexpr auto all = std::make_integer_sequence<int, kLoads>();
     load_some<0>(all, 0);
     if constexpr (kNS == 4) {
@@ -394,7 +417,7 @@ struct MxTile {
       load_some<2>(all, 2);
     }
     load_some<kNS - 1>(std::make_integer_sequence<int, early()>(), kNS - 1);  // (row loads come first)
-    wait_vm_lgkm0<kAhead + early()>();
+    wait_vm_lgkm0<(kNS == 2 ? 0 : ahead(0)) + early()>();
     barrier();
     Frags f0, f1;
     Raw c;

@@ -80,8 +80,19 @@ struct NormArgs {
   float eps, inv_n;
 };
 
-// One row a workgroup of T threads, P pieces of 8 values a thread in
-// registers; P = 0: any length, three reads of the row.
+// One row a workgroup of T threads (or a wave, T = 64, which needs no barrier),
+// P pieces of 8 values a thread in registers; P = 0: any length, three reads of
+// the row, the last two from the caches.  Reading x and writing y once bound it:
+// 8192 x 4096 bf16 29 us from memory (134 MB, 4.6 TB/s), 4093 x 5000 fp16 19;
+// 8 x 4096 2.7, the latency of a load and two sums across the row.
+// T x P, us for 2^25 bf16 values:
+//   N = 512     64 x 1   23.5   256 x 1  50.8
+//   N = 1024    64 x 2   22.3   256 x 1  32.5
+//   N = 2048    256 x 1  23.2   64 x 4   23.2   256 x 2  23.5
+//   N = 4096    256 x 2  22.0   512 x 1  23.6
+//   N = 6144    512 x 2  21.8   256 x 3  22.8
+//   N = 8192    512 x 2  22.4   256 x 4  23.5   512 x 4  22.3
+//   N = 16384   512 x 4  24.2   1024 x 2 24.5   any length 29.4
 template <int DT, int WDT, int T, int P>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_kernel(const NormArgs a) {
   constexpr int kB = bytes_of(DT), kW = bytes_of(WDT), kWaves = T / 64, kRows = T < 256 ? 256 / T : 1;
@@ -199,10 +210,9 @@ hipError_t launch_norm_types(const Norm &g) {
     fn = reinterpret_cast<const void *>(&norm_kernel<DT, WDT, 256, 1>);
   } else if (g.N <= 4096) {
     fn = reinterpret_cast<const void *>(&norm_kernel<DT, WDT, 256, 2>);
-  } else if (g.N <= 6144) {
-    fn = reinterpret_cast<const void *>(&norm_kernel<DT, WDT, 256, 3>);
   } else if (g.N <= 8192) {
-    fn = reinterpret_cast<const void *>(&norm_kernel<DT, WDT, 256, 4>);
+    fn = reinterpret_cast<const void *>(&norm_kernel<DT, WDT, 512, 2>);
+    threads = 512;
   } else if (g.N <= 16384) {
     fn = reinterpret_cast<const void *>(&norm_kernel<DT, WDT, 512, 4>);
     threads = 512;
@@ -221,10 +231,19 @@ hipError_t launch_norm_types(const Norm &g) {
 // Rows of up to 8192 values in one pass (norm_grad_kernel): T threads hold a row
 // of x, dy and the residual in registers between its two sums and dx, and add
 // up dy h and dy of their own columns over all the rows that their workgroup
-// takes.  The workgroups, one a CU (two of 1032 to 2048 values), take sets of rows in turn; the sums of the row groups of a workgroup meet in LDS, those of the
-// workgroups in the workspace, where norm_sum_kernel adds them in order (atomics
-// would add them in another each time).  The next rows are loaded before the
-// sums of the present ones are waited for.
+// takes.  The workgroups, one or two a CU, take sets of rows in turn; the sums of
+// the row groups of a workgroup meet in LDS, those of the workgroups in the
+// workspace, where norm_sum_kernel adds them in order (atomics would add them in
+// another each time).  The next rows are loaded before the sums of the present
+// ones are waited for.  Four arrays of one read or write bound it: 8192 x 4096
+// bf16 with the residual 52 us (268 MB, 5.1 TB/s), its column sums 4.8.
+// T x P, us for 2^25 bf16 values without a residual, the sums with them, for one
+// and two workgroups a CU:
+//   N = 512    64 x 1   44.2 40.2   256 x 1  148  94.7
+//   N = 1024   64 x 2   40.7 45.7   256 x 1  84.2 58.4
+//   N = 2048   256 x 1  50.8 42.4   512 x 1  83.9 56.7   256 x 2  57.9 61.3
+//   N = 4096   256 x 2  46.3 50.7   512 x 1  51.9 45.3
+//   N = 8192   512 x 2  49.6 55.0
 //
 // Longer rows in two steps: norm_rows_kernel, a row a workgroup, leaves
 // mean(g) and mean(g h) in the workspace; norm_columns_kernel takes kRowsWg
@@ -511,7 +530,8 @@ constexpr int64_t kFusedMost = 8192;  // values of a row
 int grad_blocks(int64_t M, int64_t N) {
   if (N > kFusedMost) return (int)((M + kRowsWg - 1) / kRowsWg);
   const int groups = N <= 1024 ? 8 : N <= 4096 ? 2 : 1;  // rows of a workgroup at a time
-  return (int)std::min<int64_t>((M + groups - 1) / groups, N > 1024 && N <= 2048 ? 2 * kGradWgs : kGradWgs);
+  const bool two = N <= 512 || (N > 1024 && N <= 2048);  // (one piece a thread: registers for two a CU)
+  return (int)std::min<int64_t>((M + groups - 1) / groups, two ? 2 * kGradWgs : kGradWgs);
 }
 
 template <int DT, int WDT>
