@@ -84,6 +84,7 @@ struct MxTile {
   int lane, wave, wave_m, wave_n, m0, n0;
   __amdgpu_buffer_rsrc_t ra, rb, rsa, rsb;
   uint32_t offa[kLA], offb[kLB];
+  int at_a[kLA], at_s;     // gathered: the rows of offa and offs
   int kcol[kPer16];        // this lane's byte in a slice row, by instruction % kPer16
   uint32_t offs;           // aligned offset of this lane's row of scales in slice 0
   uint32_t sh_x[2], sh_y[EXT::kGather ? kNBm : 1];  // where this lane's scales start in their dword
@@ -110,32 +111,53 @@ struct MxTile {
     }
   }
   // Row of A (of the array if gathered, else from the tile's first on) that
-  // LDS row r holds, or -1.
-  __device__ __forceinline__ int a_row(int r) const {
-    if (r >= min(a.M - m0, TM)) return -1;
+  // LDS row r holds, or -1.  at: what index(r) read.
+  __device__ __forceinline__ int index(int r) const {
     if constexpr (EXT::kGather)
-      if (x.rows) {
-        const int s = x.rows[m0 + r];
-        return s >= 0 && s < x.src_rows ? s : -1;
-      }
-    return r;
+      if (x.rows) return x.rows[m0 + min(r, a.M - m0 - 1)];
+    return 0;
+  }
+  __device__ __forceinline__ int a_row(int r, int at) const {
+    if constexpr (EXT::kGather)
+      if (x.rows) return r < min(a.M - m0, TM) && at >= 0 && at < x.src_rows ? at : -1;
+    return r < min(a.M - m0, TM) ? r : -1;
   }
 
-  __device__ __forceinline__ void init() {
+  // Up to B's rows.
+  __device__ __forceinline__ void init_b() {
     lane = threadIdx.x & 63;
     wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     wave_m = wave >> 1;
     wave_n = wave & 1;
     m0 = x.m0;
     n0 = x.n0;
+    constexpr int kCh = SL / 16;
+    const int lr = lane / kCh;
+    // (Read ahead: B's loads do not wait for them.)
+#pragma unroll
+    for (int i = 0; i < kLA; ++i) at_a[i] = index(kIR * (wave * kLA + i) + lr);
+    at_s = index(max(64 * wave - TN + lane, 0));
+    const int brows = EXT::kGated ? ext_half() + min(a.N - n0, TN / 2) : min(a.N - n0, TN);
+    rb = make_rsrc(a.B + (size_t)n0 * a.ldb, (uint32_t)(brows - 1) * (uint32_t)a.ldb + (uint32_t)a.K);
+    // Rows: lane l of instruction i writes chunk l % kCh of row kIR i + l / kCh
+    // of the wave's rows, whose number % 16 goes by i % kPer16.
+#pragma unroll
+    for (int p = 0; p < kPer16; ++p) kcol[p] = 16 * ((lane % kCh) ^ perm(kIR * p + lr));
+#pragma unroll
+    for (int i = 0; i < kLB; ++i) {
+      const int row = b_row(kIR * (wave * kLB + i) + lr);
+      offb[i] = row >= 0 ? (uint32_t)row * (uint32_t)a.ldb + (uint32_t)kcol[i % kPer16] : kOOB;
+    }
+  }
+  // The rest.
+  __device__ __forceinline__ void init_a() {
     bool gather = false;
     if constexpr (EXT::kGather) gather = x.rows != nullptr;
     int src = min(a.M - m0, TM);
     if constexpr (EXT::kGather) src = gather ? x.src_rows : src;
-    const int brows = EXT::kGated ? ext_half() + min(a.N - n0, TN / 2) : min(a.N - n0, TN);
     ra = make_rsrc(a.A + (gather ? (size_t)0 : (size_t)m0 * a.lda),
                    src > 0 ? (uint32_t)(src - 1) * (uint32_t)a.lda + (uint32_t)a.K : 0u);
-    rb = make_rsrc(a.B + (size_t)n0 * a.ldb, (uint32_t)(brows - 1) * (uint32_t)a.ldb + (uint32_t)a.K);
+    const int brows = EXT::kGated ? ext_half() + min(a.N - n0, TN / 2) : min(a.N - n0, TN);
     // Scales: based at the dword that holds the first byte, up to the one that
     // holds the last.
     const uintptr_t pa = (uintptr_t)(a.SA + (gather ? (size_t)0 : (size_t)m0 * a.kb));
@@ -145,26 +167,16 @@ struct MxTile {
     rsb = make_rsrc((const void *)(pb - mis_b), (mis_b + (uint32_t)(brows - 1) * (uint32_t)a.kb + (uint32_t)kbv + 3u) & ~3u);
 
     const int r = lane & 15, g = lane >> 4;
-    // Rows: lane l of instruction i writes chunk l % kCh of row kIR i + l / kCh
-    // of the wave's rows, whose number % 16 goes by i % kPer16.
-    constexpr int kCh = SL / 16;
-    const int lr = lane / kCh;
-#pragma unroll
-    for (int p = 0; p < kPer16; ++p) kcol[p] = 16 * ((lane % kCh) ^ perm(kIR * p + lr));
+    const int lr = lane / (SL / 16);
 #pragma unroll
     for (int i = 0; i < kLA; ++i) {
-      const int row = a_row(kIR * (wave * kLA + i) + lr);
+      const int row = a_row(kIR * (wave * kLA + i) + lr, at_a[i]);
       offa[i] = row >= 0 ? (uint32_t)row * (uint32_t)a.lda + (uint32_t)kcol[i % kPer16] : kOOB;
-    }
-#pragma unroll
-    for (int i = 0; i < kLB; ++i) {
-      const int row = b_row(kIR * (wave * kLB + i) + lr);
-      offb[i] = row >= 0 ? (uint32_t)row * (uint32_t)a.ldb + (uint32_t)kcol[i % kPer16] : kOOB;
     }
     // Scales: lane l of wave w takes row 64 w + l of B's and A's together.
     {
       const bool isb = wave < TN / 64;
-      const int row = isb ? b_row(64 * wave + lane) : a_row(64 * wave - TN + lane);
+      const int row = isb ? b_row(64 * wave + lane) : a_row(64 * wave - TN + lane, at_s);
       offs = row >= 0 ? ((isb ? mis_b : mis_a) + (uint32_t)row * (uint32_t)a.kb) & ~3u : kOOB;
     }
     if constexpr (!ALIGNED) {
@@ -174,7 +186,10 @@ struct MxTile {
       if constexpr (EXT::kGather) {
 #pragma unroll
         for (int j = 0; j < kNBm; ++j)
-          sh_y[j] = (mis_a + (uint32_t)max(a_row(wave_m * kWM + 16 * j + r), 0) * (uint32_t)a.kb) & 3u;
+        {
+          const int row = wave_m * kWM + 16 * j + r;
+          sh_y[j] = (mis_a + (uint32_t)max(a_row(row, index(row)), 0) * (uint32_t)a.kb) & 3u;
+        }
       } else {
         sh_y[0] = (mis_a + (uint32_t)r * (uint32_t)a.kb) & 3u;
       }
@@ -209,10 +224,6 @@ struct MxTile {
                                                (LDS_AS void *)(slots.s[S / kPairs] + p * kPlane + wave * 1024), 16,
                                                left > 0 ? offs : kOOB, (uint32_t)(kt / kPairs) * 16u + 4u * (uint32_t)p, 0, 0);
     }
-  }
-  template <int S, int... I>
-  __device__ __forceinline__ void load_some(std::integer_sequence<int, I...>, int kt) const {
-    (load_one<S, I>(kt), ...);
   }
 
   struct Frags {
@@ -405,19 +416,48 @@ struct MxTile {
     return n;
   }
 
+  // Loads I0 .. I0 + N - 1 of slice S, one of the first.
+  template <int S, int I0, int... I>
+  __device__ __forceinline__ void load_from(std::integer_sequence<int, I...>) const {
+    (load_one<S, I0 + I>(S), ...);
+  }
+  template <int S, int I0, int N>
+  __device__ __forceinline__ void load_part() const {
+    load_from<S, I0>(std::make_integer_sequence<int, N>());
+  }
+  template <int S>
+  __device__ __forceinline__ void load_a() const {
+    load_part<S, 0, kLA>();
+    load_part<S, kLA + kLB, kPlanes>();
+  }
+
   __device__ __forceinline__ void run() {
-    init();
+    init_b();
     const int nk = (a.K + SL - 1) / SL;
     // Slices 0 .. kNS - 2, and of slice kNS - 1 what a slice before the first
     // would have loaded behind its barrier (two slots: all; an odd slice brings no scales).
-    constexpr auto all = std::make_integer_sequence<int, kLoads>();
-    load_some<0>(all, 0);
-    if constexpr (kNS == 4) {
-      load_some<1>(all, 1);
-      load_some<2>(all, 2);
+    if constexpr (EXT::kGather) {
+      // B's rows first, which wait for no index.  (With the groups read once, below:
+      // 37 tokens of 64 experts 32.4 -> 31.1 us, 200 tokens 38.7 -> 37.2, 32768 rows of 32
+      // experts 240 -> 232, 4000 rows of 16 experts on 64 x 64 tiles 17.9 -> 16.4.)  Loads
+      // are waited for in their order: with slice 0 for slice 1's too if there are
+      // four slots, as the first step's wait counts on B's loads of slice 2 behind those.
+      load_part<0, kLA, kLB>();
+      load_part<1, kLA, kLB>();
+      if constexpr (kNS == 4) load_part<2, kLA, kLB>();
+      init_a();
+      load_a<0>();
+      load_a<1>();
+      if constexpr (kNS == 4) load_a<2>();
+    } else {
+      init_a();
+      load_part<0, 0, kLoads>();
+      load_part<1, 0, kNS == 2 ? early() : kLoads>();
+      if constexpr (kNS == 4) load_part<2, 0, kLoads>();
     }
-    load_some<kNS - 1>(std::make_integer_sequence<int, early()>(), kNS - 1);  // (row loads come first)
-    wait_vm_lgkm0<(kNS == 2 ? 0 : ahead(0)) + early()>();
+    if constexpr (kNS == 4) load_part<3, 0, early()>();  // (row loads come first)
+    constexpr int kLate = EXT::kGather ? kLA + (kNS == 4 && 2 % kPairs == 0 ? kPlanes : 0) : kNS == 2 ? 0 : ahead(0);
+    wait_vm_lgkm0<kLate + (EXT::kGather && kNS == 2 ? 0 : early())>();
     barrier();
     Frags f0, f1;
     Raw c;
@@ -637,14 +677,32 @@ struct MxGroups {
   int64_t stride_b, stride_sb, stride_bias;  // bytes, bytes, elements
 };
 
+// Unit `order(total)` of all the groups' tiles (none if that is negative).  Up to
+// 64 groups are read once for both, one a lane: every workgroup's loads wait for this.
+template <class F>
+__device__ __forceinline__ Found find_ordered(const MxGroups &g, int size, int times, int lane, F order) {
+  if (g.groups > 64) {
+    const int at = order(total_units(g.offsets, g.groups, g.R, size, times, lane));
+    return at < 0 ? Found{-1, 0, 0, 0, 0} : find_unit(g.offsets, g.groups, g.R, at, size, times, lane);
+  }
+  const Range r = lane_rows(g.offsets, g.groups, g.R, lane);
+  const int n = (r.hi - r.lo + size - 1) / size * times, upto = wave_scan(n);
+  const int at = order(__builtin_amdgcn_readlane(upto, 63));
+  const uint64_t past = at < 0 ? 0 : __ballot(at < upto);
+  if (!past) return {-1, 0, 0, 0, 0};
+  const int l = (int)__builtin_ctzll(past), before = __builtin_amdgcn_readlane(upto - n, l);
+  // (Only offsets that are no offsets can leave the unit outside the group.)
+  if (at < before || l >= g.groups) return {-1, 0, 0, 0, 0};
+  return {l, __builtin_amdgcn_readlane(r.lo, l), __builtin_amdgcn_readlane(r.hi, l), at - before, before};
+}
+
 template <int DT, int TM, int TN, bool TWO, bool ALIGNED, bool GATED, int EPI>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(TWO ? 2 : 1, TWO ? 2 : 1)))
 void mx_grouped_kernel(const Args a0, const Tail t0, const MxGroups g) {
 #if defined(__HIP_DEVICE_COMPILE__)
   const int lane = threadIdx.x & 63;
-  const int wg = (int)blockIdx.x, total = total_units(g.offsets, g.groups, g.R, TM, a0.tiles_n, lane);
-  if (wg >= total) return;
-  const Found f = find_unit(g.offsets, g.groups, g.R, xcd_order(wg, total), TM, a0.tiles_n, lane);
+  const int wg = (int)blockIdx.x;
+  const Found f = find_ordered(g, TM, a0.tiles_n, lane, [&](int total) { return wg < total ? xcd_order(wg, total) : -1; });
   if (f.e < 0) return;
   int tm, tn;
   tile_in_group(f.unit, (f.hi - f.lo + TM - 1) / TM, a0.tiles_n, tm, tn);
