@@ -93,7 +93,7 @@ int pick(const MxGemm &g) {
 //   one row: 4096 x 4096 5.2 and 7.4, 1024 x 8192 5.7 and 8.9, 4096 x 1024 5.3 and
 //   5.7, 8192 x 8192 11.3 and 11.0, 32768 x 4096 15.9 and 13.5; 16 rows of 8192 x
 //   4096 8.3 and 7.7; 64 gated experts of 2048 x 2048, 6 hit 6.7 and 6.5, 55 hit
-//   by 4 rows each 32.5 and 31.9; 55 of 2048 x 1024 16.8 and 18.4.
+//   by 4 rows each 32.5 and 31.1; 55 of 2048 x 1024 16.8 and 18.4.
 bool few_rows(const MxGemm &g) {
   if (g.M > (g.groups ? 10 * g.groups : 16)) return false;
   return g.K <= 1024 || tiles_of(g, 64) < 0.5 * g.cus;

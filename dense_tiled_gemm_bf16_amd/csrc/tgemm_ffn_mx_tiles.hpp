@@ -537,7 +537,7 @@ struct MxTile {
 
 // A bias alone, straight from the accumulators (as the rounding alone): lane l
 // holds row l % 16 and columns 4 (l / 16) .. + 3 of each block.  (4096 x 4096 x 2048
-// through LDS 29 us.)
+// through LDS 29 us, this way 21.)
 template <int DT, bool GROUPED>
 struct BiasExt {
   static constexpr bool kOn = true, kGated = false, kGather = GROUPED, kPrefetch = true;

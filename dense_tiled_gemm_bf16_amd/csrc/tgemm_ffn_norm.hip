@@ -90,7 +90,8 @@ struct NormArgs {
 //   N = 1024    64 x 2   22.3   256 x 1  32.5
 //   N = 2048    256 x 1  23.2   64 x 4   23.2   256 x 2  23.5
 //   N = 4096    256 x 2  22.0   512 x 1  23.6
-//   N = 6144    512 x 2  21.8   256 x 3  22.8
+//   N = 5000    256 x 3  23.1   512 x 2  24.6   256 x 4  23.1
+//   N = 6144    256 x 3  23.0   512 x 2  22.8
 //   N = 8192    512 x 2  22.4   256 x 4  23.5   512 x 4  22.3
 //   N = 16384   512 x 4  24.2   1024 x 2 24.5   any length 29.4
 template <int DT, int WDT, int T, int P>
@@ -210,6 +211,8 @@ hipError_t launch_norm_types(const Norm &g) {
     fn = reinterpret_cast<const void *>(&norm_kernel<DT, WDT, 256, 1>);
   } else if (g.N <= 4096) {
     fn = reinterpret_cast<const void *>(&norm_kernel<DT, WDT, 256, 2>);
+  } else if (g.N <= 6144) {
+    fn = reinterpret_cast<const void *>(&norm_kernel<DT, WDT, 256, 3>);
   } else if (g.N <= 8192) {
     fn = reinterpret_cast<const void *>(&norm_kernel<DT, WDT, 512, 2>);
     threads = 512;
