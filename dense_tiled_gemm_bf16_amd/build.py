@@ -24,6 +24,7 @@ FFN_SOURCES = [os.path.join(CSRC, "tgemm_ffn_gemm_bf16.hip"), os.path.join(CSRC,
                os.path.join(CSRC, "tgemm_ffn_rowops.hip"), os.path.join(CSRC, "tgemm_ffn_route.hip"),
                os.path.join(CSRC, "tgemm_ffn_norm.hip"), os.path.join(CSRC, "tgemm_ffn_quant.hip"),
                os.path.join(CSRC, "tgemm_ffn_mx_bf16.hip"), os.path.join(CSRC, "tgemm_ffn_mx_f16.hip"),
+               os.path.join(CSRC, "tgemm_ffn_mx_bf16_64.hip"), os.path.join(CSRC, "tgemm_ffn_mx_f16_64.hip"),
                os.path.join(CSRC, "tgemm_ffn_mx_rows.hip"), os.path.join(CSRC, "tgemm_ffn_mx.hip"),
                os.path.join(CSRC, "tgemm_ffn_abi.cpp")]
 BINDING = os.path.join(PKG, "_ffn_binding.so")
@@ -81,9 +82,10 @@ def build(verbose: bool = False) -> str:
         def obj(src):
             return os.path.join(tmp, os.path.basename(src) + ".o")
 
-        with ThreadPoolExecutor(max_workers=4) as pool:
-            list(pool.map(lambda src: _run([HIPCC, *FLAGS, "-c", src, "-o", obj(src)], verbose),
-                          SOURCES[:1] + FFN_SOURCES + SOURCES[1:]))
+        # The longest first: the tiled MXFP4 products, the dense products.
+        order = sorted(SOURCES[:1] + FFN_SOURCES + SOURCES[1:], key=lambda src: "_mx_" not in src)
+        with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as pool:
+            list(pool.map(lambda src: _run([HIPCC, *FLAGS, "-c", src, "-o", obj(src)], verbose), order))
         for lib, sources in ((LIB, SOURCES), (FFN_LIB, FFN_SOURCES)):
             _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", lib + ".tmp", *map(obj, sources)], verbose)
             os.replace(lib + ".tmp", lib)

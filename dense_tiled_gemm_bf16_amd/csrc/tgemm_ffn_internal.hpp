@@ -280,8 +280,10 @@ struct MxGemm {
 hipError_t launch_mx(const MxGemm &g);        // tgemm_ffn_mx.hip
 hipError_t launch_mx_rows(const MxGemm &g);   // tgemm_ffn_mx_rows.hip: few rows for each weight
 // Tiles of tm x tm (two: 64 x 64 tiles two to a CU): tgemm_ffn_mx_bf16.hip, tgemm_ffn_mx_f16.hip.
-hipError_t launch_mx_bf16(const MxGemm &g, int tm, bool two);
-hipError_t launch_mx_f16(const MxGemm &g, int tm, bool two);
+template <int DT>
+hipError_t launch_mx_64(const MxGemm &g, bool two);
+template <int DT>
+hipError_t launch_mx_large(const MxGemm &g, int tm);  // 128 or 256
 // Whether every row's scales start on a dword.
 inline bool mx_scales_aligned(const MxGemm &g) {
   return g.K % 128 == 0 && ((uintptr_t)g.SA | (uintptr_t)g.SB | (uintptr_t)(g.groups ? g.stride_sb : 0)) % 4 == 0;

@@ -127,7 +127,8 @@ hipError_t launch_mx(const MxGemm &g) {
   if (tm == 16) return launch_mx_rows(g);
   // 64 x 64 tiles: one a CU with a deep ring while they are that few, else two.
   const bool two = tm == 64 && tiles_of(g, 64) > (double)g.cus;
-  return g.dtype == 1 ? launch_mx_f16(g, tm, two) : launch_mx_bf16(g, tm, two);
+  if (tm == 64) return g.dtype == 1 ? launch_mx_64<1>(g, two) : launch_mx_64<0>(g, two);
+  return g.dtype == 1 ? launch_mx_large<1>(g, tm) : launch_mx_large<0>(g, tm);
 }
 
 }  // namespace ffn

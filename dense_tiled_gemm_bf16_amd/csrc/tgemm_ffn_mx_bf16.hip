@@ -1,13 +1,14 @@
-// The tiled products of MXFP4 operands with bfloat16 outputs, and the
-// K split of either (tgemm_ffn_mx_tiles.hpp).
+// The products of MXFP4 operands with bfloat16 outputs on tiles of 128 and 256 rows
+// (tgemm_ffn_mx_tiles.hpp).
 #include "tgemm_ffn_mx_tiles.hpp"
 
 namespace tgemm {
 namespace ffn {
 
-hipError_t launch_mx_bf16(const MxGemm &g, int tm, bool two) { return launch_mx_tiles_dt<0>(g, tm, two); }
-
-hipError_t launch_mx_split(const MxGemm &g) { return launch_mx_split_tiles(g); }
+template <>
+hipError_t launch_mx_large<0>(const MxGemm &g, int tm) {
+  return tm == 256 ? launch_mx_gated<0, 256, 256, false, true>(g) : launch_mx_aligned<0, 128, 128, true>(g);
+}
 
 }  // namespace ffn
 }  // namespace tgemm

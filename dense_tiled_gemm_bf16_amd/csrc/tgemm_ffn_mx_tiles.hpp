@@ -807,13 +807,6 @@ hipError_t launch_mx_aligned(const MxGemm &g) {
   return mx_scales_aligned(g) ? launch_mx_gated<DT, TM, TN, TWO, true>(g) : launch_mx_gated<DT, TM, TN, TWO, false>(g);
 }
 
-template <int DT>
-hipError_t launch_mx_tiles_dt(const MxGemm &g, int tm, bool two) {
-  if (tm == 256) return launch_mx_gated<DT, 256, 256, false, true>(g);
-  if (tm == 128) return launch_mx_aligned<DT, 128, 128, true>(g);
-  return two ? launch_mx_aligned<DT, 64, 64, true>(g) : launch_mx_aligned<DT, 64, 64, false>(g);
-}
-
 }  // namespace
 }  // namespace ffn
 }  // namespace tgemm

@@ -17,8 +17,8 @@
  *
  * Arguments come in structs of 8-byte fields; a field that does not apply is
  * 0 or NULL.  Element types: TGEMM_DT_BF16, TGEMM_DT_F16 and, for logits, norms
- * and quantisation, TGEMM_DT_F32.  Sums are held in 32 bits; each output is rounded once, to
- * nearest even.  16-bit tensors are 16-byte aligned with row strides and
+ * and quantisation, TGEMM_DT_F32.  Sums are held in 32 bits; each output is
+ * rounded once, to nearest even.  16-bit tensors are 16-byte aligned with row strides and
  * contiguous dimensions that are multiples of 8 (TGEMM_EALIGN otherwise).
  * An output may overlap no other argument, except where said.  Sizes (and T k)
  * are below 2^31 - 4096, row strides below 2^31, row groups at most 65536
@@ -414,6 +414,8 @@ TGEMM_API int dequantize_mxfp4(const tgemm_dequantize_mxfp4_args *args, hipStrea
  * preact of type dtype (BF16 or F16).  K % 32 == 0.
  * workspace: for a K split, tgemm_mxfp4_workspace_bytes(M, N, K) bytes,
  * 16-byte aligned; with less, or NULL, there is none.
+ * tgemm_ffn_set_tile: 256 x 256 (K % 256 == 0, scales on dwords), 128 x 128, 64 x 64
+ * or 16 x 16 here and in gemm_mxfp4_grouped; TGEMM_EINVAL otherwise.
  * Limits: 256 lda < 2^31 and 256 ldb < 2^31; gated, (N / 2 + 256) ldb < 2^31.
  */
 typedef struct {

@@ -485,6 +485,26 @@ def test_grouped_weights_apart():
     assert torch.equal(tg.gemm_mxfp4_grouped(a, bb[:, :N, :K // 2], sa, ss[:, :N], off), want)
 
 
+@pytest.mark.parametrize("size", TILES)
+def test_grouped_one_weight_for_all(size, tile):
+    """One weight for every group (strides of 0), and every row gathered from the same
+    token.  Products are multiples of 2^-6 of at most 48 x 12: sums of 256 fit 24 bits,
+    and every kernel gives the same."""
+    E, N, K, R = 70, 48, 256, 300
+    a, sa = (t.cuda() for t in rand_mx(0, 3, K))
+    b, sb = (t.cuda() for t in rand_mx(1, N, K, spread=1))
+    tile(size, K)
+    want = tg.gemm_mxfp4_epilogue(a, b, sa, sb, act="relu")
+    off = torch.linspace(0, R, E + 1).int().cuda()
+    for e in (E, 7):                        # (more groups than a wave has lanes, and fewer)
+        ends = off[:e + 1].clone()
+        rows = torch.full((R,), 2, dtype=torch.int32, device="cuda")
+        out = torch.full((R, N), 9.0, dtype=BF16, device="cuda")
+        tg.gemm_mxfp4_grouped(a, b.expand(e, N, K // 2), sa, sb.expand(e, N, K // 32), ends, rows=rows, act="relu", out=out)
+        n = int(ends[-1])
+        assert torch.equal(out[:n], want[2:3].expand(n, N)) and (out[n:] == 9).all()
+
+
 # --------------------------------------------------------------------------
 # Together
 # --------------------------------------------------------------------------

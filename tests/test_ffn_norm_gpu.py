@@ -213,3 +213,28 @@ def test_same_bits_in_graphs_streams_and_with_given_workspaces():
         again = [tg.layer_norm(x, w, b, mean=m2, rstd=r2)]
         again += list(tg.layer_norm_backward(dy, x, w, m2, r2))
         assert all(torch.equal(p, q) for p, q in zip(outs, again))
+
+
+def test_outputs_are_ordinary_tensors():
+    """New outputs take part in autograd, belong to inference mode inside it, and
+    torch's deterministic mode changes no result."""
+    x, w, b = (t.cuda() for t in (rand(0, 9, 264), rand(1, 264), rand(2, 264)))
+    y = tg.layer_norm(x, w, b)
+    assert not y.requires_grad and not y.is_inference()
+    z = y.clone().requires_grad_()
+    (z * y).sum().backward()
+    assert torch.equal(z.grad, y)
+    y2 = tg.layer_norm(x, w, b).requires_grad_()
+    (y2 * 2).sum().backward()
+    assert (y2.grad == 2).all()
+    with torch.inference_mode():
+        v = tg.layer_norm(x, w, b)
+        assert v.is_inference() and torch.equal(v, y)
+        v.add_(1)
+    before = torch.are_deterministic_algorithms_enabled()
+    torch.use_deterministic_algorithms(True)
+    try:
+        again = tg.layer_norm(x, w, b)
+    finally:
+        torch.use_deterministic_algorithms(before)
+    assert torch.equal(again, y)
