@@ -502,29 +502,35 @@ __global__ __launch_bounds__(256) void norm_columns_kernel(const NormGradArgs a)
   }
 }
 
-// 64 columns of both sums: sixteen waves take the blocks in turn.
+// 64 columns of both sums at a time: sixteen waves take the blocks in turn.  A dispatch
+// holds kSumWgs workgroups of 1024 threads; rows of more than 2^28 values take several turns.
+constexpr int kSumWgs = (1 << 22) - 1;
 template <int WDT>
 __global__ __launch_bounds__(1024) void norm_sum_kernel(const NormGradArgs a) {
   __shared__ float sums[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int p = (int)blockIdx.y, n = (int)blockIdx.x * 64 + lane;
+  const int p = (int)blockIdx.y;
   uint8_t *out = p ? a.db : a.dw;
   if (!out) return;
-  float v = 0.0f;
-  if (n < a.N) {
+  for (int64_t n0 = (int64_t)blockIdx.x * 64; n0 < a.N; n0 += (int64_t)gridDim.x * 64) {
+    const int64_t n = n0 + lane;
+    float v = 0.0f;
+    if (n < a.N) {
 #pragma unroll 4
-    for (int b = wave; b < a.blocks; b += 16) v += a.colsums[((size_t)b * 2 + p) * a.N + n];
-  }
-  sums[wave][lane] = v;
-  __syncthreads();
-  if (wave == 0 && n < a.N) {
-    float t = 0.0f;
+      for (int b = wave; b < a.blocks; b += 16) v += a.colsums[((size_t)b * 2 + p) * a.N + n];
+    }
+    sums[wave][lane] = v;
+    __syncthreads();
+    if (wave == 0 && n < a.N) {
+      float t = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) t += sums[i][lane];
-    if constexpr (WDT == 2)
-      *(float *)(out + (size_t)n * 4) = t;
-    else
-      *(uint16_t *)(out + (size_t)n * 2) = (uint16_t)(pack2<WDT>(t, 0.0f) & 0xffffu);
+      for (int i = 0; i < 16; ++i) t += sums[i][lane];
+      if constexpr (WDT == 2)
+        *(float *)(out + (size_t)n * 4) = t;
+      else
+        *(uint16_t *)(out + (size_t)n * 2) = (uint16_t)(pack2<WDT>(t, 0.0f) & 0xffffu);
+    }
+    __syncthreads();
   }
 }
 
@@ -580,8 +586,8 @@ hipError_t launch_norm_grad_types(const NormGrad &g) {
                           args, 0, g.stream);
   }
   if (e == hipSuccess && (g.dweight || g.dbias))
-    e = hipLaunchKernel(reinterpret_cast<const void *>(&norm_sum_kernel<WDT>), dim3((unsigned)((a.N + 63) / 64), 2),
-                        dim3(1024), args, 0, g.stream);
+    e = hipLaunchKernel(reinterpret_cast<const void *>(&norm_sum_kernel<WDT>),
+                        dim3((unsigned)std::min((a.N + 63) / 64, kSumWgs), 2), dim3(1024), args, 0, g.stream);
   return e;
 }
 

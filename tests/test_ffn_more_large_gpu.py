@@ -90,6 +90,19 @@ def test_norm_of_the_longest_row():
     assert torch.equal(y[0], x)
 
 
+def test_gradients_of_the_widest_rows():
+    """Gradients whose mean, and whose mean against the row, is 0: dx is dy, dweight dy times
+    the row, all exact.  (The longest that the sums' workspace allows: more columns than
+    one dispatch of the last step's workgroups.)"""
+    N = (1 << 30) - 8
+    print("[gpu] gradients 1", N, flush=True)
+    four = lambda *v: torch.tensor(v, dtype=BF16, device="cuda").repeat(N // 4)
+    x, dy = four(1, -1, 1, -1), four(1, 1, -1, -1)
+    one = torch.ones(1, device="cuda")
+    dx, dw, db = tg.layer_norm_backward(dy[None], x[None], None, 0 * one, one)
+    assert torch.equal(dx[0], dy) and torch.equal(db, dy) and torch.equal(dw, four(1, -1, -1, 1))
+
+
 def test_quantize():
     M, N = 524321, 16640
     print("[gpu] quantize", M, N, flush=True)
