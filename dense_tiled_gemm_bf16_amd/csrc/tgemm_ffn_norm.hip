@@ -270,8 +270,10 @@ hipError_t launch_norm_types(const Norm &g) {
 // takes.  The workgroups, one or two a CU, take sets of rows in turn; the sums of
 // the row groups of a workgroup meet in LDS, those of the workgroups in the
 // workspace, where norm_sum_kernel adds them in order (atomics would add them in
-// another each time).  The next rows are loaded before the sums of the present
-// ones are waited for.  Four arrays of one read or write bound it: 8192 x 4096
+// another each time).  A thread's sums go there every kSumTurns turns, so that no
+// running sum gets long: in one over 32768 turns (134 million rows of 8 values)
+// dweight lost 3e-4 of its sum of magnitudes.  The next rows are loaded before the
+// sums of the present ones are waited for.  Four arrays of one read or write bound it: 8192 x 4096
 // bf16 with the residual 52 us (268 MB, 5.1 TB/s), its column sums 4.8.
 // T x P, us for 2^25 bf16 values without a residual, the sums with them, for one
 // and two workgroups a CU:
@@ -289,6 +291,7 @@ hipError_t launch_norm_types(const Norm &g) {
 // ---------------------------------------------------------------------------
 constexpr int kGradWgs = 256;
 constexpr int kRowsWg = 64;
+constexpr int kSumTurns = 512;
 
 struct NormGradArgs {
   const uint8_t *dy, *x, *w, *res;
@@ -339,101 +342,112 @@ __global__ __launch_bounds__(512) void norm_grad_kernel(const NormGradArgs a) {
   Row cur;
   load(cur, first + group);
   int which = 0;
+  bool again = false;
   // (row0 is the workgroup's: every thread takes as many turns.)
-  for (int row0 = first; row0 < a.M; row0 += step, which ^= 1) {
-    const int row = row0 + group;
-    float s0 = 0.0f, s1 = 0.0f;
+  for (int row0 = first; row0 < a.M; again = true) {
+    const int end = (int)min((uint32_t)row0 + (uint32_t)kSumTurns * (uint32_t)step, (uint32_t)a.M);
+    for (; row0 < end; row0 += step, which ^= 1) {
+      const int row = row0 + group;
+      float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      float d[8], x[8], wv[8];
-      cur.x[p].get(x);
-      cur.d[p].get(d);
-      w[p].get(wv);
-      const bool in = (p * T + t) * 8 < a.N;
+      for (int p = 0; p < P; ++p) {
+        float d[8], x[8], wv[8];
+        cur.x[p].get(x);
+        cur.d[p].get(d);
+        w[p].get(wv);
+        const bool in = (p * T + t) * 8 < a.N;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const float h = in ? (x[q] - cur.mu) * cur.rs : 0.0f, g = a.w ? d[q] * wv[q] : d[q];
-        s0 += g;
-        s1 += g * h;
-        sw[p][q] += d[q] * h;
-        sb[p][q] += d[q];
+        for (int q = 0; q < 8; ++q) {
+          const float h = in ? (x[q] - cur.mu) * cur.rs : 0.0f, g = a.w ? d[q] * wv[q] : d[q];
+          s0 += g;
+          s1 += g * h;
+          sw[p][q] += d[q] * h;
+          sb[p][q] += d[q];
+        }
+      }
+      Row next;
+      if constexpr (kAhead) load(next, row + step);
+      s0 = wave_sum(s0);
+      s1 = wave_sum(s1);
+      if constexpr (kWaves > 1) {
+        if ((threadIdx.x & 63) == 0) {
+          part[which][group][0][t >> 6] = s0;
+          part[which][group][1][t >> 6] = s1;
+        }
+        __syncthreads();  // (the buffers alternate: the next turn's writes need no barrier of their own)
+        s0 = s1 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) {
+          s0 += part[which][group][0][i];
+          s1 += part[which][group][1][i];
+        }
+      }
+      const float c0 = s0 * a.inv_n, c1 = s1 * a.inv_n;
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const int n = (p * T + t) * 8;
+        float d[8], x[8], wv[8], r[8], o[8];
+        cur.d[p].get(d);
+        cur.x[p].get(x);
+        w[p].get(wv);
+        cur.r[p].get(r);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) o[q] = cur.rs * ((a.w ? d[q] * wv[q] : d[q]) - c0 - (x[q] - cur.mu) * cur.rs * c1) + r[q];
+        if (row < a.M && n < a.N) {
+          Eight<DT> e;
+          e.set(o);
+          e.store(a.dx + (size_t)row * a.ldo + (size_t)n * kB);
+        }
+      }
+      if constexpr (kAhead)
+        cur = next;
+      else
+        load(cur, row + step);
+    }
+    if (!a.dw && !a.db) continue;
+    // The row groups' sums one after the other, into the first's registers.
+#pragma unroll 1
+    for (int g = 1; g < kGroups; ++g) {
+      __syncthreads();
+      if (group == g) {
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            sums[(p * 8 + q) * T + t] = sw[p][q];
+            sums[((P + p) * 8 + q) * T + t] = sb[p][q];
+          }
+      }
+      __syncthreads();
+      if (group == 0) {
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            sw[p][q] += sums[(p * 8 + q) * T + t];
+            sb[p][q] += sums[((P + p) * 8 + q) * T + t];
+          }
       }
     }
-    Row next;
-    if constexpr (kAhead) load(next, row + step);
-    s0 = wave_sum(s0);
-    s1 = wave_sum(s1);
-    if constexpr (kWaves > 1) {
-      if ((threadIdx.x & 63) == 0) {
-        part[which][group][0][t >> 6] = s0;
-        part[which][group][1][t >> 6] = s1;
-      }
-      __syncthreads();  // (the buffers alternate: the next turn's writes need no barrier of their own)
-      s0 = s1 = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kWaves; ++i) {
-        s0 += part[which][group][0][i];
-        s1 += part[which][group][1][i];
-      }
-    }
-    const float c0 = s0 * a.inv_n, c1 = s1 * a.inv_n;
+    // Into the workspace, or (from the second time on) to what is there.
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int n = (p * T + t) * 8;
-      float d[8], x[8], wv[8], r[8], o[8];
-      cur.d[p].get(d);
-      cur.x[p].get(x);
-      w[p].get(wv);
-      cur.r[p].get(r);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) o[q] = cur.rs * ((a.w ? d[q] * wv[q] : d[q]) - c0 - (x[q] - cur.mu) * cur.rs * c1) + r[q];
-      if (row < a.M && n < a.N) {
-        Eight<DT> e;
-        e.set(o);
-        e.store(a.dx + (size_t)row * a.ldo + (size_t)n * kB);
+      if (group == 0 && n < a.N) {
+        float *c = a.colsums + (size_t)blockIdx.x * 2 * a.N + n;
+        auto put = [&](float *at, const float *v) {
+          v4f s = {v[0], v[1], v[2], v[3]};
+          if (again) s += *(const v4f *)at;
+          *(v4f *)at = s;
+        };
+        put(c, sw[p]);
+        put(c + 4, sw[p] + 4);
+        put(c + a.N, sb[p]);
+        put(c + a.N + 4, sb[p] + 4);
       }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) sw[p][q] = sb[p][q] = 0.0f;
     }
-    if constexpr (kAhead)
-      cur = next;
-    else
-      load(cur, row + step);
-  }
-  if (!a.dw && !a.db) return;
-  // The row groups' sums one after the other, into the first's registers.
-#pragma unroll 1
-  for (int g = 1; g < kGroups; ++g) {
-    __syncthreads();
-    if (group == g) {
-#pragma unroll
-      for (int p = 0; p < P; ++p)
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          sums[(p * 8 + q) * T + t] = sw[p][q];
-          sums[((P + p) * 8 + q) * T + t] = sb[p][q];
-        }
-    }
-    __syncthreads();
-    if (group == 0) {
-#pragma unroll
-      for (int p = 0; p < P; ++p)
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          sw[p][q] += sums[(p * 8 + q) * T + t];
-          sb[p][q] += sums[((P + p) * 8 + q) * T + t];
-        }
-    }
-  }
-  if (group > 0) return;
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-    const int n = (p * T + t) * 8;
-    if (n >= a.N) continue;
-    float *c = a.colsums + (size_t)blockIdx.x * 2 * a.N + n;
-    *(v4f *)c = v4f{sw[p][0], sw[p][1], sw[p][2], sw[p][3]};
-    *(v4f *)(c + 4) = v4f{sw[p][4], sw[p][5], sw[p][6], sw[p][7]};
-    c += a.N;
-    *(v4f *)c = v4f{sb[p][0], sb[p][1], sb[p][2], sb[p][3]};
-    *(v4f *)(c + 4) = v4f{sb[p][4], sb[p][5], sb[p][6], sb[p][7]};
   }
 }
 
@@ -555,8 +569,13 @@ __global__ __launch_bounds__(1024) void norm_sum_kernel(const NormGradArgs a) {
     const int64_t n = n0 + lane;
     float v = 0.0f;
     if (n < a.N) {
+      for (int b = wave; b < a.blocks;) {  // (32 of them at a time, as above)
+        const int end = min(b + 512, a.blocks);
+        float part = 0.0f;
 #pragma unroll 4
-      for (int b = wave; b < a.blocks; b += 16) v += a.colsums[((size_t)b * 2 + p) * a.N + n];
+        for (; b < end; b += 16) part += a.colsums[((size_t)b * 2 + p) * a.N + n];
+        v += part;
+      }
     }
     sums[wave][lane] = v;
     __syncthreads();

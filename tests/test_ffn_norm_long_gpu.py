@@ -69,3 +69,24 @@ def test_gradients_of_long_rows(N, dtype):
     for name, g in zip(("dx", "dweight", "dbias"), got):
         v, tol = want[name]
         ref.assert_near(first_of_equal(g), v.view(1, 8), tol.view(1, 8), name)
+
+
+# The sums over M equal rows of 8 values: 512 workgroups of 8 rows a turn.  A
+# thread's chain is at most 512 turns, then one addition per 512 turns; 8 row
+# groups, 32 workgroups and 16 waves follow.
+@pytest.mark.parametrize("M", [(1 << 20) + 5, (1 << 27) + 3])
+def test_column_sums_of_many_rows(M):
+    say("many rows", M)
+    x, dy = eight(5, F32), eight(6, F32)
+    _, _, mu, r, _, _, _, _ = more.layer_norm(x[None], None, None, 1e-5, F32)
+    many = lambda t: t.cuda().repeat(M, 1)
+    d = many(dy)
+    mean, rstd = torch.full((M,), float(mu.float()), device="cuda"), torch.full((M,), float(r.float()), device="cuda")
+    _, dw, db = tg.layer_norm_backward(d, many(x), None, mean, rstd, dx=d)
+    # (Binary32 takes 3 roundings to dy h: the difference, h and the product.)
+    h = (x.double() - mu.float().double()) * r.float().double()
+    D = 512 + M / (512 * 8 * 512) + 8 + 32 + 16
+    for name, got, v, each in (("dweight", dw, dy.double() * h, 3), ("dbias", db, dy.double(), 0)):
+        want = M * v
+        tol = M * v.abs() * (D + each) * more.U + ref.rounding(want, F32) * 1.001
+        ref.assert_near(got, want, tol, name)
