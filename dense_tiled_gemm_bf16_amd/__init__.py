@@ -128,7 +128,7 @@ def _call(fn, device, stream, *args):
         check(fn(*args, _stream_ptr(stream, device)))
 
 
-def _want(t, name, dtype, shape):
+def _want(t, name, dtype, shape, packed=True):
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
@@ -138,7 +138,7 @@ def _want(t, name, dtype, shape):
         raise ValueError(f"{name} must be on a GPU")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
+    if packed and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous (row-major, packed)")
 
 
@@ -298,17 +298,22 @@ def gemm_mxfp4_nt(a, b, scale_a, scale_b, out=None, stream=None):
 
     a (M,K/2), b (N,K/2): packed E2M1 bytes (uint8; element 2i in the low
     nibble of byte i); scale_a (M,K/32), scale_b (N,K/32): e8m0 bytes.
+    Rows of a and b may lie apart (a stride that is a multiple of 16), as those
+    of quantize_mxfp4's columns do: gemm_mxfp4_epilogue's kernels take such
+    operands.
     """
     torch = _torch()
     M, KH = a.shape
     N = b.shape[0]
     K = 2 * KH
-    _want(a, "a", torch.uint8, (M, KH))
-    _want(b, "b", torch.uint8, (N, KH))
+    _want(a, "a", torch.uint8, (M, KH), packed=False)
+    _want(b, "b", torch.uint8, (N, KH), packed=False)
     _want(scale_a, "scale_a", torch.uint8, (M, K // 32))
     _want(scale_b, "scale_b", torch.uint8, (N, K // 32))
     c = _out(out, (M, N), torch.bfloat16, a)
     dev = _same_device(a=a, b=b, scale_a=scale_a, scale_b=scale_b, out=c)
+    if not (a.is_contiguous() and b.is_contiguous()):
+        return ffn.gemm_mxfp4_epilogue(a, b, scale_a, scale_b, out=c, stream=stream)
     _call(lib().gemm_mxfp4_nt, dev, stream, M, N, K, a.data_ptr(), b.data_ptr(), scale_a.data_ptr(),
           scale_b.data_ptr(), c.data_ptr())
     return c

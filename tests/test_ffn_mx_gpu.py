@@ -391,6 +391,28 @@ def test_the_plain_product_agrees():
         ref.assert_near(got, old.cpu().double(), 2 * tol)
 
 
+@pytest.mark.parametrize("M", [1, 33, 96, 129, 256, 257, 600])
+def test_the_plain_product_takes_quantised_columns(M):
+    """Whatever M is: the rows of quantised columns lie apart where 16 bytes a block of
+    32 are no whole cache lines.  Either operand, both, and an output given."""
+    x, y = rand(M, M, 96), rand(M + 1, M, 72)
+    _, _, xt, sx = tg.quantize_mxfp4(x.cuda(), columns=True)
+    yt, sy = tg.quantize_mxfp4(y.cuda(), rows=False, columns=True)
+    assert xt.is_contiguous() == (-(-M // 32) * 16 % 128 == 0)
+    a, b = more.values(*more.quantize(x.t())), more.values(*more.quantize(y.t()))
+    want, tol, _, _ = ref.epilogue(a, b.t(), None, "none", None, BF16)
+    out = torch.empty(96, 72, dtype=BF16, device="cuda")
+    for p, q in ((xt, yt), (xt.contiguous(), yt), (xt, yt.contiguous())):
+        ref.assert_near(tg.gemm_mxfp4_nt(p, q, sx, sy), want, tol)
+        got = tg.gemm_mxfp4_nt(p, q, sx, sy, out=out, stream=torch.cuda.current_stream())
+        assert got.data_ptr() == out.data_ptr()
+        ref.assert_near(out, want, tol)
+    with pytest.raises(ValueError, match="row-major"):
+        tg.gemm_mxfp4_nt(xt.t().contiguous().t(), yt, sx, sy)
+    with pytest.raises(ValueError, match="contiguous"):
+        tg.gemm_mxfp4_nt(xt, yt, sx, sy, out=torch.empty(72, 96, dtype=BF16, device="cuda").t())
+
+
 # --------------------------------------------------------------------------
 # By expert
 # --------------------------------------------------------------------------
