@@ -312,8 +312,10 @@ def _dtype(dtype):
 
 def dequantize_mxfp4(q, scales, dtype=None, out=None, stream=None):
     """The values of MXFP4 rows q (M,N/2), scales (M,N/32): (M,N) in dtype
-    (torch.bfloat16 when None; out's if one is given), which holds each exactly
-    unless it is float16."""
+    (torch.bfloat16 when None; out's if one is given), which holds each below
+    2^128 exactly unless it is float16.  Values past the type's largest are
+    infinite: elements 4 and 6 at scale byte 253, 2 to 6 at 254; a finite number
+    from 1.75 2^127 on is quantised to such a one."""
     return _call("dequantize_mxfp4", q, stream, q, scales, _dtype(dtype), out)
 
 

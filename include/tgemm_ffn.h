@@ -395,8 +395,10 @@ TGEMM_API int quantize_mxfp4(const tgemm_quantize_mxfp4_args *args, hipStream_t 
 
 /*
  * What MXFP4 rows stand for: out[m][n] = element * 2^(scale - 127), M x N of
- * type dtype (BF16 and F32 hold every value exactly, F16 rounds to nearest even);
- * NaN where the scale byte is 255.  N % 32 == 0.
+ * type dtype; NaN where the scale byte is 255.  BF16 and F32 hold every value
+ * below 2^128 exactly, F16 rounds to nearest even; what is past the type's
+ * largest value is infinite.  (Quantised, that can be a finite number: from
+ * 1.75 * 2^127 on an element rounds to 4 * 2^126.)  N % 32 == 0.
  */
 typedef struct {
   int64_t dtype, M, N;

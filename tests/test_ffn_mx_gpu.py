@@ -184,6 +184,22 @@ def test_dequantize(dtype):
     assert torch.equal(got[ok], want[ok]) and torch.equal(torch.signbit(got[ok]), torch.signbit(want[ok]))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_values_past_the_largest(dtype):
+    """Exactly what is below 2^128; from there on infinities, to which finite numbers
+    can be quantised."""
+    q = torch.tensor([[0x10, 0x32, 0x54, 0x76] * 4] * 3, dtype=torch.uint8, device="cuda")
+    s = torch.tensor([[252], [253], [254]], dtype=torch.uint8, device="cuda")
+    got = tg.dequantize_mxfp4(q, s, dtype=dtype).cpu().double()
+    want = more.values(q.cpu(), s.cpu())
+    assert torch.equal(torch.isinf(got), want >= 2.0 ** 128)
+    assert torch.isinf(got).sum(1).tolist() == [0, 8, 16] and torch.equal(got[want < 2.0 ** 128], want[want < 2.0 ** 128])
+    x = torch.zeros(2, 32, dtype=dtype, device="cuda")
+    x[0, 3], x[1, 3] = 1.75 * 2.0 ** 127, -1.7421875 * 2.0 ** 127      # (the bfloat16 before)
+    back = tg.dequantize_mxfp4(*tg.quantize_mxfp4(x), dtype=dtype)
+    assert back[0, 3] == math.inf and back[1, 3] == -1.5 * 2.0 ** 127
+
+
 # --------------------------------------------------------------------------
 # Products with an epilogue
 # --------------------------------------------------------------------------
