@@ -301,19 +301,24 @@ hipError_t launch_one(const MxGemm &g) {
   return hipLaunchKernel(fn, dim3((unsigned)wgs), dim3(64 * W), args, 0, g.stream);
 }
 
-// NB blocks of weight rows a wave and W waves; one row by N x K from memory, us
-// between launches of a graph:
-//   N      K     NB 1, W 4   W 8    NB 2, W 4   W 8
-//   4096   1024  2.86        2.95   3.33        3.45
-//   4096   2048  3.46        3.55   4.08        4.18
-//   4096   4096  4.72        4.63   6.13        5.83
-//   4096   8192  7.66        6.86   10.8        10.0
-//   8192   4096  6.48        6.54   7.26        6.72
-//   16384  4096  9.80        9.84   10.3        9.67
+// NB blocks of 16 weight rows a wave and W waves: eight waves where each of four would
+// take more than one unit of K, and two blocks for four waves and so many weight rows that one
+// a wave fills the chip more than once.  (K above 1024 with that many goes to 64 x 64
+// tiles.)  us between launches of a graph, weights from memory:
+//   one row: N   K     NB 1, W 4   W 8      rows   N      K     groups  NB 1, W 4   NB 2, W 4
+//   4096         1024  2.86        2.95     1      16384  1024  -       4.58        4.77
+//   4096         2048  3.46        3.55     1      65536  1024  -       9.40        9.95
+//   4096         4096  4.72        4.63     16     16384  1024  -       5.45        5.16
+//   4096         8192  7.66        6.86     16     65536  1024  -       12.9        10.9
+//   8192         4096  6.48        6.54     74     2048   256   64      10.4        9.07
+//                                           74     2048   1024  64      15.1        13.9
+//                                           600    4096   1024  64      42.3        37.1
 template <int DT, int W>
 hipError_t launch_waves(const MxGemm &g) {
   if (is_gated(g.act)) return launch_one<DT, W, 2, true>(g);
-  return g.N * (g.groups ? std::min(g.groups, g.M) : 1) <= 32 * g.cus ? launch_one<DT, W, 1, false>(g) : launch_one<DT, W, 2, false>(g);
+  if constexpr (W == 4)
+    if (g.N * (g.groups ? std::min(g.groups, g.M) : 1) > 32 * g.cus) return launch_one<DT, W, 2, false>(g);
+  return launch_one<DT, W, 1, false>(g);
 }
 
 template <int DT>

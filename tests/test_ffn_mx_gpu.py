@@ -543,6 +543,20 @@ def test_grouped_one_weight_for_all(size, tile):
         assert torch.equal(out[:n], want[2:3].expand(n, N)) and (out[n:] == 9).all()
 
 
+@pytest.mark.parametrize("size", [0, 16])
+@pytest.mark.parametrize("K", [96, 160, 1024])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_few_rows_of_many_weight_rows(K, dtype, size, tile):
+    """The kernel for few rows where a wave takes two blocks of weight rows (more than
+    32 a compute unit, by all groups that have rows), the last ones incomplete."""
+    tile(size, K)
+    run_epilogue(3, 8264, K, dtype, "silu", seed=K)
+    run_epilogue(16, 8232, K, dtype, bias=False, residual=False, preact=False, seed=K + 1)
+    sizes = [(7 * i) % 5 for i in range(40)]
+    run_grouped(sizes, 264, K, dtype, "gelu", True, seed=K + 2)
+    run_grouped(sizes, 248, K, dtype, "none", False, bias=False, preact=False, seed=K + 3)
+
+
 # --------------------------------------------------------------------------
 # Together
 # --------------------------------------------------------------------------
