@@ -238,3 +238,28 @@ def test_outputs_are_ordinary_tensors():
     finally:
         torch.use_deterministic_algorithms(before)
     assert torch.equal(again, y)
+
+
+def test_new_outputs_are_seen_by_dispatch_modes_and_profilers():
+    """As torch.empty's are: by the operators of both kinds, and the results are the same."""
+    from torch.profiler import ProfilerActivity, profile
+    from torch.utils._python_dispatch import TorchDispatchMode
+
+    class Seen(TorchDispatchMode):
+        def __init__(self):
+            super().__init__()
+            self.names = []
+
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            self.names.append(func.overloadpacket.__name__)
+            return func(*args, **(kwargs or {}))
+
+    x, w = rand(0, 9, 264).cuda(), rand(1, 264, 264).cuda()
+    for call in (lambda: tg.layer_norm(x), lambda: tg.gemm_epilogue(x, w, act="silu")):
+        want = call()
+        with Seen() as seen:
+            got = call()
+        assert seen.names == ["empty"] and torch.equal(got, want)
+        with profile(activities=[ProfilerActivity.CPU], acc_events=True) as p:
+            got = call()
+        assert any(e.name == "aten::empty" for e in p.events()) and torch.equal(got, want)
