@@ -79,6 +79,19 @@ def test_norm(M, N):
     assert ((dw.double() - want[0]).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("M,N", [(560001, 4096), (131101, 16640)])
+def test_column_sums(M, N):
+    """Of whole numbers, with mean 0 and rstd 1: exact sums, rounded once."""
+    print("[gpu] column sums", M, N, flush=True)
+    x, dy = (torch.empty(M, N, dtype=BF16, device="cuda").random_(-2, 3, generator=gen(i)) for i in range(2))
+    _, dw, db = tg.layer_norm_backward(dy, x, None, torch.zeros(M, device="cuda"), torch.ones(M, device="cuda"))
+    want = torch.zeros(2, N, dtype=torch.float64, device="cuda")
+    for lo in range(0, M, 1 << 14):
+        d, v = dy[lo:lo + (1 << 14)].float(), x[lo:lo + (1 << 14)].float()
+        want += torch.stack(((d * v).sum(0, dtype=torch.float64), d.sum(0, dtype=torch.float64)))
+    assert torch.equal(dw, want[0].to(BF16)) and torch.equal(db, want[1].to(BF16))
+
+
 def test_norm_of_the_longest_row():
     """+1 and -1 in turn: mean 0 and variance 1 without a rounding that matters to
     a bfloat16 (1 / sqrt(1 + 1e-5) is within 2^-9 of 1)."""

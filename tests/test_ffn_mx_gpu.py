@@ -396,6 +396,28 @@ def test_nothing_to_multiply():
     assert tg.gemm_mxfp4_epilogue(e(3, 32), e(0, 32), e(3, 2), e(0, 2)).shape == (3, 0)
 
 
+@pytest.mark.parametrize("size", [0, 16, 64, 128])
+@pytest.mark.parametrize("M", [1, 70, 300, 20000])
+def test_an_empty_k(M, size, tile):
+    """Each kernel's loop over no K at all, null operands: the epilogue of zeros."""
+    tile(size, 0)
+    N, E = 40, 3
+    e = lambda *s: torch.zeros(*s, dtype=torch.uint8, device="cuda")
+    bias, rs = rand(0, N).cuda(), rand(1, M, N).cuda()
+    z = torch.full((M, N), 7.0, dtype=BF16, device="cuda")
+    y = tg.gemm_mxfp4_epilogue(e(M, 0), e(N, 0), e(M, 0), e(N, 0), bias=bias, act="relu", residual=rs, preact=z)
+    assert torch.equal(z, bias.expand(M, N))
+    assert torch.equal(y, (bias.float().relu() + rs.float()).to(BF16))
+    assert (tg.gemm_mxfp4_epilogue(e(M, 0), e(N, 0), e(M, 0), e(N, 0)) == 0).all()
+    off = torch.tensor([0, M // 2, M // 2, M], dtype=torch.int32, device="cuda")
+    src = torch.arange(M, dtype=torch.int32, device="cuda").flip(0)
+    for rows in (None, src):
+        z.fill_(7.0)
+        b3 = rand(2, E, N).cuda()
+        tg.gemm_mxfp4_grouped(e(M, 0), e(E, N, 0), e(M, 0), e(E, N, 0), off, rows=rows, bias=b3, out=z)
+        assert torch.equal(z[:M // 2], b3[0].expand(M // 2, N)) and torch.equal(z[M // 2:], b3[2].expand(M - M // 2, N))
+
+
 def test_the_plain_product_agrees():
     """gemm_mxfp4_nt on the same operands: sums in another order, each rounded once."""
     for M, N, K in [(300, 264, 1024), (256, 512, 96)]:

@@ -72,6 +72,40 @@ def test_rows(M, N):
     run(M, N, BF16 if M % 2 else F16, F32 if M % 3 else None, residual=M % 2 == 0, seed=M)
 
 
+@pytest.mark.parametrize("M,N", [(9001, 8), (4500, 504), (5001, 520), (2301, 1024), (2900, 1032), (1301, 2056), (700, 4104),
+                                 (530, 8192)])
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_rows_in_several_turns(M, N, dtype):
+    """More rows than all workgroups of the gradients take at once: 4096 of up to 512
+    values, 2048 of up to 1024, 1024 of up to 2048, 512 of up to 4096, 256 of up to 8192."""
+    run(M, N, dtype, F32 if N % 3 == 0 else None, residual=N % 16 == 0, seed=M)
+
+
+@pytest.mark.parametrize("M,N", [((1 << 22) + 5003, 8), ((1 << 20) + 5003, 520), ((1 << 20) + 3, 1032), (600001, 2056), (270001, 8192),
+                                 (70001, 8200)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_column_sums_of_many_rows_are_exact(M, N, dtype):
+    """Whole numbers, whose sums binary32 holds in any order: no row is left out or
+    counted twice, where the workgroups' sums go to the workspace more than once (from
+    513 turns on) and where they do not.  And dx of rows of later turns."""
+    say("column sums", M, N, dtype)
+    g = torch.Generator(device="cuda").manual_seed(N)
+    x, dy = (torch.empty(M, N, dtype=dtype, device="cuda").random_(-2, 3, generator=g) for _ in range(2))
+    mean, rstd, w = torch.zeros(M, device="cuda"), torch.ones(M, device="cuda"), torch.ones(N, device="cuda")
+    dx, dw, db = tg.layer_norm_backward(dy, x, w, mean, rstd)
+    want = torch.zeros(2, N, dtype=torch.float64, device="cuda")
+    step = max((1 << 26) // N, 1)
+    for lo in range(0, M, step):
+        d, v = dy[lo:lo + step].float(), x[lo:lo + step].float()
+        want += torch.stack(((d * v).sum(0, dtype=torch.float64), d.sum(0, dtype=torch.float64)))
+    assert want.abs().max() < 2 ** 24
+    assert torch.equal(dw.double(), want[0]) and torch.equal(db.double(), want[1])
+    for lo in (M // 2, M - 40):
+        part = slice(lo, lo + 40)
+        few = tg.layer_norm_backward(dy[part].clone(), x[part].clone(), w, mean[:40], rstd[:40], want_dweight=False)[0]
+        assert torch.equal(dx[part], few)
+
+
 @pytest.mark.parametrize("weight,bias", [(False, False), (True, False), (False, True)])
 def test_without_weight_or_bias(weight, bias):
     run(37, 264, BF16, F32 if weight else None, weight=weight, bias=bias, residual=False)
