@@ -88,12 +88,13 @@ int pick(const MxGemm &g) {
 
 // Whether a product takes the kernel for few rows: up to 16 rows of one
 // weight, up to 10 a group on average, where 64 x 64 tiles are fewer than half
-// the CUs or K is short; with more of them those read the weights faster.  us, this
-// kernel and 64 x 64 tiles:
-//   one row: 4096 x 4096 5.2 and 7.4, 1024 x 8192 5.7 and 8.9, 4096 x 1024 5.3 and
-//   5.7, 8192 x 8192 11.3 and 11.0, 32768 x 4096 15.9 and 13.5; 16 rows of 8192 x
-//   4096 8.3 and 7.7; 64 gated experts of 2048 x 2048, 6 hit 6.7 and 6.5, 55 hit
-//   by 4 rows each 32.5 and 31.1; 55 of 2048 x 1024 16.8 and 18.4.
+// the CUs or K is short; with more of them those read the weights faster, or (at the
+// border, 8192 x 8192) soon will.  us between launches of a graph, weights from
+// memory, this kernel and 64 x 64 tiles:
+//   one row: 4096 x 4096 4.9 and 7.5, 1024 x 8192 6.0 and 10.4, 4096 x 1024 2.9 and
+//   4.0, 8192 x 8192 10.6 and 12.3, 32768 x 4096 18.1 and 16.3; 16 rows of 8192 x
+//   4096 8.6 and 8.2; 64 gated experts of 2048 x 2048 by 6 rows 6.4 and 6.2, by
+//   220 32.7 and 32.8; 64 of 2048 x 1024 by 220 19.5 and 24.2.
 bool few_rows(const MxGemm &g) {
   if (g.M > (g.groups ? 10 * g.groups : 16)) return false;
   return g.K <= 1024 || tiles_of(g, 64) < 0.5 * g.cus;

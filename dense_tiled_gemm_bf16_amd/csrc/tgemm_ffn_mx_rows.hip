@@ -2,9 +2,9 @@
 // for gfx950: single tokens and small batches against 4-bit weights (N x K).
 //
 // What bounds such a product is reading the weight once, 17 bytes per 32
-// elements (16384 x 4096 9.7 us, 3.7 TB/s), and below some megabytes the latency
-// of a launch and one load (4096 x 1024 2.9).  A workgroup takes 16 NB rows of the weight (columns of C) and up
-// to 16 rows of A, and its W waves divide K: wave w takes units of 512 K
+// elements (220 rows of 64 experts of 2048 x 1024 19.5 us, 3.5 TB/s), and below some
+// megabytes the latency of a launch and one load (4096 x 1024 2.9).  A workgroup
+// takes 16 NB rows of the weight (columns of C) and up to 16 rows of A, and its W waves divide K: wave w takes units of 512 K
 // elements (256 bytes of each row) w, w + W, ...  Rows and scales go from
 // memory straight into the registers of the scaled v_mfma 16x16x128: in
 // product s of a unit lane l holds row l % 16 and block 4 s + l / 16 of 32
@@ -302,17 +302,23 @@ hipError_t launch_one(const MxGemm &g) {
 }
 
 // NB blocks of 16 weight rows a wave and W waves: eight waves where each of four would
-// take more than one unit of K, and two blocks for four waves and so many weight rows that one
-// a wave fills the chip more than once.  (K above 1024 with that many goes to 64 x 64
-// tiles.)  us between launches of a graph, weights from memory:
-//   one row: N   K     NB 1, W 4   W 8      rows   N      K     groups  NB 1, W 4   NB 2, W 4
-//   4096         1024  2.86        2.95     1      16384  1024  -       4.58        4.77
-//   4096         2048  3.46        3.55     1      65536  1024  -       9.40        9.95
-//   4096         4096  4.72        4.63     16     16384  1024  -       5.45        5.16
-//   4096         8192  7.66        6.86     16     65536  1024  -       12.9        10.9
-//   8192         4096  6.48        6.54     74     2048   256   64      10.4        9.07
-//                                           74     2048   1024  64      15.1        13.9
-//                                           600    4096   1024  64      42.3        37.1
+// take more than one unit of K, and two blocks for four waves and so many weight rows
+// that one a wave fills the chip more than once.  (K above 1024 with that many goes to
+// 64 x 64 tiles.)  us between launches of a graph, weights from memory; one row, NB 1:
+//   N      K     W 4    W 8
+//   4096   1024  2.86   2.95
+//   4096   2048  3.46   3.55
+//   4096   4096  4.72   4.63
+//   4096   8192  7.66   6.86
+// and W 4:
+//   rows  groups  N      K     NB 1   NB 2
+//   1     -       16384  1024  4.58   4.77
+//   1     -       65536  1024  9.40   9.95
+//   16    -       16384  1024  5.45   5.16
+//   16    -       65536  1024  12.9   10.9
+//   74    64      2048   256   10.4   9.07
+//   74    64      2048   1024  15.1   13.9
+//   600   64      4096   1024  42.3   37.1
 template <int DT, int W>
 hipError_t launch_waves(const MxGemm &g) {
   if (is_gated(g.act)) return launch_one<DT, W, 2, true>(g);

@@ -78,7 +78,7 @@ __device__ __forceinline__ float wave_sum(float v) {
 // addition rounded away).  One running sum over a row of 2^31 values, 2^21 additions
 // a thread, lost 0.8% of the mean: once it is large every addition rounds the same
 // way.  (Gradients of 8 x 65536 bf16: one running sum 18.2 us, this way 18.7, every
-// piece compensated 19.9; 2048 x 20000 forward 42.0, 42.5 and 42.5.)
+// piece compensated 19.9; 2048 x 20000 forward 42.5 and, this way, 43.3.)
 constexpr int kLongTurns = 16;
 __device__ __forceinline__ float sum8(const float (&v)[8]) {
   return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
@@ -105,8 +105,9 @@ struct NormArgs {
 // One row a workgroup of T threads (or a wave, T = 64, which needs no barrier),
 // P pieces of 8 values a thread in registers; P = 0: any length, three reads of
 // the row, the last two from the caches.  Reading x and writing y once bound it:
-// 8192 x 4096 bf16 29 us from memory (134 MB, 4.6 TB/s), 4093 x 5000 fp16 19;
-// 8 x 4096 2.7, the latency of a load and two sums across the row.
+// 8192 x 4096 bf16 29 us from memory (134 MB, 4.6 TB/s), 4093 x 5000 fp16 19,
+// 8192 x 4096 binary32 48 (268 MB, 5.6 TB/s, one call after another); 8 x 4096 2.7
+// between launches of a graph, the latency of a load and two sums across the row.
 // T x P, us for 2^25 bf16 values:
 //   N = 512     64 x 1   23.5   256 x 1  50.8
 //   N = 1024    64 x 2   22.3   256 x 1  32.5
@@ -273,10 +274,13 @@ hipError_t launch_norm_types(const Norm &g) {
 // another each time).  A thread's sums go there every kSumTurns turns, so that no
 // running sum gets long: in one over 32768 turns (134 million rows of 8 values)
 // dweight lost 3e-4 of its sum of magnitudes.  The next rows are loaded before the
-// sums of the present ones are waited for.  Four arrays of one read or write bound it: 8192 x 4096
-// bf16 with the residual 52 us (268 MB, 5.1 TB/s), its column sums 4.8.
+// sums of the present ones are waited for.  Four arrays of one read or write bound
+// it: 8192 x 4096 bf16 with the residual 45 us behind the forward pass (268 MB, 6.0
+// TB/s: part of x is still in the caches), its column sums 4.7; binary32 without a
+// residual 80 us with them (403 MB, 5.0 TB/s), though its loads do not run ahead.
 // T x P, us for 2^25 bf16 values without a residual, the sums with them, for one
-// and two workgroups a CU:
+// and two workgroups a CU, before the sums went to the workspace in runs (the
+// chosen ones since then, in turn: 39.6, 37.8, 39.0, 38.6, 41.2):
 //   N = 512    64 x 1   44.2 40.2   256 x 1  148  94.7
 //   N = 1024   64 x 2   40.7 45.7   256 x 1  84.2 58.4
 //   N = 2048   256 x 1  50.8 42.4   512 x 1  83.9 56.7   256 x 2  57.9 61.3
@@ -287,7 +291,7 @@ hipError_t launch_norm_types(const Norm &g) {
 // mean(g) and mean(g h) in the workspace; norm_columns_kernel takes kRowsWg
 // rows and 256 columns (as the epilogue's gradient), writes dx and adds up its
 // columns.  (8192 x 4096 bf16 with the residual this way 23 + 57 us, in one pass
-// 53, 5.1 TB/s; but 2048 x 12288 48 and 69, whose one pass would spill.)
+// 45; but 2048 x 12288 48 and 69, whose one pass would spill.)
 // ---------------------------------------------------------------------------
 constexpr int kGradWgs = 256;
 constexpr int kRowsWg = 64;

@@ -130,6 +130,9 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(const QuantArgs a) {
 // share a cache line meet in its L2.  Both ways, 3999 x 4992 binary32 24 us (101 MB,
 // 4.2 TB/s; tiles half as wide 37, twice as wide the same), 4001 x 4096 bf16 12 (50 MB);
 // a 64-byte piece of a column is what is written at once, half a cache line.
+// The stores into the tile do meet on banks: in binary32 a lane's 16 bytes lie 32
+// from the next one's, so that each store uses half of the banks (of the LDS's busy
+// cycles 50%; 33% with 16-bit values).  What that costs has not been measured.
 template <int DT, bool ROWS>
 __global__ __launch_bounds__(256) void quant_columns_kernel(const QuantArgs a) {
   constexpr int kB = DT == 2 ? 4 : 2, kPer = Raw<DT>::kPer, kTM = 128, kTN = 64 * kPer;

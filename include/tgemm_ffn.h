@@ -311,8 +311,10 @@ TGEMM_API int expert_combine_backward(const tgemm_expert_combine_backward_args *
  *            pointer and stride)
  *   weight, bias   N values of type wdtype (dtype or F32), or NULL: ones, zeros
  *   mean, rstd     M binary32 each, for the backward pass, or NULL
- * Sums are binary32, the variance's over differences from the mean.  Binary32
- * tensors are 16-byte aligned too, with strides that are multiples of 8.
+ * Sums are binary32, the variance's over differences from the mean, and lose no
+ * digits as N grows; they overflow where the formula's own sums leave binary32 (values
+ * past 2^127 / N or so, differences past 2^63 / sqrt(N)).  Binary32 tensors are
+ * 16-byte aligned too, with strides that are multiples of 8.
  * N >= 8; eps finite and not negative (0: a row of equal values gives NaN or
  * infinity, as the formula does).
  */
